@@ -319,6 +319,42 @@ LCE_API int lce_set_gemm_form(int form);
  * device is usable. */
 LCE_API int lce_gemm_pair_slots(void);
 
+/* ---- layer norm ---------------------------------------------------------
+ *
+ * The norm whose output is the head's X.  For each row of x [rows, H]:
+ *   mean = sum_h x / H,  rstd = 1 / sqrt(sum_h (x - mean)^2 / H + eps),
+ *   xh = (x - mean) rstd,  y = xh weight + bias,
+ * and from grad_y, with g = grad_y weight:
+ *   grad_x = rstd (g - mean_h(g) - xh mean_h(g xh)),
+ *   grad_weight = sum_rows grad_y xh,  grad_bias = sum_rows grad_y.
+ * Sums are FP32 and in an order fixed by the sizes, so equal calls give
+ * equal bits.
+ *  - dtype (LCE_BF16, LCE_F16, LCE_F32) is the type of x, y, grad_y and
+ *    grad_x; wtype, the type of weight, bias and their gradients, is dtype
+ *    or LCE_F32 (another pair is LCE_ERR_UNSUPPORTED).
+ *  - Rows are contiguous, ldx/ldy/ldg/ldgx elements apart (>= H).  Pointers
+ *    need only the alignment of their element type; rows that start on
+ *    16-byte boundaries with H a multiple of 16 bytes are read in vectors.
+ *  - 1 <= H <= LCE_NORM_MAX_H, 0 <= rows < 2^31 (no rows: nothing is read,
+ *    grad_weight and grad_bias become zero).
+ *  - weight and bias may each be NULL (1 and 0).  mean and rstd [rows] float
+ *    are written by the forward (both or neither) and read by the backward.
+ *  - grad_x, grad_weight and grad_bias may each be NULL; ws (256-byte
+ *    aligned, lce_layer_norm_workspace_size() bytes) is needed for the
+ *    latter two.
+ *  - Outputs must not overlap inputs. */
+enum { LCE_BF16 = 0, LCE_F16 = 1, LCE_F32 = 2 };
+#define LCE_NORM_MAX_H (1 << 20)
+LCE_API lce_status_t lce_layer_norm_forward(int64_t rows, int64_t H, int dtype, int wtype, const void* x,
+                                    int64_t ldx, const void* weight, const void* bias, float eps, void* y,
+                                    int64_t ldy, float* mean, float* rstd, lce_stream_t stream);
+LCE_API lce_status_t lce_layer_norm_workspace_size(int64_t rows, int64_t H, size_t* bytes);
+LCE_API lce_status_t lce_layer_norm_backward(int64_t rows, int64_t H, int dtype, int wtype, const void* grad_y,
+                                     int64_t ldg, const void* x, int64_t ldx, const void* weight,
+                                     const float* mean, const float* rstd, void* grad_x, int64_t ldgx,
+                                     void* grad_weight, void* grad_bias, void* ws, size_t ws_bytes,
+                                     lce_stream_t stream);
+
 /* Per-kernel device time, for benchmarks.  Between lce_profile_begin() and
  * lce_profile_end(), every kernel the library enqueues is bracketed by two
  * CUDA events recorded on the call's own stream (events are created on

@@ -28,6 +28,7 @@ __all__ = [
     "lce_static_ws_check_status",
     "lce_scale_grads",
     "workspace", "forward", "backward", "fused",
+    "BF16", "F16", "F32", "lce_layer_norm_forward", "lce_layer_norm_workspace_size", "lce_layer_norm_backward",
 ]
 
 IGNORE_INDEX = -100
@@ -73,6 +74,11 @@ _SIGS = {
     "lce_scale_grads": [_I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P],
     "lce_set_gemm_form": [ctypes.c_int],
     "lce_gemm_pair_slots": [],
+    "lce_layer_norm_forward": [_I64, _I64, ctypes.c_int, ctypes.c_int, _P, _I64, _P, _P, ctypes.c_float, _P, _I64,
+                               _P, _P, _P],
+    "lce_layer_norm_workspace_size": [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "lce_layer_norm_backward": [_I64, _I64, ctypes.c_int, ctypes.c_int, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64,
+                                _P, _P, _P, ctypes.c_size_t, _P],
     "lce_profile_begin": [],
     "lce_profile_end": [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64)],
 }
@@ -267,6 +273,28 @@ def lce_set_gemm_form(form) -> int:
 def lce_gemm_pair_slots() -> int:
     """CTA pairs of the pair form resident at once on the current device (0: not available)."""
     return int(lib().lce_gemm_pair_slots())
+
+
+BF16, F16, F32 = 0, 1, 2  # LCE_BF16, LCE_F16, LCE_F32
+
+
+def lce_layer_norm_forward(rows, H, dtype, wtype, x, ldx, weight, bias, eps, y, ldy, mean, rstd, stream) -> None:
+    _check(lib().lce_layer_norm_forward(rows, H, dtype, wtype, _ptr(x), ldx, _ptr(weight), _ptr(bias), eps, _ptr(y),
+                                        ldy, _ptr(mean), _ptr(rstd), _stream(stream)), "lce_layer_norm_forward")
+
+
+def lce_layer_norm_workspace_size(rows: int, H: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().lce_layer_norm_workspace_size(rows, H, ctypes.byref(out)), "lce_layer_norm_workspace_size")
+    return out.value
+
+
+def lce_layer_norm_backward(rows, H, dtype, wtype, grad_y, ldg, x, ldx, weight, mean, rstd, grad_x, ldgx,
+                            grad_weight, grad_bias, ws, ws_bytes, stream) -> None:
+    _check(lib().lce_layer_norm_backward(rows, H, dtype, wtype, _ptr(grad_y), ldg, _ptr(x), ldx, _ptr(weight),
+                                         _ptr(mean), _ptr(rstd), _ptr(grad_x), ldgx, _ptr(grad_weight),
+                                         _ptr(grad_bias), _ptr(ws), ws_bytes, _stream(stream)),
+           "lce_layer_norm_backward")
 
 
 def lce_profile_begin() -> None:

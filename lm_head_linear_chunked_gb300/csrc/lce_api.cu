@@ -616,6 +616,9 @@ lce_status_t run(const Problem& pb, const Outputs& o, bool do_fwd, bool do_bwd, 
 
 }  // namespace
 
+long profile_start(cudaStream_t s) { return prof_start(s, PK_OTHER); }
+void profile_stop(cudaStream_t s, long slot) { prof_stop(s, slot); }
+
 cudaError_t launch_gemm(int mode, const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_c,
                         const GemmArgs& args, int grid, cudaStream_t stream, bool pair) {
     if (grid <= 0) return cudaErrorInvalidConfiguration;

@@ -311,6 +311,19 @@ cudaError_t launch_gemm_gradx_wide(const CUtensorMap& map_a, const CUtensorMap& 
 // the form cannot launch).
 int gemm_pair_slots();
 
+// Event brackets of lce_profile_begin/end around a launch (lce_api.cu); the
+// kernels outside the loss's GEMMs count as kind 4 ("all other").
+long profile_start(cudaStream_t s);
+void profile_stop(cudaStream_t s, long slot);
+#define LCE_PROFILED(...)                                     \
+    do {                                                      \
+        const long slot_ = ::lce::profile_start(s);           \
+        __VA_ARGS__;                                          \
+        const cudaError_t e_ = cudaGetLastError();            \
+        ::lce::profile_stop(s, slot_);                        \
+        if (e_ != cudaSuccess) return LCE_ERR_CUDA;           \
+    } while (0)
+
 // Small kernels (lce_aux.cu).
 cudaError_t launch_prepass(const int64_t* y, int64_t N, int64_t V, int64_t ignore_index,
                            WsHeader* hdr, int* label_counts, cudaStream_t s);
