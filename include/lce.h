@@ -83,8 +83,9 @@ typedef enum {
     LCE_ERR_LABEL_RANGE = 4,   /* device: a label outside [0,V) and != ignore_index */
     LCE_ERR_TIMEOUT = 5,       /* device: a pipeline wait exceeded its time limit */
     LCE_ERR_CUDA = 6,          /* a CUDA runtime call or launch failed */
-    LCE_ERR_BOUNDS = 7         /* device, bounds-checking build only: an index or TMA coordinate fell
+    LCE_ERR_BOUNDS = 7,        /* device, bounds-checking build only: an index or TMA coordinate fell
                                   outside its buffer (the access was skipped) */
+    LCE_ERR_INDEX_RANGE = 8    /* device: an expert index outside [-1,E), or a parent outside [0,beams) */
 } lce_status_t;
 
 /* Which entry point a workspace is sized for.  LCE_WS_FUSED is the size for
@@ -203,8 +204,8 @@ LCE_API lce_status_t lce_scale_grads(int64_t N, int64_t H, int64_t V, const floa
 
 /* Synchronises `stream`, then returns the device status of the last call
  * that used workspace `ws` (LCE_OK, LCE_ERR_LABEL_RANGE, LCE_ERR_TIMEOUT,
- * or LCE_ERR_BOUNDS from the bounds-checking build), or LCE_ERR_CUDA if the
- * stream reported an error.  A call that found an error on the device also
+ * LCE_ERR_INDEX_RANGE, or LCE_ERR_BOUNDS from the bounds-checking build), or
+ * LCE_ERR_CUDA if the stream reported an error.  A call that found an error on the device also
  * writes NaN to its loss.
  *
  * Bounds-checking build.  The same sources compiled with LCE_DEBUG give
@@ -354,6 +355,53 @@ LCE_API lce_status_t lce_layer_norm_backward(int64_t rows, int64_t H, int dtype,
                                      const float* mean, const float* rstd, void* grad_x, int64_t ldgx,
                                      void* grad_weight, void* grad_bias, void* ws, size_t ws_bytes,
                                      lce_stream_t stream);
+
+/* ---- balance loss of a mixture of experts --------------------------------
+ *
+ * The auxiliary loss that a mixture-of-experts model adds to the head's
+ * cross-entropy, with the per-expert counts and the router's gradient.
+ * logits [groups, T, E] are the router's (a group is a layer or a sequence),
+ * experts [groups, T, k] the slots' expert indices.  Per group, over the n
+ * tokens that the mask keeps:
+ *   p = softmax over E,  counts[e] = slots that name e,
+ *   f_e = counts[e] E / (k n),  P_e = sum_t p_te / n,
+ *   group loss = sum_e f_e P_e          (1 for an even load; 0 when n = 0),
+ * loss = the mean over all groups, or with LCE_REDUCTION_SUM their sum.
+ * With s = grad_scale * *d_grad_output (NULL: 1), / groups for the mean,
+ *   grad_logits[t,e] = s p_te (f_e - sum_j f_j p_tj) / n, 0 for masked tokens
+ * (f takes no gradient).
+ *  - Logits have strides (elements) for groups and tokens, experts are
+ *    contiguous; grad_logits is contiguous, of the logits' type.
+ *  - experts: int32 or int64 (index_bytes 4 or 8).  -1 is an unused slot;
+ *    another index outside [0, E) gives loss = NaN and LCE_ERR_INDEX_RANGE
+ *    from lce_check_status(ws).
+ *  - mask: one byte per token (0 = left out), [T] with mask_group_stride 0
+ *    or [groups, T] with its stride; NULL keeps all.  What masked tokens
+ *    hold, NaN included, has no influence.
+ *  - 1 <= groups <= 65535, T < 2^31, E <= LCE_BALANCE_MAX_E, 1 <= k <= E.
+ *  - counts [groups, E] and n_valid [groups] are written by the forward and
+ *    the fused call, and read by the backward.  group_loss may be NULL.
+ * lce_balance_fused gives loss and gradient in one pass over the logits. */
+#define LCE_BALANCE_MAX_E 1024
+LCE_API lce_status_t lce_balance_workspace_size(int64_t groups, int64_t T, int64_t E, int64_t k, size_t* bytes);
+LCE_API lce_status_t lce_balance_forward(int64_t groups, int64_t T, int64_t E, int64_t k, int dtype,
+                                 const void* logits, int64_t group_stride, int64_t token_stride,
+                                 const void* experts, int index_bytes, const uint8_t* mask,
+                                 int64_t mask_group_stride, float* loss, float* group_loss, int64_t* counts,
+                                 int64_t* n_valid, void* ws, size_t ws_bytes, lce_stream_t stream,
+                                 uint32_t flags);
+LCE_API lce_status_t lce_balance_backward(int64_t groups, int64_t T, int64_t E, int64_t k, int dtype,
+                                  const void* logits, int64_t group_stride, int64_t token_stride,
+                                  const int64_t* counts, const int64_t* n_valid, const uint8_t* mask,
+                                  int64_t mask_group_stride, float grad_scale, const float* d_grad_output,
+                                  void* grad_logits, lce_stream_t stream, uint32_t flags);
+LCE_API lce_status_t lce_balance_fused(int64_t groups, int64_t T, int64_t E, int64_t k, int dtype,
+                               const void* logits, int64_t group_stride, int64_t token_stride,
+                               const void* experts, int index_bytes, const uint8_t* mask,
+                               int64_t mask_group_stride, float grad_scale, const float* d_grad_output,
+                               float* loss, float* group_loss, int64_t* counts, int64_t* n_valid,
+                               void* grad_logits, void* ws, size_t ws_bytes, lce_stream_t stream,
+                               uint32_t flags);
 
 /* Per-kernel device time, for benchmarks.  Between lce_profile_begin() and
  * lce_profile_end(), every kernel the library enqueues is bracketed by two

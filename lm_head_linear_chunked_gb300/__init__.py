@@ -29,12 +29,14 @@ __all__ = [
     "lce_scale_grads",
     "workspace", "forward", "backward", "fused",
     "BF16", "F16", "F32", "lce_layer_norm_forward", "lce_layer_norm_workspace_size", "lce_layer_norm_backward",
+    "lce_balance_workspace_size", "lce_balance_forward", "lce_balance_backward", "lce_balance_fused",
 ]
 
 IGNORE_INDEX = -100
 WS_FORWARD, WS_BACKWARD, WS_FUSED, WS_FUSED_MIN = 0, 1, 2, 3
 STATUS = {0: "LCE_OK", 1: "LCE_ERR_INVALID_ARG", 2: "LCE_ERR_UNSUPPORTED", 3: "LCE_ERR_WORKSPACE",
-          4: "LCE_ERR_LABEL_RANGE", 5: "LCE_ERR_TIMEOUT", 6: "LCE_ERR_CUDA", 7: "LCE_ERR_BOUNDS"}
+          4: "LCE_ERR_LABEL_RANGE", 5: "LCE_ERR_TIMEOUT", 6: "LCE_ERR_CUDA", 7: "LCE_ERR_BOUNDS",
+          8: "LCE_ERR_INDEX_RANGE"}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # LCE_LIBRARY=debug in the environment loads the bounds-checking build
@@ -79,6 +81,13 @@ _SIGS = {
     "lce_layer_norm_workspace_size": [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
     "lce_layer_norm_backward": [_I64, _I64, ctypes.c_int, ctypes.c_int, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64,
                                 _P, _P, _P, ctypes.c_size_t, _P],
+    "lce_balance_workspace_size": [_I64, _I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "lce_balance_forward": [_I64, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _I64, _P, ctypes.c_int, _P, _I64,
+                            _P, _P, _P, _P, _P, ctypes.c_size_t, _P, ctypes.c_uint32],
+    "lce_balance_backward": [_I64, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _I64, _P, _P, _P, _I64,
+                             ctypes.c_float, _P, _P, _P, ctypes.c_uint32],
+    "lce_balance_fused": [_I64, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _I64, _P, ctypes.c_int, _P, _I64,
+                          ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, ctypes.c_uint32],
     "lce_profile_begin": [],
     "lce_profile_end": [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64)],
 }
@@ -295,6 +304,38 @@ def lce_layer_norm_backward(rows, H, dtype, wtype, grad_y, ldg, x, ldx, weight, 
                                          _ptr(mean), _ptr(rstd), _ptr(grad_x), ldgx, _ptr(grad_weight),
                                          _ptr(grad_bias), _ptr(ws), ws_bytes, _stream(stream)),
            "lce_layer_norm_backward")
+
+
+def lce_balance_workspace_size(groups: int, T: int, E: int, k: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().lce_balance_workspace_size(groups, T, E, k, ctypes.byref(out)), "lce_balance_workspace_size")
+    return out.value
+
+
+def lce_balance_forward(groups, T, E, k, dtype, logits, group_stride, token_stride, experts, index_bytes, mask,
+                        mask_group_stride, loss, group_loss, counts, n_valid, ws, ws_bytes, stream, flags) -> None:
+    _check(lib().lce_balance_forward(groups, T, E, k, dtype, _ptr(logits), group_stride, token_stride, _ptr(experts),
+                                     index_bytes, _ptr(mask), mask_group_stride, _ptr(loss), _ptr(group_loss),
+                                     _ptr(counts), _ptr(n_valid), _ptr(ws), ws_bytes, _stream(stream), int(flags)),
+           "lce_balance_forward")
+
+
+def lce_balance_backward(groups, T, E, k, dtype, logits, group_stride, token_stride, counts, n_valid, mask,
+                         mask_group_stride, grad_scale, d_grad_output, grad_logits, stream, flags) -> None:
+    _check(lib().lce_balance_backward(groups, T, E, k, dtype, _ptr(logits), group_stride, token_stride, _ptr(counts),
+                                      _ptr(n_valid), _ptr(mask), mask_group_stride, grad_scale, _ptr(d_grad_output),
+                                      _ptr(grad_logits), _stream(stream), int(flags)),
+           "lce_balance_backward")
+
+
+def lce_balance_fused(groups, T, E, k, dtype, logits, group_stride, token_stride, experts, index_bytes, mask,
+                      mask_group_stride, grad_scale, d_grad_output, loss, group_loss, counts, n_valid, grad_logits,
+                      ws, ws_bytes, stream, flags) -> None:
+    _check(lib().lce_balance_fused(groups, T, E, k, dtype, _ptr(logits), group_stride, token_stride, _ptr(experts),
+                                   index_bytes, _ptr(mask), mask_group_stride, grad_scale, _ptr(d_grad_output),
+                                   _ptr(loss), _ptr(group_loss), _ptr(counts), _ptr(n_valid), _ptr(grad_logits),
+                                   _ptr(ws), ws_bytes, _stream(stream), int(flags)),
+           "lce_balance_fused")
 
 
 def lce_profile_begin() -> None:

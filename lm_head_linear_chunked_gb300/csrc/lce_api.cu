@@ -758,6 +758,7 @@ lce_status_t lce_check_status(const void* ws, lce_stream_t stream) {
     if (st & STATUS_TIMEOUT) return LCE_ERR_TIMEOUT;
     if (st & STATUS_LABEL) return LCE_ERR_LABEL_RANGE;
     if (st & STATUS_BOUNDS) return LCE_ERR_BOUNDS;
+    if (st & STATUS_INDEX) return LCE_ERR_INDEX_RANGE;
     return LCE_OK;
 }
 
@@ -771,6 +772,7 @@ const char* lce_status_string(lce_status_t status) {
         case LCE_ERR_TIMEOUT: return "device wait timed out";
         case LCE_ERR_CUDA: return "CUDA error";
         case LCE_ERR_BOUNDS: return "index outside its buffer (bounds-checking build)";
+        case LCE_ERR_INDEX_RANGE: return "expert or beam index out of range";
         default: return "unknown status";
     }
 }

@@ -151,6 +151,7 @@ __host__ __device__ inline TailPlan gradx_tail_plan(int n_act, int slots, int k_
 constexpr unsigned STATUS_LABEL = 1u << LCE_ERR_LABEL_RANGE;
 constexpr unsigned STATUS_TIMEOUT = 1u << LCE_ERR_TIMEOUT;
 constexpr unsigned STATUS_BOUNDS = 1u << LCE_ERR_BOUNDS;
+constexpr unsigned STATUS_INDEX = 1u << LCE_ERR_INDEX_RANGE;
 
 // Bounds-checking build (LCE_DEBUG): LCE_IN(cond, status) is `cond`, and a
 // false condition also raises STATUS_BOUNDS in the call's status word; the
