@@ -403,6 +403,56 @@ LCE_API lce_status_t lce_balance_fused(int64_t groups, int64_t T, int64_t E, int
                                void* grad_logits, void* ws, size_t ws_bytes, lce_stream_t stream,
                                uint32_t flags);
 
+/* ---- beam search ---------------------------------------------------------
+ *
+ * lce_beam_select: one step of beam search over the head's logits
+ * [items, beams, V] (rows `ld` elements apart).  With lse the natural
+ * logarithm of a row's sum of exponentials, candidate (beam, token) has the
+ * score scores[beam] + logits[beam, token] - lse[beam]; a beam that
+ * `finished` marks (one byte each; NULL: none) keeps its score, with
+ * pad_token, as its only candidate, and its logits are not read.  Per item
+ * the n_out best go to out_scores, out_tokens and out_parents (the beam)
+ * [items, n_out], ordered by score (down), beam (up), logit (down), token
+ * (up).  out_finished (may be NULL): the parent was finished, or the token
+ * is eos_token (negative: none).
+ *  - A NaN logit or score counts as -inf, a logit of +inf as the largest
+ *    finite float.  A row without a finite logit has candidates of score
+ *    -inf, ordered by token.  Where fewer than n_out candidates exist, as
+ *    with finished beams, the rest have score -inf and pad_token.
+ *  - Scores are compared in FP64; each lse is within a few 2^-24 of exact.
+ *    Equal rows have equal lse, whatever their alignment.
+ *  - 1 <= beams, n_out <= LCE_BEAM_MAX, n_out <= beams * V,
+ *    items * beams <= 65535, V < 2^31.
+ *
+ * lce_beam_reorder: copies each state's rows as the selection says: output
+ * row item * out_beams + j is input row item * beams + parents[item, j]
+ * (int64).  A state's row is n1 x n2 runs of run_bytes bytes, with strides in
+ * bytes between rows, outer and inner runs, so a cache whose used part is
+ * shorter than its room moves only that part.  All states move in one launch
+ * per 24.  src and dst must not overlap.  A parent outside [0, beams) gives a
+ * row of zero bytes and, with `status` (a device word that the caller has
+ * zeroed, such as a workspace's first; may be NULL), LCE_ERR_INDEX_RANGE from
+ * lce_check_status(status).  A row of a state has at most 2 GB. */
+#define LCE_BEAM_MAX 64
+typedef struct {
+    const void* src;
+    void* dst;
+    int64_t src_row, dst_row;
+    int64_t n1, src1, dst1;
+    int64_t n2, src2, dst2;
+    int64_t run_bytes;
+} lce_beam_state_t;
+LCE_API lce_status_t lce_beam_workspace_size(int64_t items, int64_t beams, int64_t V, int64_t n_out,
+                                     size_t* bytes);
+LCE_API lce_status_t lce_beam_select(int64_t items, int64_t beams, int64_t V, int64_t n_out, int dtype,
+                             const void* logits, int64_t ld, const float* scores, const uint8_t* finished,
+                             int64_t pad_token, int64_t eos_token, float* out_scores, int64_t* out_tokens,
+                             int64_t* out_parents, uint8_t* out_finished, void* ws, size_t ws_bytes,
+                             lce_stream_t stream);
+LCE_API lce_status_t lce_beam_reorder(int64_t items, int64_t beams, int64_t out_beams, const int64_t* parents,
+                              const lce_beam_state_t* states, int64_t n_states, void* status,
+                              lce_stream_t stream);
+
 /* Per-kernel device time, for benchmarks.  Between lce_profile_begin() and
  * lce_profile_end(), every kernel the library enqueues is bracketed by two
  * CUDA events recorded on the call's own stream (events are created on

@@ -30,6 +30,7 @@ __all__ = [
     "workspace", "forward", "backward", "fused",
     "BF16", "F16", "F32", "lce_layer_norm_forward", "lce_layer_norm_workspace_size", "lce_layer_norm_backward",
     "lce_balance_workspace_size", "lce_balance_forward", "lce_balance_backward", "lce_balance_fused",
+    "BeamState", "lce_beam_workspace_size", "lce_beam_select", "lce_beam_reorder",
 ]
 
 IGNORE_INDEX = -100
@@ -50,6 +51,15 @@ _lock = threading.Lock()
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _STATUS = ctypes.c_int
+
+
+
+class BeamState(ctypes.Structure):
+    """lce_beam_state_t: one state that lce_beam_reorder moves."""
+    _fields_ = [("src", _P), ("dst", _P), ("src_row", _I64), ("dst_row", _I64),
+                ("n1", _I64), ("src1", _I64), ("dst1", _I64),
+                ("n2", _I64), ("src2", _I64), ("dst2", _I64), ("run_bytes", _I64)]
+
 
 # name -> argument types, in the order of include/lce.h
 _SIGS = {
@@ -88,6 +98,10 @@ _SIGS = {
                              ctypes.c_float, _P, _P, _P, ctypes.c_uint32],
     "lce_balance_fused": [_I64, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _I64, _P, ctypes.c_int, _P, _I64,
                           ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, ctypes.c_uint32],
+    "lce_beam_workspace_size": [_I64, _I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "lce_beam_select": [_I64, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _P,
+                        ctypes.c_size_t, _P],
+    "lce_beam_reorder": [_I64, _I64, _I64, _P, ctypes.POINTER(BeamState), _I64, _P, _P],
     "lce_profile_begin": [],
     "lce_profile_end": [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64)],
 }
@@ -336,6 +350,25 @@ def lce_balance_fused(groups, T, E, k, dtype, logits, group_stride, token_stride
                                    _ptr(loss), _ptr(group_loss), _ptr(counts), _ptr(n_valid), _ptr(grad_logits),
                                    _ptr(ws), ws_bytes, _stream(stream), int(flags)),
            "lce_balance_fused")
+
+
+def lce_beam_workspace_size(items: int, beams: int, V: int, n_out: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().lce_beam_workspace_size(items, beams, V, n_out, ctypes.byref(out)), "lce_beam_workspace_size")
+    return out.value
+
+
+def lce_beam_select(items, beams, V, n_out, dtype, logits, ld, scores, finished, pad_token, eos_token, out_scores,
+                    out_tokens, out_parents, out_finished, ws, ws_bytes, stream) -> None:
+    _check(lib().lce_beam_select(items, beams, V, n_out, dtype, _ptr(logits), ld, _ptr(scores), _ptr(finished),
+                                 pad_token, eos_token, _ptr(out_scores), _ptr(out_tokens), _ptr(out_parents),
+                                 _ptr(out_finished), _ptr(ws), ws_bytes, _stream(stream)), "lce_beam_select")
+
+
+def lce_beam_reorder(items, beams, out_beams, parents, states, n_states, status, stream) -> None:
+    """states: a ctypes array of BeamState."""
+    _check(lib().lce_beam_reorder(items, beams, out_beams, _ptr(parents), states, n_states, _ptr(status),
+                                  _stream(stream)), "lce_beam_reorder")
 
 
 def lce_profile_begin() -> None:

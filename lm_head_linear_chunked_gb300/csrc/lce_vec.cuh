@@ -42,6 +42,8 @@ inline size_t dtype_bytes(int dtype) { return dtype == LCE_F32 ? 4 : 2; }
 inline bool dtype_known(int dtype) { return dtype == LCE_BF16 || dtype == LCE_F16 || dtype == LCE_F32; }
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+__device__ __forceinline__ bool aligned_dev(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // Calls f with a value of the element type that `dtype` names.
 template <typename F>
 auto with_dtype(int dtype, F f) {
