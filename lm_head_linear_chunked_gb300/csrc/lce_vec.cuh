@@ -26,13 +26,65 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// VEC elements read or written at once; the address is a multiple of the size.
+// VEC elements read or written at once; the address is a multiple of the size,
+// or of 16 bytes for larger ones.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Vec {
+struct alignas(sizeof(T) * VEC < 16 ? sizeof(T) * VEC : 16) Vec {
     T v[VEC];
     __device__ __forceinline__ float f(int i) const { return to_f32(v[i]); }
     __device__ __forceinline__ void set(int i, float x) { v[i] = from_f32<T>(x); }
 };
+
+// Two FP32 values in one 64-bit register: sm_100's packed add, multiply and
+// fused multiply-add round each half as the scalar instruction does, at one
+// issue slot for the two.
+struct F2 {
+    uint64_t u;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float lo(F2 a) { return __uint_as_float(static_cast<uint32_t>(a.u)); }
+__device__ __forceinline__ float hi(F2 a) { return __uint_as_float(static_cast<uint32_t>(a.u >> 32)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return r;
+}
+
+// Two neighbouring elements as a pair, and back (rounded to nearest even).
+__device__ __forceinline__ F2 pair_of(const float* v) { return f2(v[0], v[1]); }
+__device__ __forceinline__ F2 pair_of(const __nv_bfloat16* v) {
+    uint32_t u;
+    __builtin_memcpy(&u, v, 4);
+    return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ F2 pair_of(const __half* v) { return f2(__half2float(v[0]), __half2float(v[1])); }
+__device__ __forceinline__ void set_pair(float* v, F2 a) {
+    v[0] = lo(a);
+    v[1] = hi(a);
+}
+__device__ __forceinline__ void set_pair(__nv_bfloat16* v, F2 a) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo(a), hi(a));
+    __builtin_memcpy(v, &r, 4);
+}
+__device__ __forceinline__ void set_pair(__half* v, F2 a) {
+    const __half2 r = __floats2half2_rn(lo(a), hi(a));
+    __builtin_memcpy(v, &r, 4);
+}
 
 // Elements of T in a 16-byte vector.
 template <typename T>
@@ -50,6 +102,23 @@ auto with_dtype(int dtype, F f) {
     if (dtype == LCE_BF16) return f(__nv_bfloat16{});
     if (dtype == LCE_F16) return f(__half{});
     return f(float{});
+}
+
+// 4, 8 or 16 bytes from global to shared memory without a register, in groups
+// that the thread that started them waits for.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but the thread's last N groups have arrived.
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

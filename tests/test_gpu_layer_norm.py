@@ -82,6 +82,26 @@ def test_forward_and_backward(rows, H, dtype, wtype):
     check(x, w, b, dy, 1e-5, run(x, w, b, dy))
 
 
+@pytest.mark.parametrize("rows,H", [(1, 256), (2000, 256), (650, 1024), (3000, 2048), (5, 2562), (9, 4098), (7, 6001),
+                                    (3, 8191), (5, 8200), (2, 12288), (611, 16384), (3, 16390), (10, 4104)])
+@pytest.mark.parametrize("dtype,wtype", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+def test_every_form(rows, H, dtype, wtype):
+    """Widths on both sides of each choice of kernel, and more rows than blocks."""
+    t, v = DTYPES[dtype], DTYPES[wtype]
+    x = normal((rows, H), 41, t, std=0.5, mean=-0.7)
+    w, b = normal(H, 42, v, std=0.2, mean=1.0), normal(H, 43, v, std=0.2)
+    dy = normal((rows, H), 44, t, std=0.7)
+    check(x, w, b, dy, 1e-6, run(x, w, b, dy, 1e-6))
+
+
+def test_weight_and_bias_at_every_alignment():
+    """A float32 weight that starts between 32-byte, 16-byte and 4-byte boundaries."""
+    x, dy = normal((33, 512), 45, torch.bfloat16), normal((33, 512), 46, torch.bfloat16)
+    w, b = normal(530, 47), normal(530, 48)
+    for k in (0, 1, 2, 4, 8, 12):
+        check(x, w[k:k + 512], b[k:k + 512], dy, 1e-5, run(x, w[k:k + 512], b[k:k + 512], dy))
+
+
 @pytest.mark.parametrize("weight", [False, True])
 @pytest.mark.parametrize("bias", [False, True])
 def test_without_weight_or_bias(weight, bias):
