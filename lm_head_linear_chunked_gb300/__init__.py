@@ -118,6 +118,8 @@ class LCEError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded liblce.so (ImportError if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(library_path):

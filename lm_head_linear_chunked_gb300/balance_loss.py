@@ -20,76 +20,83 @@ from typing import Optional
 
 import torch
 
-from . import LCEError, _flags, lce_balance_backward, lce_balance_forward, lce_balance_fused, \
-    lce_balance_workspace_size, lce_check_status
-from ._tensors import check_cuda, check_shape, dtype_code
+from . import LCEError, _flags, lce_check_status
+from ._tensors import address, balance_workspace, call, check_cuda, check_shape, dtype_code, stream_handle
 
 
 def _shapes(logits: torch.Tensor, mask):
-    """(groups, tokens, experts, type code, logits with a last stride of 1, group stride, token stride, mask,
-    mask group stride)."""
+    """(groups, tokens, experts, type code, logits with rows in place, group stride, token stride, mask, mask
+    group stride)."""
     code = dtype_code(logits, "router_logits")
-    if logits.dim() not in (2, 3):
-        raise ValueError(f"router_logits must be [tokens, experts] or [groups, tokens, experts], got {list(logits.shape)}")
-    if 0 in logits.shape:
-        raise ValueError(f"router_logits is empty: {list(logits.shape)}")
-    if logits.stride(-1) != 1 or (logits.shape[-2] > 1 and logits.stride(-2) < logits.shape[-1]):
-        logits = logits.contiguous()
-    G = logits.shape[0] if logits.dim() == 3 else 1
-    T, E = logits.shape[-2:]
-    zg = logits.stride(0) if logits.dim() == 3 else 0
-    zt = logits.stride(-2) if T > 1 else E
+    dim, shape = logits.dim(), logits.shape
+    if dim not in (2, 3):
+        raise ValueError(f"router_logits must be [tokens, experts] or [groups, tokens, experts], got {list(shape)}")
+    T, E = shape[-2], shape[-1]
+    G = shape[0] if dim == 3 else 1
+    if not (G and T and E):
+        raise ValueError(f"router_logits is empty: {list(shape)}")
+    if logits.is_contiguous():
+        zg, zt = T * E, E
+    else:
+        if logits.stride(-1) != 1 or (T > 1 and logits.stride(-2) < E):
+            logits = logits.contiguous()
+        zg = logits.stride(0) if dim == 3 else 0
+        zt = logits.stride(-2) if T > 1 else E
     mg = 0
     if mask is not None:
         if mask.dtype != torch.bool:
             raise TypeError(f"mask must be bool, got {mask.dtype}")
-        if mask.dim() == 2 and logits.dim() == 3:
+        if mask.dim() == 2 and dim == 3:
             check_shape(mask, (G, T), "mask")
             mg = T
         else:
             check_shape(mask, (T,), "mask")
-        mask = mask.contiguous()
+        if not mask.is_contiguous():
+            mask = mask.contiguous()
     return G, T, E, code, logits, zg, zt, mask, mg
 
 
-def _experts(experts: torch.Tensor, logits: torch.Tensor):
-    if experts.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"experts must be int32 or int64, got {experts.dtype}")
-    if experts.dim() != logits.dim() or experts.shape[:-1] != logits.shape[:-1] or experts.shape[-1] == 0:
-        raise ValueError(f"experts must have shape {list(logits.shape[:-1])} + [slots], got {list(experts.shape)}")
-    return experts.contiguous(), experts.shape[-1], experts.element_size()
-
-
-def _grad_output(grad_output, dev):
+def _check_grad_output(grad_output, dev):
     if grad_output is not None:
         if grad_output.numel() != 1 or grad_output.dtype != torch.float32:
             raise TypeError("grad_output must be one float32 value")
-        check_cuda(dev, grad_output=grad_output)
-    return grad_output
+        check_cuda(dev, grad_output)
 
 
 def _loss_call(router_logits, experts, mask, reduction, stream, grad, grad_scale, grad_output):
     flags = _flags(reduction, False)
     G, T, E, code, z, zg, zt, mask, mg = _shapes(router_logits, mask)
-    experts, k, index_bytes = _experts(experts, router_logits)
-    dev = z.device
-    check_cuda(dev, experts=experts, mask=mask)
-    _grad_output(grad_output, dev)
-    nws = lce_balance_workspace_size(G, T, E, k)
-    floats = torch.empty(1 + G, dtype=torch.float32, device=dev)
-    ints = torch.empty(G * (E + 1), dtype=torch.int64, device=dev)
-    out = {"loss": floats[:1], "group_loss": floats[1:],
-           "counts": ints[:G * E].view(router_logits.shape[:-2] + (E,)), "n_valid": ints[G * E:],
-           "ws": torch.empty(nws, dtype=torch.uint8, device=dev)}
-    stream = stream or torch.cuda.current_stream(dev)
-    if grad:
-        out["grad_logits"] = torch.empty(z.shape, dtype=z.dtype, device=dev)
-        lce_balance_fused(G, T, E, k, code, z, zg, zt, experts, index_bytes, mask, mg, grad_scale, grad_output,
-                          out["loss"], out["group_loss"], out["counts"], out["n_valid"], out["grad_logits"],
-                          out["ws"], nws, stream, flags)
+    if experts.dtype == torch.int64:
+        index_bytes = 8
+    elif experts.dtype == torch.int32:
+        index_bytes = 4
     else:
-        lce_balance_forward(G, T, E, k, code, z, zg, zt, experts, index_bytes, mask, mg, out["loss"],
-                            out["group_loss"], out["counts"], out["n_valid"], out["ws"], nws, stream, flags)
+        raise TypeError(f"experts must be int32 or int64, got {experts.dtype}")
+    lead = router_logits.shape[:-1]
+    if experts.shape[:-1] != lead or experts.shape[-1] == 0:
+        raise ValueError(f"experts must have shape {list(lead)} + [slots], got {list(experts.shape)}")
+    if not experts.is_contiguous():
+        experts = experts.contiguous()
+    k = experts.shape[-1]
+    dev = z.device
+    check_cuda(dev, experts, mask)
+    _check_grad_output(grad_output, dev)
+    nws = balance_workspace(G, T, E, k)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    group_loss = torch.empty(G, dtype=torch.float32, device=dev)
+    counts = torch.empty(lead[:-1] + (E,), dtype=torch.int64, device=dev)
+    n_valid = torch.empty(G, dtype=torch.int64, device=dev)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+    out = {"loss": loss, "group_loss": group_loss, "counts": counts, "n_valid": n_valid, "ws": ws}
+    if grad:
+        out["grad_logits"] = dz = torch.empty_like(z, memory_format=torch.contiguous_format)
+        call("lce_balance_fused", G, T, E, k, code, z.data_ptr(), zg, zt, experts.data_ptr(), index_bytes,
+             address(mask), mg, grad_scale, address(grad_output), loss.data_ptr(), group_loss.data_ptr(),
+             counts.data_ptr(), n_valid.data_ptr(), dz.data_ptr(), ws.data_ptr(), nws, stream_handle(stream, dev), flags)
+    else:
+        call("lce_balance_forward", G, T, E, k, code, z.data_ptr(), zg, zt, experts.data_ptr(), index_bytes,
+             address(mask), mg, loss.data_ptr(), group_loss.data_ptr(), counts.data_ptr(), n_valid.data_ptr(),
+             ws.data_ptr(), nws, stream_handle(stream, dev), flags)
     return out
 
 
@@ -121,11 +128,11 @@ def balance_backward(router_logits: torch.Tensor, counts: torch.Tensor, n_valid:
     for what, t in (("counts", counts), ("n_valid", n_valid)):
         if t.dtype != torch.int64 or not t.is_contiguous():
             raise TypeError(f"{what} must be a contiguous int64 tensor")
-    check_cuda(dev, counts=counts, n_valid=n_valid, mask=mask)
-    _grad_output(grad_output, dev)
-    grad = torch.empty(z.shape, dtype=z.dtype, device=dev)
-    lce_balance_backward(G, T, E, slots, code, z, zg, zt, counts, n_valid, mask, mg, grad_scale, grad_output, grad,
-                         stream or torch.cuda.current_stream(dev), flags)
+    check_cuda(dev, counts, n_valid, mask)
+    _check_grad_output(grad_output, dev)
+    grad = torch.empty_like(z, memory_format=torch.contiguous_format)
+    call("lce_balance_backward", G, T, E, slots, code, z.data_ptr(), zg, zt, counts.data_ptr(), n_valid.data_ptr(),
+         address(mask), mg, grad_scale, address(grad_output), grad.data_ptr(), stream_handle(stream, dev), flags)
     return {"grad_logits": grad}
 
 

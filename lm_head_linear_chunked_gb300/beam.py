@@ -11,12 +11,14 @@ lce_beam_reorder call for all states; torch only allocates the outputs.
 """
 from __future__ import annotations
 
+import ctypes
+from functools import lru_cache
 from typing import Optional, Sequence
 
 import torch
 
-from . import BeamState, LCEError, lce_beam_reorder, lce_beam_select, lce_beam_workspace_size, lce_check_status
-from ._tensors import check_cuda, check_shape, dtype_code
+from . import BeamState, LCEError, lce_check_status
+from ._tensors import address, beam_workspace, call, check_cuda, check_shape, dtype_code, stream_handle
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = None,
@@ -48,48 +50,66 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
     if eos_token is not None and eos_token < 0:
         raise ValueError("eos_token must not be negative")
     dev = logits.device
-    check_cuda(dev, scores=scores, finished=finished)
+    check_cuda(dev, scores, finished)
     # rows evenly spaced (as a last position's logits are in [items * beams, length, V])?
-    ld = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
-    if logits.stride(2) != 1 or ld < V or (B > 1 and K > 1 and logits.stride(0) != K * ld):
-        logits, ld = logits.contiguous(), V
-    scores = scores.contiguous()
-    nws = lce_beam_workspace_size(B, K, V, n)
+    ld = V
+    if not logits.is_contiguous():
+        ld = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
+        if logits.stride(2) != 1 or ld < V or (B > 1 and K > 1 and logits.stride(0) != K * ld):
+            logits, ld = logits.contiguous(), V
+    if not scores.is_contiguous():
+        scores = scores.contiguous()
+    nws = beam_workspace(B, K, V, n)
     ws = torch.empty(nws, dtype=torch.uint8, device=dev)
-    tokens, parents = torch.empty((2, B, n), dtype=torch.int64, device=dev).unbind(0)
+    tokens = torch.empty((B, n), dtype=torch.int64, device=dev)
+    parents = torch.empty_like(tokens)
     out = {"scores": torch.empty((B, n), dtype=torch.float32, device=dev), "tokens": tokens, "parents": parents}
-    if eos_token is not None:
-        out["finished"] = torch.empty((B, n), dtype=torch.bool, device=dev)
-    lce_beam_select(B, K, V, n, code, logits, ld, scores, finished, pad_token, -1 if eos_token is None else eos_token,
-                    out["scores"], tokens, parents, out.get("finished"), ws, nws,
-                    stream or torch.cuda.current_stream(dev))
+    ended = None
+    if eos_token is None:
+        eos_token = -1
+    else:
+        out["finished"] = ended = torch.empty((B, n), dtype=torch.bool, device=dev)
+    call("lce_beam_select", B, K, V, n, code, logits.data_ptr(), ld, scores.data_ptr(), address(finished), pad_token,
+         eos_token, out["scores"].data_ptr(), tokens.data_ptr(), parents.data_ptr(), address(ended), ws.data_ptr(),
+         nws, stream_handle(stream, dev))
     return out
 
 
-def _runs(src: torch.Tensor, dst: torch.Tensor):
-    """A state's row as (n1, strides, n2, strides, run) in elements, the same for src and dst; None where that
-    takes more than two strided dimensions."""
+@lru_cache(maxsize=4096)
+def _layout(shape: tuple, src: tuple, dst: tuple, size: int):
+    """A state's row as the C ABI describes it, (n1, strides, n2, strides, run) in bytes, from the shape and the
+    strides of src and dst; None where that takes more than two strided dimensions."""
     dims = []  # outermost first: [size, src stride, dst stride]
-    for size, a, b in zip(src.shape[1:], src.stride()[1:], dst.stride()[1:]):
-        if size == 1:
+    for n, a, b in zip(shape[1:], src[1:], dst[1:]):
+        if n == 1:
             continue
-        if dims and dims[-1][1] == size * a and dims[-1][2] == size * b:
-            dims[-1] = [dims[-1][0] * size, a, b]
+        if dims and dims[-1][1] == n * a and dims[-1][2] == n * b:
+            dims[-1] = [dims[-1][0] * n, a, b]
         else:
-            dims.append([size, a, b])
+            dims.append([n, a, b])
     run = 1
     if dims and dims[-1][1] == 1 and dims[-1][2] == 1:
         run = dims.pop()[0]
     if len(dims) > 2:
         return None
-    dims = [[1, 0, 0]] * (2 - len(dims)) + dims
-    return dims[0], dims[1], run
+    (n1, s1, d1), (n2, s2, d2) = [[1, 0, 0]] * (2 - len(dims)) + dims
+    return n1, s1 * size, d1 * size, n2, s2 * size, d2 * size, run * size
 
 
-def _extent(t: torch.Tensor):
-    """The addresses from t's first to its last byte."""
-    first = t.data_ptr()
-    return first, first + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+@lru_cache(maxsize=4096)
+def _bytes_spanned(shape: tuple, strides: tuple, size: int) -> int:
+    """Bytes from a tensor's first to its last (0 for an empty one)."""
+    return 0 if 0 in shape else (sum((n - 1) * s for n, s in zip(shape, strides)) + 1) * size
+
+
+def _overlap(ranges) -> bool:
+    """Whether a range (first, end, whose) of one side meets one of the other's."""
+    ends = [0, 0]
+    for first, end, whose in sorted(ranges):
+        if first < ends[1 - whose]:
+            return True
+        ends[whose] = max(ends[whose], end)
+    return False
 
 
 def beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor,
@@ -115,43 +135,47 @@ def beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor,
         if fresh else list(out)
     if len(out) != len(states):
         raise ValueError(f"{len(states)} states, but {len(out)} outputs")
+    fields, ranges, keep = [], [], []  # keep: contiguous copies live until the launch is enqueued
     for i, (a, b) in enumerate(zip(states, out)):
-        if a.dim() == 0 or a.shape[0] != rows:
-            raise ValueError(f"states must have {rows} rows each, states[{i}] has shape {list(a.shape)}")
-        check_shape(b, (B * n,) + tuple(a.shape[1:]), f"out[{i}]")
+        shape = tuple(a.shape)
+        if not shape or shape[0] != rows:
+            raise ValueError(f"states must have {rows} rows each, states[{i}] has shape {list(shape)}")
+        if tuple(b.shape) != (B * n,) + shape[1:]:
+            check_shape(b, (B * n,) + shape[1:], f"out[{i}]")
         if a.dtype != b.dtype:
             raise TypeError(f"out[{i}] must be {a.dtype}, got {b.dtype}")
         if b.device != dev or a.device != dev:
             raise ValueError(f"states and outputs must be on {dev}")
-    check_cuda(dev, parents=parents)
-    extents = [] if fresh else [_extent(b) for b in out if b.numel()]
-    for lo, hi in (_extent(a) for a in states if a.numel()) if extents else ():
-        if any(lo < h and l < hi for l, h in extents):
-            raise ValueError("out overlaps the states")
-    array = (BeamState * len(states))()
-    keep = []  # contiguous copies live until the launch is enqueued
-    for s, a, b in zip(array, states, out):
-        if a.numel() == 0:
+        size, strides, to = a.element_size(), a.stride(), b.stride()
+        span = _bytes_spanned(shape, strides, size)
+        if not span:
             continue
-        r = _runs(a, b)
-        if r is None:
+        src, dst = a.data_ptr(), b.data_ptr()
+        if not fresh:
+            ranges.append((src, src + span, 0))
+            ranges.append((dst, dst + _bytes_spanned((B * n,) + shape[1:], to, size), 1))
+        row = _layout(shape, strides, to, size)
+        if row is None:
             a = a.contiguous()
             keep.append(a)
-            r = _runs(a, b)
-            if r is None:
-                raise ValueError(f"an output's strides {b.stride()} have more than two strided dimensions")
-        (n1, s1, d1), (n2, s2, d2), run = r
-        size = a.element_size()
-        s.src, s.dst = a.data_ptr(), b.data_ptr()
-        s.src_row, s.dst_row = a.stride(0) * size, b.stride(0) * size
-        s.n1, s.src1, s.dst1 = n1, s1 * size, d1 * size
-        s.n2, s.src2, s.dst2 = n2, s2 * size, d2 * size
-        s.run_bytes = run * size
-    stream = stream or torch.cuda.current_stream(dev)
+            src, strides = a.data_ptr(), a.stride()
+            row = _layout(shape, strides, to, size)
+            if row is None:
+                raise ValueError(f"an output's strides {to} have more than two strided dimensions")
+        fields += (src, dst, strides[0] * size, to[0] * size)
+        fields += row
+    check_cuda(dev, parents)
+    if _overlap(ranges):
+        raise ValueError("out overlaps the states")
+    if not parents.is_contiguous():
+        parents = parents.contiguous()
+    array = (ctypes.c_int64 * len(fields))(*fields)
+    handle = stream_handle(stream, dev)
     status = torch.zeros(64, dtype=torch.int32, device=dev) if check else None
-    lce_beam_reorder(B, rows // B, n, parents.contiguous(), array, len(states), status, stream)
+    call("lce_beam_reorder", B, rows // B, n, parents.data_ptr(), ctypes.cast(array, ctypes.POINTER(BeamState)),
+         len(fields) // 11, address(status), handle)
     if check:
-        st = lce_check_status(status, stream)
+        st = lce_check_status(status, handle)
         if st != 0:
             raise LCEError(st, "beam_reorder")
     return out

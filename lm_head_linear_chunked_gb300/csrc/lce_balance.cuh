@@ -1,0 +1,306 @@
+// The balance loss of a mixture of experts, its per-expert counts and its
+// gradient.  For each group g (a layer or a sequence) of T tokens, E experts
+// and k slots per token, over the n_g tokens that the mask keeps:
+//
+//   p = softmax_e(z),  c_e = slots that name e,  f_e = c_e E / (k n_g)
+//   L_g = sum_e f_e P_e,  P_e = sum_t p_te / n_g        (0 when n_g = 0)
+//   dL_g/dz_te = p_te (f_e - sum_j f_j p_tj) / n_g
+//
+// A row of p adds up to 1, so f - 1 in place of f gives the same gradient,
+// without the cancellation of two numbers near 1 when the load is even.
+//
+// The counts need only the expert indices, which are k/E of the logits'
+// size, so the loss and its gradient together take one pass over the logits.
+// Nothing is added by atomics on floats: each block writes its own sums, and
+// they are added in a fixed order.
+//
+// A row of logits is short (8 to 1024 values), so a token takes only as many
+// lanes of a warp as it has 16-byte vectors, and its sums as many shuffles.
+#pragma once
+
+#include "lce_internal.cuh"
+#include "lce_vec.cuh"
+
+namespace lce {
+
+constexpr int BAL_WARPS = 8;
+constexpr int BAL_THREADS = 32 * BAL_WARPS;
+// Blocks of the pass over all groups (a group's blocks share its tokens out):
+// four on each of 152 SMs; and the fewest tokens that are worth one.
+constexpr int64_t BAL_BLOCKS = 608;
+constexpr int64_t BAL_MIN_TOKENS = 32;
+// Blocks per group of the counting by itself (the fused call): every block of
+// the pass adds their counts up, so they are few.
+constexpr int64_t BAL_COUNT_PARTS = 32;
+
+struct BalArgs {
+    const void* z;
+    int64_t zg, zt;  // strides of a group and of a token, in elements
+    const void* idx;  // [G, T, k]
+    bool idx64;
+    const uint8_t* mask;  // nullable; [T] with group stride 0, or [G, T]
+    int64_t mask_g;
+    int64_t T, per_part, per_count;
+    int32_t G, E, k, parts, count_parts;
+    int32_t lanes;     // of a token in the pass: a power of two
+    // workspace: per (group, part) the counts, the kept tokens and the sums of p
+    WsHeader* hdr;
+    unsigned* done;    // blocks of the finish that are through
+    int32_t* part_c;   // [G, count_parts, E]
+    int32_t* part_n;   // [G, count_parts]: kept tokens, or -1 - kept if an index is out of range
+    float* part_p;     // [G, parts, E]
+    double* part_l;    // [G, tiles] of the finish
+    // finished counts (read by the backward)
+    const int64_t* counts;
+    const int64_t* n_valid;
+    float grad_scale;
+    const float* d_grad_output;
+    float inv_groups;  // 1 / G, or 1 for the sum over groups
+    void* dz;          // [G, T, E], contiguous
+    // outputs of the finish
+    float *loss, *group_loss;
+    int64_t *counts_out, *n_out;
+};
+
+enum BalMode { BAL_FORWARD, BAL_BACKWARD, BAL_FUSED };
+
+lce_status_t bal_pass_bf16(BalArgs a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_f16(BalArgs a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_f32(BalArgs a, BalMode mode, cudaStream_t s);
+
+namespace {
+
+__device__ __forceinline__ bool kept(const BalArgs& a, int g, int64_t t) {
+    return !a.mask || a.mask[g * a.mask_g + t] != 0;
+}
+
+// Counts of the tokens t0 .. t1 of a group, by the whole block: a histogram
+// per warp in shared memory (`hist`, [BAL_WARPS, E]), then one of the block.
+__device__ __forceinline__ void count_tokens(const BalArgs& a, int g, int part, int64_t t0, int64_t t1, int32_t* hist) {
+    __shared__ int32_t total, bad;
+    for (int e = threadIdx.x; e < BAL_WARPS * a.E; e += BAL_THREADS) hist[e] = 0;
+    if (threadIdx.x == 0) total = bad = 0;
+    __syncthreads();
+    int32_t* mine = hist + (threadIdx.x >> 5) * a.E;
+    int32_t n = 0;
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += BAL_THREADS) {
+        if (!kept(a, g, t)) continue;
+        ++n;
+        const int64_t at = (static_cast<int64_t>(g) * a.T + t) * a.k;
+#pragma unroll 4
+        for (int j = 0; j < a.k; ++j) {
+            const int64_t e = a.idx64 ? static_cast<const int64_t*>(a.idx)[at + j]
+                                      : static_cast<const int32_t*>(a.idx)[at + j];
+            if (e >= 0 && e < a.E)
+                atomicAdd(mine + e, 1);
+            else if (e != -1)
+                bad = 1;
+        }
+    }
+    if (n) atomicAdd(&total, n);
+    __syncthreads();
+    const int64_t slot = static_cast<int64_t>(g) * a.count_parts + part;
+    for (int e = threadIdx.x; e < a.E; e += BAL_THREADS) {
+        int32_t c = 0;
+#pragma unroll
+        for (int w = 0; w < BAL_WARPS; ++w) c += hist[w * a.E + e];
+        a.part_c[slot * a.E + e] = c;
+    }
+    if (threadIdx.x == 0) a.part_n[slot] = bad ? -1 - total : total;
+}
+
+// The finish starts from a zeroed counter and status.
+__device__ __forceinline__ void open_finish(const BalArgs& a) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+        a.hdr->status = 0;
+        *a.done = 0;
+    }
+}
+
+// One pass over a part's logits: column sums of p, the gradient, or both.
+// Vector i of lane l holds the experts (i lanes + l) VEC + 0 .. VEC - 1; the
+// next token's vectors are read while this one's are worked on.  A token that
+// the mask leaves out counts as a row of zeros with a factor of zero, so what
+// it holds is never used and the lanes of a warp stay together.
+template <typename T, int VEC, int ITEMS, int MODE>
+__global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
+    constexpr bool SUM = MODE != BAL_BACKWARD, GRAD = MODE != BAL_FORWARD;
+    constexpr int PAIRS = ITEMS * VEC / 2;
+    constexpr float LOG2E = 1.4426950408889634f;
+    using V = Vec<T, VEC>;
+    extern __shared__ float sm[];  // f [E]; histograms or the warps' sums [BAL_WARPS, E]
+    __shared__ float scale_s;
+    const int g = blockIdx.y, part = blockIdx.x;
+    const int lanes = a.lanes, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane & (lanes - 1), sub = lane / lanes, tpw = 32 / lanes;
+    const int n = a.E / VEC;
+    const int64_t t0 = part * a.per_part, t1 = t0 + a.per_part < a.T ? t0 + a.per_part : a.T;
+    if (MODE == BAL_FORWARD) {
+        open_finish(a);
+        count_tokens(a, g, part, t0, t1, reinterpret_cast<int32_t*>(sm));
+        __syncthreads();
+    }
+    F2 f[PAIRS], sum[PAIRS];
+    float scale = 0.f;
+    auto column = [&](int e) { return ((e / VEC) * lanes + l) * VEC + e % VEC; };
+    if (GRAD) {
+        // f - 1 from the group's counts: finished (the backward), or the sums of their parts
+        int64_t kept_n = 0;
+        if (MODE == BAL_BACKWARD) {
+            kept_n = a.n_valid[g];
+        } else {
+            for (int q = 0; q < a.count_parts; ++q) {
+                const int32_t m = a.part_n[static_cast<int64_t>(g) * a.count_parts + q];
+                kept_n += m < 0 ? -1 - m : m;
+            }
+        }
+        const double per = kept_n > 0 ? static_cast<double>(a.E) / (static_cast<double>(a.k) * kept_n) : 0.0;
+        for (int e = threadIdx.x; e < a.E; e += BAL_THREADS) {
+            int64_t c = 0;
+            if (MODE == BAL_BACKWARD) {
+                c = a.counts[static_cast<int64_t>(g) * a.E + e];
+            } else {
+#pragma unroll 4
+                for (int q = 0; q < a.count_parts; ++q)
+                    c += a.part_c[(static_cast<int64_t>(g) * a.count_parts + q) * a.E + e];
+            }
+            sm[e] = static_cast<float>(static_cast<double>(c) * per - 1.0);
+        }
+        if (threadIdx.x == 0) {
+            const float go = a.d_grad_output ? *a.d_grad_output : 1.f;
+            scale_s = kept_n > 0 ? static_cast<float>(static_cast<double>(a.grad_scale) * go * a.inv_groups / kept_n) : 0.f;
+        }
+        __syncthreads();
+        scale = scale_s;
+    }
+#pragma unroll
+    for (int p = 0; p < PAIRS; ++p) {
+        const int c0 = column(2 * p), c1 = column(2 * p + 1);
+        f[p] = GRAD ? f2(c0 < a.E ? sm[c0] : 0.f, c1 < a.E ? sm[c1] : 0.f) : f2(0.f);
+        sum[p] = f2(0.f);
+    }
+    if (GRAD && SUM) __syncthreads();
+    const T* zg = static_cast<const T*>(a.z) + g * a.zg;
+    T* dzg = GRAD ? static_cast<T*>(a.dz) + static_cast<int64_t>(g) * a.T * a.E : nullptr;
+    const int64_t step = BAL_WARPS * tpw;
+    int64_t t = t0 + warp * tpw + sub;
+    V next[ITEMS];
+    bool next_ok = false;
+    auto fetch = [&](int64_t at) {
+        next_ok = at < t1 && kept(a, g, at);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (at < t1 && i * lanes + l < n) next[i] = reinterpret_cast<const V*>(zg + at * a.zt)[i * lanes + l];
+    };
+    fetch(t);
+    // the warp's first subgroup has the lowest token: the warp goes on while that one has
+    for (; t - sub < t1; t += step) {
+        V z[ITEMS];
+        const bool ok = next_ok;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) z[i] = next[i];
+        fetch(t + step);
+        float v[2 * PAIRS], m = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 2 * PAIRS; ++e) {
+            const bool in = (e / VEC) * lanes + l < n;
+            v[e] = ok ? (in ? z[e / VEC].f(e % VEC) : -INFINITY) : 0.f;
+            m = fmaxf(m, v[e]);
+        }
+        for (int o = lanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        // the max's product rounds the same way for every expert of the row and cancels in p
+        const F2 m2 = f2(-m * LOG2E), l2 = f2(LOG2E);
+        F2 ex[PAIRS], s2 = f2(0.f), q2 = f2(0.f);
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) {
+            const F2 y = fma2(f2(v[2 * p], v[2 * p + 1]), l2, m2);
+            ex[p] = f2(exp2f(lo(y)), exp2f(hi(y)));
+            s2 = add2(s2, ex[p]);
+            if (GRAD) q2 = fma2(f[p], ex[p], q2);
+        }
+        float s = lo(s2) + hi(s2), q = GRAD ? lo(q2) + hi(q2) : 0.f;
+        for (int o = lanes >> 1; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            if (GRAD) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+        }
+        const float r = ok ? 1.f / s : 0.f;
+        const F2 r2 = f2(r), fp = f2(-q * r), sc = f2(scale);
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) {
+            const F2 pr = mul2(ex[p], r2);
+            if (SUM) sum[p] = add2(sum[p], pr);
+            if (GRAD) {
+                const F2 d = mul2(mul2(sc, pr), add2(f[p], fp));
+                z[2 * p / VEC].set(2 * p % VEC, lo(d));
+                z[(2 * p + 1) / VEC].set((2 * p + 1) % VEC, hi(d));
+            }
+        }
+        if (GRAD && t < t1)
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+                if (i * lanes + l < n) reinterpret_cast<V*>(dzg + t * a.E)[i * lanes + l] = z[i];
+    }
+    if (!SUM) return;
+    // the subgroups of a warp, then the warps, in a fixed order
+#pragma unroll
+    for (int p = 0; p < PAIRS; ++p)
+        for (int o = lanes; o < 32; o <<= 1)
+            sum[p] = add2(sum[p], f2(__shfl_xor_sync(0xFFFFFFFFu, lo(sum[p]), o), __shfl_xor_sync(0xFFFFFFFFu, hi(sum[p]), o)));
+    if (sub == 0)
+#pragma unroll
+        for (int e = 0; e < 2 * PAIRS; ++e) {
+            const int c = column(e);
+            if (c < a.E) sm[warp * a.E + c] = e & 1 ? hi(sum[e / 2]) : lo(sum[e / 2]);
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += BAL_THREADS) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < BAL_WARPS; ++w) v += sm[w * a.E + e];
+        a.part_p[(static_cast<int64_t>(g) * a.parts + part) * a.E + e] = v;
+    }
+}
+
+template <typename T, int VEC, int ITEMS>
+lce_status_t bal_pass_items(const BalArgs& a, BalMode mode, cudaStream_t s) {
+    const dim3 grid(a.parts, a.G);
+    const size_t f = static_cast<size_t>(a.E) * 4;
+    if (mode == BAL_FORWARD)
+        LCE_PROFILED(bal_pass_kernel<T, VEC, ITEMS, BAL_FORWARD><<<grid, BAL_THREADS, BAL_WARPS * f, s>>>(a));
+    else if (mode == BAL_BACKWARD)
+        LCE_PROFILED(bal_pass_kernel<T, VEC, ITEMS, BAL_BACKWARD><<<grid, BAL_THREADS, f, s>>>(a));
+    else
+        LCE_PROFILED(bal_pass_kernel<T, VEC, ITEMS, BAL_FUSED><<<grid, BAL_THREADS, BAL_WARPS * f, s>>>(a));
+    return LCE_OK;
+}
+
+// Rows that start on 16-byte boundaries are read in 16-byte vectors, else in
+// 8-byte ones where that fits (60 experts in 16 bits), else by the element.
+template <typename T>
+lce_status_t bal_pass(BalArgs a, BalMode mode, cudaStream_t s) {
+    auto fits = [&](int vec) {
+        const size_t b = vec * sizeof(T);
+        return a.E % vec == 0 && a.zt % vec == 0 && a.zg % vec == 0 && aligned_to(a.z, b) && aligned_to(a.dz, b);
+    };
+    constexpr int V16 = 16 / sizeof(T), V8 = 8 / sizeof(T);
+    const int vec = fits(V16) ? V16 : fits(V8) ? V8 : 1;
+    const int n = a.E / vec;
+    a.lanes = 1;
+    while (a.lanes < n && a.lanes < 32) a.lanes *= 2;
+    const int items = (n + a.lanes - 1) / a.lanes;
+    if (vec == V16)
+        return items <= 1   ? bal_pass_items<T, V16, 1>(a, mode, s)
+               : items <= 2 ? bal_pass_items<T, V16, 2>(a, mode, s)
+               : items <= 4 ? bal_pass_items<T, V16, 4>(a, mode, s)
+                            : bal_pass_items<T, V16, 8>(a, mode, s);
+    if (vec == V8)
+        return items <= 1   ? bal_pass_items<T, V8, 1>(a, mode, s)
+               : items <= 4 ? bal_pass_items<T, V8, 4>(a, mode, s)
+                            : bal_pass_items<T, V8, 16>(a, mode, s);
+    return items <= 2   ? bal_pass_items<T, 1, 2>(a, mode, s)
+           : items <= 8 ? bal_pass_items<T, 1, 8>(a, mode, s)
+                        : bal_pass_items<T, 1, 32>(a, mode, s);
+}
+
+}  // namespace
+}  // namespace lce

@@ -16,25 +16,23 @@ from typing import Optional
 
 import torch
 
-from . import F32, lce_layer_norm_backward, lce_layer_norm_forward, lce_layer_norm_workspace_size
-from ._tensors import check_cuda, check_shape, dtype_code, rows_of
+from . import F32
+from ._tensors import address, call, check_cuda, check_shape, dtype_code, norm_workspace, rows_of, stream_handle
 
 
-def _check_affine(x, code, weight, bias):
-    """The type of weight and bias (code of the C ABI)."""
-    wcode = F32
-    for what, t in (("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
-        check_shape(t, (x.shape[-1],), what)
-        if t.dtype != x.dtype and t.dtype != torch.float32:
-            raise TypeError(f"{what} must be {x.dtype} or float32, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-        wcode = dtype_code(t, what)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError(f"weight and bias must have one type, got {weight.dtype} and {bias.dtype}")
-    return wcode if (weight is not None or bias is not None) else code
+def _width(x: torch.Tensor) -> int:
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x needs a last dimension of at least one element")
+    return x.shape[-1]
+
+
+def _check_affine(x, H, t, what):
+    if t.shape != (H,):
+        check_shape(t, (H,), what)
+    if t.dtype != x.dtype and t.dtype != torch.float32:
+        raise TypeError(f"{what} must be {x.dtype} or float32, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
 
 
 def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -42,21 +40,27 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, b
     """{"y", "mean", "rstd"}: the output and, with `stats`, each row's float32
     mean and reciprocal standard deviation [number of rows], which the
     backward reads."""
-    code = dtype_code(x, "x")
-    if x.dim() == 0 or x.shape[-1] == 0:
-        raise ValueError("x needs a last dimension of at least one element")
-    wcode = _check_affine(x, code, weight, bias)
+    code = wcode = dtype_code(x, "x")
+    H = _width(x)
+    if weight is not None:
+        _check_affine(x, H, weight, "weight")
+        wcode = code if weight.dtype == x.dtype else F32
+    if bias is not None:
+        _check_affine(x, H, bias, "bias")
+        if weight is not None and weight.dtype != bias.dtype:
+            raise TypeError(f"weight and bias must have one type, got {weight.dtype} and {bias.dtype}")
+        wcode = code if bias.dtype == x.dtype else F32
     dev = x.device
-    check_cuda(dev, weight=weight, bias=bias)
-    H = x.shape[-1]
-    rows = x.numel() // H
+    check_cuda(dev, weight, bias)
     x, ldx = rows_of(x)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    rows = x.numel() // H
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
     mean = rstd = None
     if stats:
-        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
-    lce_layer_norm_forward(rows, H, code, wcode, x, ldx, weight, bias, eps, y, H, mean, rstd,
-                           stream or torch.cuda.current_stream(dev))
+        mean = torch.empty(rows, dtype=torch.float32, device=dev)
+        rstd = torch.empty_like(mean)
+    call("lce_layer_norm_forward", rows, H, code, wcode, x.data_ptr(), ldx, address(weight), address(bias), eps,
+         y.data_ptr(), H, address(mean), address(rstd), stream_handle(stream, dev))
     return {"y": y, "mean": mean, "rstd": rstd}
 
 
@@ -67,36 +71,42 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[
     forward's mean and rstd.  The sums over the rows are of weight's type
     (`grad_dtype`, or x's type, without a weight)."""
     code = dtype_code(x, "x")
-    check_shape(grad_y, tuple(x.shape), "grad_y")
+    H = _width(x)
+    if grad_y.shape != x.shape:
+        check_shape(grad_y, tuple(x.shape), "grad_y")
     if grad_y.dtype != x.dtype:
         raise TypeError(f"grad_y must be {x.dtype}, got {grad_y.dtype}")
-    if x.dim() == 0 or x.shape[-1] == 0:
-        raise ValueError("x needs a last dimension of at least one element")
-    H = x.shape[-1]
+    if weight is not None:
+        _check_affine(x, H, weight, "weight")
+        gdtype = weight.dtype
+    else:
+        gdtype = grad_dtype or x.dtype
+        if gdtype != x.dtype and gdtype != torch.float32:
+            raise TypeError(f"grad_dtype must be {x.dtype} or float32, got {gdtype}")
     rows = x.numel() // H
-    _check_affine(x, code, weight, None)
-    gdtype = weight.dtype if weight is not None else (grad_dtype or x.dtype)
-    if gdtype != x.dtype and gdtype != torch.float32:
-        raise TypeError(f"grad_dtype must be {x.dtype} or float32, got {gdtype}")
     for what, t in (("mean", mean), ("rstd", rstd)):
-        check_shape(t, (rows,), what)
+        if t.shape != (rows,):
+            check_shape(t, (rows,), what)
         if t.dtype != torch.float32 or not t.is_contiguous():
             raise TypeError(f"{what} must be a contiguous float32 tensor")
     dev = x.device
-    check_cuda(dev, grad_y=grad_y, weight=weight, mean=mean, rstd=rstd)
-    wcode = F32 if gdtype == torch.float32 else code
+    check_cuda(dev, grad_y, weight, mean, rstd)
     x, ldx = rows_of(x)
     grad_y, ldg = rows_of(grad_y)
-    grad_x = torch.empty(x.shape, dtype=x.dtype, device=dev) if want_grad_x else None
-    grad_weight = torch.empty(H, dtype=gdtype, device=dev) if want_grad_weight else None
-    grad_bias = torch.empty(H, dtype=gdtype, device=dev) if want_grad_bias else None
-    ws, nws = None, 0
+    grad_x = torch.empty_like(x, memory_format=torch.contiguous_format) if want_grad_x else None
+    grad_weight = grad_bias = ws = None
+    nws = 0
+    if want_grad_weight:
+        grad_weight = torch.empty(H, dtype=gdtype, device=dev)
+    if want_grad_bias:
+        grad_bias = torch.empty(H, dtype=gdtype, device=dev)
     if want_grad_weight or want_grad_bias:
-        nws = lce_layer_norm_workspace_size(rows, H)
+        nws = norm_workspace(rows, H)
         ws = torch.empty(nws, dtype=torch.uint8, device=dev)
     if want_grad_x or ws is not None:
-        lce_layer_norm_backward(rows, H, code, wcode, grad_y, ldg, x, ldx, weight, mean, rstd, grad_x, H,
-                                grad_weight, grad_bias, ws, nws, stream or torch.cuda.current_stream(dev))
+        call("lce_layer_norm_backward", rows, H, code, code if gdtype == x.dtype else F32, grad_y.data_ptr(), ldg,
+             x.data_ptr(), ldx, address(weight), mean.data_ptr(), rstd.data_ptr(), address(grad_x), H,
+             address(grad_weight), address(grad_bias), address(ws), nws, stream_handle(stream, dev))
     return {"grad_x": grad_x, "grad_weight": grad_weight, "grad_bias": grad_bias}
 
 
