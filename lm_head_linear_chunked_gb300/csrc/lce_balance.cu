@@ -15,18 +15,22 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_count_kernel(BalArgs a) {
 
 // Adds the parts up.  A block takes 32 experts of a group, a row of 32 threads
 // each 1/32 of the parts; the last block to end adds the blocks' shares of the
-// loss, in order.
+// loss, in order.  The sums are FP32 (at most 24 terms in sequence; this GPU's
+// FP64 adds run at 1/64 of their rate, and took 8 of 11 us here) and only the
+// last few scalars FP64.
 __global__ void __launch_bounds__(1024) bal_finish_kernel(BalArgs a) {
-    __shared__ double sp[32][33];
+    __shared__ float sp[32][33];
     __shared__ long long sc[32][33];
+    __shared__ int32_t sn[32];
     __shared__ int bad;
     __shared__ bool last;
     const int g = blockIdx.y, lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int e = blockIdx.x * 32 + lane;
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
-    double p = 0.0;
+    float p = 0.f;
     long long c = 0;
+    int32_t n = 0;
     if (e < a.E) {
 #pragma unroll 4
         for (int q = row; q < a.parts; q += 32) p += a.part_p[(static_cast<int64_t>(g) * a.parts + q) * a.E + e];
@@ -35,40 +39,31 @@ __global__ void __launch_bounds__(1024) bal_finish_kernel(BalArgs a) {
     }
     sp[row][lane] = p;
     sc[row][lane] = c;
-    long long n = 0;
     for (int q = threadIdx.x; q < a.count_parts; q += 1024) {
         const int32_t m = a.part_n[static_cast<int64_t>(g) * a.count_parts + q];
         n += m < 0 ? -1 - m : m;
         if (m < 0) bad = 1;
     }
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (lane == 0) sn[row] = n;
     __syncthreads();
-    p = sp[lane][row];
+    p = warp_sum(sp[lane][row]);  // expert `row` of the block
     c = sc[lane][row];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        p += __shfl_xor_sync(0xFFFFFFFFu, p, o);
-        c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
-        n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
     __syncthreads();
     if (lane == 0) {
         const int at = blockIdx.x * 32 + row;
         if (at < a.E) a.counts_out[static_cast<int64_t>(g) * a.E + at] = c;
-        sp[0][row] = at < a.E ? static_cast<double>(c) * p : 0.0;
-        sc[0][row] = n;
+        sp[0][row] = at < a.E ? static_cast<float>(c) * p : 0.f;
     }
     __syncthreads();
     if (row == 0) {
-        double v = sp[0][lane];
-        n = sc[0][lane];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-        }
+        const float v = warp_sum(sp[0][lane]);
+        n = __reduce_add_sync(0xFFFFFFFFu, sn[lane]);
         if (lane == 0) {
             a.part_l[static_cast<int64_t>(g) * gridDim.x + blockIdx.x] =
-                n > 0 ? v * a.E / (static_cast<double>(a.k) * n * n) : 0.0;
+                n > 0 ? static_cast<double>(v) * a.E / (static_cast<double>(a.k) * n * n) : 0.0;
             if (blockIdx.x == 0) a.n_out[g] = n;
             if (bad) atomicOr(&a.hdr->status, STATUS_INDEX);
             __threadfence();
@@ -76,10 +71,10 @@ __global__ void __launch_bounds__(1024) bal_finish_kernel(BalArgs a) {
         }
     }
     __syncthreads();
-    if (!last) return;
+    if (!last || row != 0) return;
     __threadfence();
     double total = 0.0;
-    for (int k = threadIdx.x; k < a.G; k += 1024) {
+    for (int k = lane; k < a.G; k += 32) {
         double v = 0.0;
         for (unsigned i = 0; i < gridDim.x; ++i) v += __ldcg(a.part_l + static_cast<int64_t>(k) * gridDim.x + i);
         if (a.group_loss) a.group_loss[k] = static_cast<float>(v);
@@ -87,15 +82,8 @@ __global__ void __launch_bounds__(1024) bal_finish_kernel(BalArgs a) {
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    if (lane == 0) sp[1][row] = total;
-    __syncthreads();
-    if (row == 0) {
-        total = sp[1][lane];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-        const bool wrong = (__ldcg(&a.hdr->status) & STATUS_INDEX) != 0;
-        if (lane == 0) *a.loss = wrong ? __int_as_float(0x7FC00000) : static_cast<float>(total * a.inv_groups);
-    }
+    const bool wrong = (__ldcg(&a.hdr->status) & STATUS_INDEX) != 0;
+    if (lane == 0) *a.loss = wrong ? __int_as_float(0x7FC00000) : static_cast<float>(total * a.inv_groups);
 }
 
 lce_status_t bal_pass_any(const BalArgs& a, int dtype, BalMode mode, cudaStream_t s) {

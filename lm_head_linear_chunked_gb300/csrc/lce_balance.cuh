@@ -42,7 +42,6 @@ struct BalArgs {
     int64_t mask_g;
     int64_t T, per_part, per_count;
     int32_t G, E, k, parts, count_parts;
-    int32_t lanes;     // of a token in the pass: a power of two
     // workspace: per (group, part) the counts, the kept tokens and the sums of p
     WsHeader* hdr;
     unsigned* done;    // blocks of the finish that are through
@@ -64,9 +63,9 @@ struct BalArgs {
 
 enum BalMode { BAL_FORWARD, BAL_BACKWARD, BAL_FUSED };
 
-lce_status_t bal_pass_bf16(BalArgs a, BalMode mode, cudaStream_t s);
-lce_status_t bal_pass_f16(BalArgs a, BalMode mode, cudaStream_t s);
-lce_status_t bal_pass_f32(BalArgs a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_bf16(const BalArgs& a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_f16(const BalArgs& a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_f32(const BalArgs& a, BalMode mode, cudaStream_t s);
 
 namespace {
 
@@ -83,18 +82,42 @@ __device__ __forceinline__ void count_tokens(const BalArgs& a, int g, int part, 
     __syncthreads();
     int32_t* mine = hist + (threadIdx.x >> 5) * a.E;
     int32_t n = 0;
+    auto count = [&](int64_t e) {
+        if (e >= 0 && e < a.E)
+            atomicAdd(mine + e, 1);
+        else if (e != -1)
+            bad = 1;
+    };
+    // 16 bytes of indices at a time where a token's begin on such a boundary
+    const int per = a.idx64 ? 2 : 4;
+    const bool vec = a.k % per == 0 && aligned_dev(a.idx);
     for (int64_t t = t0 + threadIdx.x; t < t1; t += BAL_THREADS) {
         if (!kept(a, g, t)) continue;
         ++n;
         const int64_t at = (static_cast<int64_t>(g) * a.T + t) * a.k;
+        if (vec && a.idx64) {
+            const longlong2* p = reinterpret_cast<const longlong2*>(static_cast<const int64_t*>(a.idx) + at);
 #pragma unroll 4
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t e = a.idx64 ? static_cast<const int64_t*>(a.idx)[at + j]
-                                      : static_cast<const int32_t*>(a.idx)[at + j];
-            if (e >= 0 && e < a.E)
-                atomicAdd(mine + e, 1);
-            else if (e != -1)
-                bad = 1;
+            for (int j = 0; j < a.k / 2; ++j) {
+                const longlong2 e = p[j];
+                count(e.x);
+                count(e.y);
+            }
+        } else if (vec) {
+            const int4* p = reinterpret_cast<const int4*>(static_cast<const int32_t*>(a.idx) + at);
+#pragma unroll 2
+            for (int j = 0; j < a.k / 4; ++j) {
+                const int4 e = p[j];
+                count(e.x);
+                count(e.y);
+                count(e.z);
+                count(e.w);
+            }
+        } else {
+#pragma unroll 4
+            for (int j = 0; j < a.k; ++j)
+                count(a.idx64 ? static_cast<const int64_t*>(a.idx)[at + j]
+                              : static_cast<const int32_t*>(a.idx)[at + j]);
         }
     }
     if (n) atomicAdd(&total, n);
@@ -122,7 +145,7 @@ __device__ __forceinline__ void open_finish(const BalArgs& a) {
 // next token's vectors are read while this one's are worked on.  A token that
 // the mask leaves out counts as a row of zeros with a factor of zero, so what
 // it holds is never used and the lanes of a warp stay together.
-template <typename T, int VEC, int ITEMS, int MODE>
+template <typename T, int VEC, int LANES, int ITEMS, int MODE>
 __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
     constexpr bool SUM = MODE != BAL_BACKWARD, GRAD = MODE != BAL_FORWARD;
     constexpr int PAIRS = ITEMS * VEC / 2;
@@ -131,9 +154,11 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
     extern __shared__ float sm[];  // f [E]; histograms or the warps' sums [BAL_WARPS, E]
     __shared__ float scale_s;
     const int g = blockIdx.y, part = blockIdx.x;
-    const int lanes = a.lanes, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int l = lane & (lanes - 1), sub = lane / lanes, tpw = 32 / lanes;
+    constexpr int tpw = 32 / LANES;  // tokens of a warp at a time
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane & (LANES - 1), sub = lane / LANES;
     const int n = a.E / VEC;
+    const bool whole = n == LANES * ITEMS;  // no lane has a vector outside the row
     const int64_t t0 = part * a.per_part, t1 = t0 + a.per_part < a.T ? t0 + a.per_part : a.T;
     if (MODE == BAL_FORWARD) {
         open_finish(a);
@@ -142,7 +167,7 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
     }
     F2 f[PAIRS], sum[PAIRS];
     float scale = 0.f;
-    auto column = [&](int e) { return ((e / VEC) * lanes + l) * VEC + e % VEC; };
+    auto column = [&](int e) { return ((e / VEC) * LANES + l) * VEC + e % VEC; };
     if (GRAD) {
         // f - 1 from the group's counts: finished (the backward), or the sums of their parts
         int64_t kept_n = 0;
@@ -189,62 +214,64 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
     auto fetch = [&](int64_t at) {
         next_ok = at < t1 && kept(a, g, at);
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i)
-            if (at < t1 && i * lanes + l < n) next[i] = reinterpret_cast<const V*>(zg + at * a.zt)[i * lanes + l];
+        for (int i = 0; i < ITEMS; ++i) {
+            next[i] = V{};
+            if (at < t1 && (whole || i * LANES + l < n)) next[i] = reinterpret_cast<const V*>(zg + at * a.zt)[i * LANES + l];
+        }
     };
     fetch(t);
     // the warp's first subgroup has the lowest token: the warp goes on while that one has
     for (; t - sub < t1; t += step) {
-        V z[ITEMS];
+        RowVectors<T, VEC, ITEMS> z;
         const bool ok = next_ok;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) z[i] = next[i];
+        for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? next[i] : V{};
         fetch(t + step);
-        float v[2 * PAIRS], m = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 2 * PAIRS; ++e) {
-            const bool in = (e / VEC) * lanes + l < n;
-            v[e] = ok ? (in ? z[e / VEC].f(e % VEC) : -INFINITY) : 0.f;
-            m = fmaxf(m, v[e]);
-        }
-        for (int o = lanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        // the max's product rounds the same way for every expert of the row and cancels in p
-        const F2 m2 = f2(-m * LOG2E), l2 = f2(LOG2E);
-        F2 ex[PAIRS], s2 = f2(0.f), q2 = f2(0.f);
+        F2 v[PAIRS];
+        float m = -INFINITY;
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
-            const F2 y = fma2(f2(v[2 * p], v[2 * p + 1]), l2, m2);
-            ex[p] = f2(exp2f(lo(y)), exp2f(hi(y)));
-            s2 = add2(s2, ex[p]);
-            if (GRAD) q2 = fma2(f[p], ex[p], q2);
+            v[p] = z.pair(p);
+            if (!whole)
+                v[p] = f2((2 * p / VEC) * LANES + l < n ? lo(v[p]) : -INFINITY,
+                          ((2 * p + 1) / VEC) * LANES + l < n ? hi(v[p]) : -INFINITY);
+            m = fmaxf(m, fmaxf(lo(v[p]), hi(v[p])));
+        }
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        // the max's product rounds the same way for every expert of the row and cancels in p
+        const F2 m2 = f2(-m * LOG2E), l2 = f2(LOG2E);
+        F2 s2 = f2(0.f), q2 = f2(0.f);
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) {
+            const F2 y = fma2(v[p], l2, m2);
+            v[p] = f2(fast_exp2(lo(y)), fast_exp2(hi(y)));
+            s2 = add2(s2, v[p]);
+            if (GRAD) q2 = fma2(f[p], v[p], q2);
         }
         float s = lo(s2) + hi(s2), q = GRAD ? lo(q2) + hi(q2) : 0.f;
-        for (int o = lanes >> 1; o > 0; o >>= 1) {
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) {
             s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             if (GRAD) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
         }
-        const float r = ok ? 1.f / s : 0.f;
-        const F2 r2 = f2(r), fp = f2(-q * r), sc = f2(scale);
+        const float r = ok ? __frcp_rn(s) : 0.f;
+        const F2 r2 = f2(r), fp = f2(-q * r), sr = f2(scale * r);
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
-            const F2 pr = mul2(ex[p], r2);
-            if (SUM) sum[p] = add2(sum[p], pr);
-            if (GRAD) {
-                const F2 d = mul2(mul2(sc, pr), add2(f[p], fp));
-                z[2 * p / VEC].set(2 * p % VEC, lo(d));
-                z[(2 * p + 1) / VEC].set((2 * p + 1) % VEC, hi(d));
-            }
+            if (SUM) sum[p] = fma2(v[p], r2, sum[p]);
+            if (GRAD) z.set(p, mul2(mul2(v[p], sr), add2(f[p], fp)));
         }
         if (GRAD && t < t1)
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i)
-                if (i * lanes + l < n) reinterpret_cast<V*>(dzg + t * a.E)[i * lanes + l] = z[i];
+                if (whole || i * LANES + l < n) reinterpret_cast<V*>(dzg + t * a.E)[i * LANES + l] = z.v[i];
     }
     if (!SUM) return;
     // the subgroups of a warp, then the warps, in a fixed order
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p)
-        for (int o = lanes; o < 32; o <<= 1)
+        for (int o = LANES; o < 32; o <<= 1)
             sum[p] = add2(sum[p], f2(__shfl_xor_sync(0xFFFFFFFFu, lo(sum[p]), o), __shfl_xor_sync(0xFFFFFFFFu, hi(sum[p]), o)));
     if (sub == 0)
 #pragma unroll
@@ -261,45 +288,49 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
     }
 }
 
-template <typename T, int VEC, int ITEMS>
-lce_status_t bal_pass_items(const BalArgs& a, BalMode mode, cudaStream_t s) {
+template <typename T, int VEC, int LANES, int ITEMS>
+lce_status_t bal_pass_form(const BalArgs& a, BalMode mode, cudaStream_t s) {
     const dim3 grid(a.parts, a.G);
     const size_t f = static_cast<size_t>(a.E) * 4;
     if (mode == BAL_FORWARD)
-        LCE_PROFILED(bal_pass_kernel<T, VEC, ITEMS, BAL_FORWARD><<<grid, BAL_THREADS, BAL_WARPS * f, s>>>(a));
+        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FORWARD><<<grid, BAL_THREADS, BAL_WARPS * f, s>>>(a));
     else if (mode == BAL_BACKWARD)
-        LCE_PROFILED(bal_pass_kernel<T, VEC, ITEMS, BAL_BACKWARD><<<grid, BAL_THREADS, f, s>>>(a));
+        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_BACKWARD><<<grid, BAL_THREADS, f, s>>>(a));
     else
-        LCE_PROFILED(bal_pass_kernel<T, VEC, ITEMS, BAL_FUSED><<<grid, BAL_THREADS, BAL_WARPS * f, s>>>(a));
+        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FUSED><<<grid, BAL_THREADS, BAL_WARPS * f, s>>>(a));
     return LCE_OK;
 }
 
 // Rows that start on 16-byte boundaries are read in 16-byte vectors, else in
 // 8-byte ones where that fits (60 experts in 16 bits), else by the element.
 template <typename T>
-lce_status_t bal_pass(BalArgs a, BalMode mode, cudaStream_t s) {
+lce_status_t bal_pass(const BalArgs& a, BalMode mode, cudaStream_t s) {
     auto fits = [&](int vec) {
         const size_t b = vec * sizeof(T);
         return a.E % vec == 0 && a.zt % vec == 0 && a.zg % vec == 0 && aligned_to(a.z, b) && aligned_to(a.dz, b);
     };
     constexpr int V16 = 16 / sizeof(T), V8 = 8 / sizeof(T);
-    const int vec = fits(V16) ? V16 : fits(V8) ? V8 : 1;
-    const int n = a.E / vec;
-    a.lanes = 1;
-    while (a.lanes < n && a.lanes < 32) a.lanes *= 2;
-    const int items = (n + a.lanes - 1) / a.lanes;
-    if (vec == V16)
-        return items <= 1   ? bal_pass_items<T, V16, 1>(a, mode, s)
-               : items <= 2 ? bal_pass_items<T, V16, 2>(a, mode, s)
-               : items <= 4 ? bal_pass_items<T, V16, 4>(a, mode, s)
-                            : bal_pass_items<T, V16, 8>(a, mode, s);
-    if (vec == V8)
-        return items <= 1   ? bal_pass_items<T, V8, 1>(a, mode, s)
-               : items <= 4 ? bal_pass_items<T, V8, 4>(a, mode, s)
-                            : bal_pass_items<T, V8, 16>(a, mode, s);
-    return items <= 2   ? bal_pass_items<T, 1, 2>(a, mode, s)
-           : items <= 8 ? bal_pass_items<T, 1, 8>(a, mode, s)
-                        : bal_pass_items<T, 1, 32>(a, mode, s);
+    if (fits(V16)) {
+        const int n = a.E / V16;
+        return n <= 1    ? bal_pass_form<T, V16, 1, 1>(a, mode, s)
+               : n <= 2  ? bal_pass_form<T, V16, 2, 1>(a, mode, s)
+               : n <= 4  ? bal_pass_form<T, V16, 4, 1>(a, mode, s)
+               : n <= 8  ? bal_pass_form<T, V16, 8, 1>(a, mode, s)
+               : n <= 16 ? bal_pass_form<T, V16, 16, 1>(a, mode, s)
+               : n <= 32 ? bal_pass_form<T, V16, 32, 1>(a, mode, s)
+               : n <= 64 ? bal_pass_form<T, V16, 32, 2>(a, mode, s)
+                         : bal_pass_form<T, V16, 32, LCE_BALANCE_MAX_E / (32 * V16)>(a, mode, s);
+    }
+    if (fits(V8)) {
+        const int n = a.E / V8;
+        return n <= 16   ? bal_pass_form<T, V8, 16, 1>(a, mode, s)
+               : n <= 32 ? bal_pass_form<T, V8, 32, 1>(a, mode, s)
+                         : bal_pass_form<T, V8, 32, LCE_BALANCE_MAX_E / (32 * V8)>(a, mode, s);
+    }
+    return a.E <= 16    ? bal_pass_form<T, 1, 8, 2>(a, mode, s)
+           : a.E <= 64  ? bal_pass_form<T, 1, 32, 2>(a, mode, s)
+           : a.E <= 256 ? bal_pass_form<T, 1, 32, 8>(a, mode, s)
+                        : bal_pass_form<T, 1, 32, 32>(a, mode, s);
 }
 
 }  // namespace

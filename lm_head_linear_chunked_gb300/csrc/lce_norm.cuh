@@ -81,30 +81,15 @@ __device__ __forceinline__ float load_w(const void* w, bool w32, int64_t i) {
 // of a block.  The row stays in registers between the sums and the output, as
 // pairs of FP32 values.
 template <typename T, int VEC, int ITEMS>
-struct RowRegs {
-    static constexpr int PAIRS = ITEMS * VEC / 2;
-    Vec<T, VEC> v[ITEMS];
+struct RowRegs : RowVectors<T, VEC, ITEMS> {
+    using Base = RowVectors<T, VEC, ITEMS>;
+    using Base::v;
+    static constexpr int PAIRS = Base::PAIRS;
     __device__ __forceinline__ void load(const T* row, int t, int tpr, int n) {
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             v[i] = Vec<T, VEC>{};
             if (i * tpr + t < n) v[i] = reinterpret_cast<const Vec<T, VEC>*>(row)[i * tpr + t];
-        }
-    }
-    // Pair p: two neighbours of a vector, or with single elements (VEC = 1)
-    // the elements 2p and 2p + 1 of the thread.
-    __device__ __forceinline__ F2 pair(int p) const {
-        if constexpr (VEC == 1)
-            return f2(to_f32(v[2 * p].v[0]), to_f32(v[2 * p + 1].v[0]));
-        else
-            return pair_of(v[2 * p / VEC].v + 2 * p % VEC);
-    }
-    __device__ __forceinline__ void set(int p, F2 x) {
-        if constexpr (VEC == 1) {
-            v[2 * p].v[0] = from_f32<T>(lo(x));
-            v[2 * p + 1].v[0] = from_f32<T>(hi(x));
-        } else {
-            set_pair(v[2 * p / VEC].v + 2 * p % VEC, x);
         }
     }
     __device__ __forceinline__ void store(T* row, int t, int tpr, int n) const {

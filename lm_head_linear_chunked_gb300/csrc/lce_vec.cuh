@@ -65,6 +65,13 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 
+// 2^x by the hardware's approximation (relative error 2^-22), 0 below 2^-126.
+__device__ __forceinline__ float fast_exp2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Two neighbouring elements as a pair, and back (rounded to nearest even).
 __device__ __forceinline__ F2 pair_of(const float* v) { return f2(v[0], v[1]); }
 __device__ __forceinline__ F2 pair_of(const __nv_bfloat16* v) {
@@ -85,6 +92,28 @@ __device__ __forceinline__ void set_pair(__half* v, F2 a) {
     const __half2 r = __floats2half2_rn(lo(a), hi(a));
     __builtin_memcpy(v, &r, 4);
 }
+
+// A thread's vectors of a row, seen as pairs: two neighbours of a vector, or
+// with single elements (VEC = 1) the elements 2p and 2p + 1 of the thread.
+template <typename T, int VEC, int ITEMS>
+struct RowVectors {
+    static constexpr int PAIRS = ITEMS * VEC / 2;
+    Vec<T, VEC> v[ITEMS];
+    __device__ __forceinline__ F2 pair(int p) const {
+        if constexpr (VEC == 1)
+            return f2(to_f32(v[2 * p].v[0]), to_f32(v[2 * p + 1].v[0]));
+        else
+            return pair_of(v[2 * p / VEC].v + 2 * p % VEC);
+    }
+    __device__ __forceinline__ void set(int p, F2 x) {
+        if constexpr (VEC == 1) {
+            v[2 * p].v[0] = from_f32<T>(lo(x));
+            v[2 * p + 1].v[0] = from_f32<T>(hi(x));
+        } else {
+            set_pair(v[2 * p / VEC].v + 2 * p % VEC, x);
+        }
+    }
+};
 
 // Elements of T in a 16-byte vector.
 template <typename T>
