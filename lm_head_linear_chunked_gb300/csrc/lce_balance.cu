@@ -94,7 +94,7 @@ lce_status_t bal_pass_any(const BalArgs& a, int dtype, BalMode mode, cudaStream_
 
 int64_t bal_parts(int64_t G, int64_t T) {
     const int64_t most = (T + BAL_MIN_TOKENS - 1) / BAL_MIN_TOKENS;
-    const int64_t p = (BAL_BLOCKS + G - 1) / G;
+    const int64_t p = BAL_BLOCKS / G > 1 ? BAL_BLOCKS / G : 1;
     return p < most ? p : most;
 }
 

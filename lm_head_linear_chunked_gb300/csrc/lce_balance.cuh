@@ -26,7 +26,9 @@ namespace lce {
 constexpr int BAL_WARPS = 8;
 constexpr int BAL_THREADS = 32 * BAL_WARPS;
 // Blocks of the pass over all groups (a group's blocks share its tokens out):
-// four on each of 152 SMs; and the fewest tokens that are worth one.
+// at most four on each of 152 SMs, which all run at once (sixteen more than
+// that took a second round, and half as long again); and the fewest tokens
+// that are worth one.
 constexpr int64_t BAL_BLOCKS = 608;
 constexpr int64_t BAL_MIN_TOKENS = 32;
 // Blocks per group of the counting by itself (the fused call): every block of
@@ -142,7 +144,7 @@ __device__ __forceinline__ void open_finish(const BalArgs& a) {
 
 // One pass over a part's logits: column sums of p, the gradient, or both.
 // Vector i of lane l holds the experts (i lanes + l) VEC + 0 .. VEC - 1; the
-// next token's vectors are read while this one's are worked on.  A token that
+// next tokens' vectors are read while this one's are worked on.  A token that
 // the mask leaves out counts as a row of zeros with a factor of zero, so what
 // it holds is never used and the lanes of a warp stay together.
 template <typename T, int VEC, int LANES, int ITEMS, int MODE>
@@ -154,7 +156,8 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
     extern __shared__ float sm[];  // f [E]; histograms or the warps' sums [BAL_WARPS, E]
     __shared__ float scale_s;
     const int g = blockIdx.y, part = blockIdx.x;
-    constexpr int tpw = 32 / LANES;  // tokens of a warp at a time
+    constexpr int tpw = 32 / LANES;                 // tokens of a warp at a time
+    constexpr int AHEAD = ITEMS * sizeof(V) <= 32 ? 3 : 1;  // tokens read ahead
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane & (LANES - 1), sub = lane / LANES;
     const int n = a.E / VEC;
@@ -209,24 +212,31 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
     T* dzg = GRAD ? static_cast<T*>(a.dz) + static_cast<int64_t>(g) * a.T * a.E : nullptr;
     const int64_t step = BAL_WARPS * tpw;
     int64_t t = t0 + warp * tpw + sub;
-    V next[ITEMS];
-    bool next_ok = false;
-    auto fetch = [&](int64_t at) {
-        next_ok = at < t1 && kept(a, g, at);
+    V next[AHEAD][ITEMS];
+    bool next_ok[AHEAD];
+    auto fetch = [&](int64_t at, V* to, bool* valid) {
+        *valid = at < t1 && kept(a, g, at);
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            next[i] = V{};
-            if (at < t1 && (whole || i * LANES + l < n)) next[i] = reinterpret_cast<const V*>(zg + at * a.zt)[i * LANES + l];
+            to[i] = V{};
+            if (at < t1 && (whole || i * LANES + l < n)) to[i] = reinterpret_cast<const V*>(zg + at * a.zt)[i * LANES + l];
         }
     };
-    fetch(t);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) fetch(t + k * step, next[k], next_ok + k);
     // the warp's first subgroup has the lowest token: the warp goes on while that one has
     for (; t - sub < t1; t += step) {
         RowVectors<T, VEC, ITEMS> z;
-        const bool ok = next_ok;
+        const bool ok = next_ok[0];
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? next[i] : V{};
-        fetch(t + step);
+        for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? next[0][i] : V{};
+#pragma unroll
+        for (int k = 0; k + 1 < AHEAD; ++k) {
+            next_ok[k] = next_ok[k + 1];
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) next[k][i] = next[k + 1][i];
+        }
+        fetch(t + AHEAD * step, next[AHEAD - 1], next_ok + AHEAD - 1);
         F2 v[PAIRS];
         float m = -INFINITY;
 #pragma unroll
