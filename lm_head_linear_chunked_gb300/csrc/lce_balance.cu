@@ -83,10 +83,10 @@ __global__ void __launch_bounds__(1024) bal_finish_kernel(BalArgs a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
     const bool wrong = (__ldcg(&a.hdr->status) & STATUS_INDEX) != 0;
-    if (lane == 0) *a.loss = wrong ? __int_as_float(0x7FC00000) : static_cast<float>(total * a.inv_groups);
+    if (lane == 0) *a.loss = wrong ? __int_as_float(0x7FC00000) : static_cast<float>(total / a.groups);
 }
 
-lce_status_t bal_pass_any(const BalArgs& a, int dtype, BalMode mode, cudaStream_t s) {
+lce_status_t bal_pass_any(BalArgs& a, int dtype, BalMode mode, cudaStream_t s) {
     return dtype == LCE_BF16  ? bal_pass_bf16(a, mode, s)
            : dtype == LCE_F16 ? bal_pass_f16(a, mode, s)
                               : bal_pass_f32(a, mode, s);
@@ -153,7 +153,7 @@ lce_status_t bal_in(const BalIn& in, BalArgs* a) {
     a->G = static_cast<int32_t>(in.G);
     a->E = static_cast<int32_t>(in.E);
     a->k = static_cast<int32_t>(in.k);
-    a->inv_groups = (in.flags & LCE_REDUCTION_SUM) ? 1.f : 1.f / static_cast<float>(in.G);
+    a->groups = (in.flags & LCE_REDUCTION_SUM) ? 1 : in.G;
     return LCE_OK;
 }
 

@@ -29,7 +29,10 @@ constexpr int BAL_THREADS = 32 * BAL_WARPS;
 // at most four on each of 152 SMs, which all run at once (sixteen more than
 // that took a second round, and half as long again); and the fewest tokens
 // that are worth one.
-constexpr int64_t BAL_BLOCKS = 608;
+constexpr int64_t BAL_SMS = 152;
+constexpr int64_t BAL_BLOCKS = 4 * BAL_SMS;
+// Blocks of the pass on an SM, by the experts of a lane (which it keeps in registers).
+constexpr int bal_resident(int experts) { return experts <= 8 ? 4 : experts <= 16 ? 2 : 1; }
 constexpr int64_t BAL_MIN_TOKENS = 32;
 // Blocks per group of the counting by itself (the fused call): every block of
 // the pass adds their counts up, so they are few.
@@ -56,18 +59,20 @@ struct BalArgs {
     const int64_t* n_valid;
     float grad_scale;
     const float* d_grad_output;
-    float inv_groups;  // 1 / G, or 1 for the sum over groups
+    int64_t groups;    // that the loss is divided by: G, or 1 for the sum over groups
     void* dz;          // [G, T, E], contiguous
     // outputs of the finish
     float *loss, *group_loss;
     int64_t *counts_out, *n_out;
 };
 
+// The pass chooses its number of parts by the form it takes (at most the
+// workspace's) and leaves it in `a` for the finish.
 enum BalMode { BAL_FORWARD, BAL_BACKWARD, BAL_FUSED };
 
-lce_status_t bal_pass_bf16(const BalArgs& a, BalMode mode, cudaStream_t s);
-lce_status_t bal_pass_f16(const BalArgs& a, BalMode mode, cudaStream_t s);
-lce_status_t bal_pass_f32(const BalArgs& a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_bf16(BalArgs& a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_f16(BalArgs& a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_f32(BalArgs& a, BalMode mode, cudaStream_t s);
 
 namespace {
 
@@ -148,16 +153,17 @@ __device__ __forceinline__ void open_finish(const BalArgs& a) {
 // the mask leaves out counts as a row of zeros with a factor of zero, so what
 // it holds is never used and the lanes of a warp stay together.
 template <typename T, int VEC, int LANES, int ITEMS, int MODE>
-__global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
+__global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pass_kernel(BalArgs a) {
     constexpr bool SUM = MODE != BAL_BACKWARD, GRAD = MODE != BAL_FORWARD;
     constexpr int PAIRS = ITEMS * VEC / 2;
     constexpr float LOG2E = 1.4426950408889634f;
     using V = Vec<T, VEC>;
     extern __shared__ float sm[];  // f [E]; histograms or the warps' sums [BAL_WARPS, E]
     __shared__ float scale_s;
+    __shared__ int64_t n_s;
     const int g = blockIdx.y, part = blockIdx.x;
     constexpr int tpw = 32 / LANES;                 // tokens of a warp at a time
-    constexpr int AHEAD = ITEMS * sizeof(V) <= 32 ? 3 : 1;  // tokens read ahead
+    constexpr int AHEAD = ITEMS * sizeof(V) <= 32 ? 2 : 1;  // tokens read ahead
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane & (LANES - 1), sub = lane / LANES;
     const int n = a.E / VEC;
@@ -172,31 +178,39 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
     float scale = 0.f;
     auto column = [&](int e) { return ((e / VEC) * LANES + l) * VEC + e % VEC; };
     if (GRAD) {
-        // f - 1 from the group's counts: finished (the backward), or the sums of their parts
-        int64_t kept_n = 0;
-        if (MODE == BAL_BACKWARD) {
-            kept_n = a.n_valid[g];
-        } else {
-            for (int q = 0; q < a.count_parts; ++q) {
-                const int32_t m = a.part_n[static_cast<int64_t>(g) * a.count_parts + q];
-                kept_n += m < 0 ? -1 - m : m;
+        // f - 1 = (c E - k n) / (k n), the numerator exact in integers, from the group's
+        // counts: finished (the backward), or the sums of their parts.  (In FP64 this took
+        // 20 of 60 us on 2^26 logits: its rate is 1/64.)
+        if (warp == 0) {
+            int32_t m = 0;
+            if (MODE == BAL_FUSED)
+                for (int q = lane; q < a.count_parts; q += 32) {
+                    const int32_t v = a.part_n[static_cast<int64_t>(g) * a.count_parts + q];
+                    m += v < 0 ? -1 - v : v;
+                }
+            const int64_t kept_n = MODE == BAL_BACKWARD ? a.n_valid[g] : __reduce_add_sync(0xFFFFFFFFu, m);
+            if (lane == 0) {
+                const float go = a.d_grad_output ? *a.d_grad_output : 1.f;
+                n_s = kept_n;
+                scale_s = kept_n > 0 ? a.grad_scale * go / static_cast<float>(a.groups * kept_n) : 0.f;
             }
         }
-        const double per = kept_n > 0 ? static_cast<double>(a.E) / (static_cast<double>(a.k) * kept_n) : 0.0;
-        for (int e = threadIdx.x; e < a.E; e += BAL_THREADS) {
-            int64_t c = 0;
-            if (MODE == BAL_BACKWARD) {
-                c = a.counts[static_cast<int64_t>(g) * a.E + e];
-            } else {
-#pragma unroll 4
-                for (int q = 0; q < a.count_parts; ++q)
-                    c += a.part_c[(static_cast<int64_t>(g) * a.count_parts + q) * a.E + e];
+        int64_t c = 0;
+        for (int e0 = 0; e0 < a.E; e0 += BAL_THREADS) {
+            const int e = e0 + threadIdx.x;
+            c = 0;
+            if (e < a.E) {
+                if (MODE == BAL_BACKWARD) {
+                    c = a.counts[static_cast<int64_t>(g) * a.E + e];
+                } else {
+#pragma unroll 8
+                    for (int q = 0; q < a.count_parts; ++q)
+                        c += a.part_c[(static_cast<int64_t>(g) * a.count_parts + q) * a.E + e];
+                }
             }
-            sm[e] = static_cast<float>(static_cast<double>(c) * per - 1.0);
-        }
-        if (threadIdx.x == 0) {
-            const float go = a.d_grad_output ? *a.d_grad_output : 1.f;
-            scale_s = kept_n > 0 ? static_cast<float>(static_cast<double>(a.grad_scale) * go * a.inv_groups / kept_n) : 0.f;
+            if (e0 == 0) __syncthreads();  // n_s
+            const int64_t all = a.k * n_s;
+            if (e < a.E) sm[e] = all > 0 ? static_cast<float>(c * a.E - all) / static_cast<float>(all) : 0.f;
         }
         __syncthreads();
         scale = scale_s;
@@ -224,19 +238,13 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
     };
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) fetch(t + k * step, next[k], next_ok + k);
-    // the warp's first subgroup has the lowest token: the warp goes on while that one has
-    for (; t - sub < t1; t += step) {
+    // one token of each subgroup, from slot k of the tokens read ahead
+    auto token = [&](V (&slot)[ITEMS], bool& slot_ok) {
         RowVectors<T, VEC, ITEMS> z;
-        const bool ok = next_ok[0];
+        const bool ok = slot_ok;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? next[0][i] : V{};
-#pragma unroll
-        for (int k = 0; k + 1 < AHEAD; ++k) {
-            next_ok[k] = next_ok[k + 1];
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) next[k][i] = next[k + 1][i];
-        }
-        fetch(t + AHEAD * step, next[AHEAD - 1], next_ok + AHEAD - 1);
+        for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? slot[i] : V{};
+        fetch(t + AHEAD * step, slot, &slot_ok);
         F2 v[PAIRS];
         float m = -INFINITY;
 #pragma unroll
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
             s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             if (GRAD) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
         }
-        const float r = ok ? __frcp_rn(s) : 0.f;
+        const float r = ok ? fast_rcp(s) : 0.f;
         const F2 r2 = f2(r), fp = f2(-q * r), sr = f2(scale * r);
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
@@ -276,7 +284,14 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i)
                 if (whole || i * LANES + l < n) reinterpret_cast<V*>(dzg + t * a.E)[i * LANES + l] = z.v[i];
-    }
+    };
+    // the warp's first subgroup has the lowest token: the warp goes on while that one has
+    while (t - sub < t1)
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (t - sub < t1) token(next[k], next_ok[k]);
+            t += step;
+        }
     if (!SUM) return;
     // the subgroups of a warp, then the warps, in a fixed order
 #pragma unroll
@@ -299,7 +314,11 @@ __global__ void __launch_bounds__(BAL_THREADS) bal_pass_kernel(BalArgs a) {
 }
 
 template <typename T, int VEC, int LANES, int ITEMS>
-lce_status_t bal_pass_form(const BalArgs& a, BalMode mode, cudaStream_t s) {
+lce_status_t bal_pass_form(BalArgs& a, BalMode mode, cudaStream_t s) {
+    const int64_t fit = BAL_SMS * bal_resident(ITEMS * VEC) / a.G;
+    if (a.parts > fit) a.parts = static_cast<int32_t>(fit > 1 ? fit : 1);
+    if (mode == BAL_FORWARD) a.count_parts = a.parts;
+    a.per_part = (a.T + a.parts - 1) / a.parts;
     const dim3 grid(a.parts, a.G);
     const size_t f = static_cast<size_t>(a.E) * 4;
     if (mode == BAL_FORWARD)
@@ -314,7 +333,7 @@ lce_status_t bal_pass_form(const BalArgs& a, BalMode mode, cudaStream_t s) {
 // Rows that start on 16-byte boundaries are read in 16-byte vectors, else in
 // 8-byte ones where that fits (60 experts in 16 bits), else by the element.
 template <typename T>
-lce_status_t bal_pass(const BalArgs& a, BalMode mode, cudaStream_t s) {
+lce_status_t bal_pass(BalArgs& a, BalMode mode, cudaStream_t s) {
     auto fits = [&](int vec) {
         const size_t b = vec * sizeof(T);
         return a.E % vec == 0 && a.zt % vec == 0 && a.zg % vec == 0 && aligned_to(a.z, b) && aligned_to(a.dz, b);

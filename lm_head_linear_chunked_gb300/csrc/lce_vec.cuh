@@ -72,6 +72,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return r;
 }
 
+// 1 / x by the hardware's approximation (one unit in the last place).
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Two neighbouring elements as a pair, and back (rounded to nearest even).
 __device__ __forceinline__ F2 pair_of(const float* v) { return f2(v[0], v[1]); }
 __device__ __forceinline__ F2 pair_of(const __nv_bfloat16* v) {
