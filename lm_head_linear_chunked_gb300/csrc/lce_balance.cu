@@ -1,92 +1,19 @@
-// The balance loss's counting and finish, and its C entry points (the
+// The balance loss's counting and its C entry points (the
 // mathematics and the pass over the logits: lce_balance.cuh).
 #include "lce_balance.cuh"
 
 namespace lce {
 namespace {
 
-// Counts by themselves, before the fused call's pass.
+// Counts, before the pass over the logits.
 __global__ void __launch_bounds__(BAL_THREADS) bal_count_kernel(BalArgs a) {
     extern __shared__ int32_t hist[];
-    open_finish(a);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.done = 0;
     const int64_t t0 = blockIdx.x * a.per_count;
     count_tokens(a, blockIdx.y, blockIdx.x, t0, t0 + a.per_count < a.T ? t0 + a.per_count : a.T, hist);
 }
 
-// Adds the parts up.  A block takes 32 experts of a group, a row of 32 threads
-// each 1/32 of the parts; the last block to end adds the blocks' shares of the
-// loss, in order.  The sums are FP32 (at most 24 terms in sequence; this GPU's
-// FP64 adds run at 1/64 of their rate, and took 8 of 11 us here) and only the
-// last few scalars FP64.
-__global__ void __launch_bounds__(1024) bal_finish_kernel(BalArgs a) {
-    __shared__ float sp[32][33];
-    __shared__ long long sc[32][33];
-    __shared__ int32_t sn[32];
-    __shared__ int bad;
-    __shared__ bool last;
-    const int g = blockIdx.y, lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const int e = blockIdx.x * 32 + lane;
-    if (threadIdx.x == 0) bad = 0;
-    __syncthreads();
-    float p = 0.f;
-    long long c = 0;
-    int32_t n = 0;
-    if (e < a.E) {
-#pragma unroll 4
-        for (int q = row; q < a.parts; q += 32) p += a.part_p[(static_cast<int64_t>(g) * a.parts + q) * a.E + e];
-#pragma unroll 4
-        for (int q = row; q < a.count_parts; q += 32) c += a.part_c[(static_cast<int64_t>(g) * a.count_parts + q) * a.E + e];
-    }
-    sp[row][lane] = p;
-    sc[row][lane] = c;
-    for (int q = threadIdx.x; q < a.count_parts; q += 1024) {
-        const int32_t m = a.part_n[static_cast<int64_t>(g) * a.count_parts + q];
-        n += m < 0 ? -1 - m : m;
-        if (m < 0) bad = 1;
-    }
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (lane == 0) sn[row] = n;
-    __syncthreads();
-    p = warp_sum(sp[lane][row]);  // expert `row` of the block
-    c = sc[lane][row];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
-    __syncthreads();
-    if (lane == 0) {
-        const int at = blockIdx.x * 32 + row;
-        if (at < a.E) a.counts_out[static_cast<int64_t>(g) * a.E + at] = c;
-        sp[0][row] = at < a.E ? static_cast<float>(c) * p : 0.f;
-    }
-    __syncthreads();
-    if (row == 0) {
-        const float v = warp_sum(sp[0][lane]);
-        n = __reduce_add_sync(0xFFFFFFFFu, sn[lane]);
-        if (lane == 0) {
-            a.part_l[static_cast<int64_t>(g) * gridDim.x + blockIdx.x] =
-                n > 0 ? static_cast<double>(v) * a.E / (static_cast<double>(a.k) * n * n) : 0.0;
-            if (blockIdx.x == 0) a.n_out[g] = n;
-            if (bad) atomicOr(&a.hdr->status, STATUS_INDEX);
-            __threadfence();
-            last = atomicAdd(a.done, 1u) == gridDim.x * gridDim.y - 1;
-        }
-    }
-    __syncthreads();
-    if (!last || row != 0) return;
-    __threadfence();
-    double total = 0.0;
-    for (int k = lane; k < a.G; k += 32) {
-        double v = 0.0;
-        for (unsigned i = 0; i < gridDim.x; ++i) v += __ldcg(a.part_l + static_cast<int64_t>(k) * gridDim.x + i);
-        if (a.group_loss) a.group_loss[k] = static_cast<float>(v);
-        total += v;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    const bool wrong = (__ldcg(&a.hdr->status) & STATUS_INDEX) != 0;
-    if (lane == 0) *a.loss = wrong ? __int_as_float(0x7FC00000) : static_cast<float>(total / a.groups);
-}
-
-lce_status_t bal_pass_any(BalArgs& a, int dtype, BalMode mode, cudaStream_t s) {
+lce_status_t bal_pass_any(const BalArgs& a, int dtype, BalMode mode, cudaStream_t s) {
     return dtype == LCE_BF16  ? bal_pass_bf16(a, mode, s)
            : dtype == LCE_F16 ? bal_pass_f16(a, mode, s)
                               : bal_pass_f32(a, mode, s);
@@ -106,26 +33,26 @@ lce_status_t bal_sizes(int64_t G, int64_t T, int64_t E, int64_t k) {
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-size_t bal_ws(int64_t G, int64_t T, int64_t E, bool fused, BalArgs* a, void* ws) {
-    const int64_t parts = bal_parts(G, T);
-    const int64_t counting = fused && parts > BAL_COUNT_PARTS ? BAL_COUNT_PARTS : parts;
-    const size_t c = 1024, n = c + align256(static_cast<size_t>(G * parts * E) * 4);
-    const size_t p = n + align256(static_cast<size_t>(G * parts) * 4);
-    const size_t l = p + align256(static_cast<size_t>(G * parts * E) * 4);
+size_t bal_ws(int64_t G, int64_t T, int64_t E, BalArgs* a, void* ws) {
+    int64_t parts = bal_parts(G, T);
+    const bool alone = G == 1 && T <= BAL_ALONE_TOKENS;
+    if (alone) parts = 1;
+    const int64_t counting = parts < BAL_COUNT_PARTS ? parts : BAL_COUNT_PARTS;
+    const size_t c = 1024, n = c + align256(static_cast<size_t>(G * counting * E) * 4);
+    const size_t q = n + align256(static_cast<size_t>(G * counting) * 4);
     if (a) {
         uint8_t* w = static_cast<uint8_t*>(ws);
         a->parts = static_cast<int32_t>(parts);
-        a->per_part = (T + parts - 1) / parts;
         a->count_parts = static_cast<int32_t>(counting);
         a->per_count = (T + counting - 1) / counting;
+        a->inline_count = alone;
         a->hdr = reinterpret_cast<WsHeader*>(w);
         a->done = reinterpret_cast<unsigned*>(w + 256);
         a->part_c = reinterpret_cast<int32_t*>(w + c);
         a->part_n = reinterpret_cast<int32_t*>(w + n);
-        a->part_p = reinterpret_cast<float*>(w + p);
-        a->part_l = reinterpret_cast<double*>(w + l);
+        a->part_q = reinterpret_cast<float*>(w + q);
     }
-    return l + align256(static_cast<size_t>(G * ((E + 31) / 32)) * 8);
+    return q + align256(static_cast<size_t>(G * parts) * 4);
 }
 
 struct BalIn {
@@ -169,7 +96,7 @@ lce_status_t bal_loss(const BalIn& in, const void* idx, int idx_bytes, bool grad
     if (!counts || !n_valid || !aligned_to(counts, 8) || !aligned_to(n_valid, 8)) return LCE_ERR_INVALID_ARG;
     if (!ws || !aligned_to(ws, 256) || !aligned_to(d_grad_output, 4)) return LCE_ERR_INVALID_ARG;
     if (grad && (!dz || !aligned_to(dz, dtype_bytes(in.dtype)))) return LCE_ERR_INVALID_ARG;
-    if (ws_bytes < bal_ws(in.G, in.T, in.E, grad, &a, ws)) return LCE_ERR_WORKSPACE;
+    if (ws_bytes < bal_ws(in.G, in.T, in.E, &a, ws)) return LCE_ERR_WORKSPACE;
     a.idx = idx;
     a.idx64 = idx_bytes == 8;
     a.grad_scale = grad_scale;
@@ -179,13 +106,10 @@ lce_status_t bal_loss(const BalIn& in, const void* idx, int idx_bytes, bool grad
     a.group_loss = group_loss;
     a.counts_out = counts;
     a.n_out = n_valid;
-    if (grad)
+    if (!a.inline_count)
         LCE_PROFILED(bal_count_kernel<<<dim3(a.count_parts, a.G), BAL_THREADS,
                                         static_cast<size_t>(a.E) * 4 * BAL_WARPS, s>>>(a));
-    const lce_status_t pt = bal_pass_any(a, in.dtype, grad ? BAL_FUSED : BAL_FORWARD, s);
-    if (pt != LCE_OK) return pt;
-    LCE_PROFILED(bal_finish_kernel<<<dim3((a.E + 31) / 32, a.G), 1024, 0, s>>>(a));
-    return LCE_OK;
+    return bal_pass_any(a, in.dtype, grad ? BAL_FUSED : BAL_FORWARD, s);
 }
 
 }  // namespace
@@ -198,7 +122,7 @@ extern "C" {
 lce_status_t lce_balance_workspace_size(int64_t groups, int64_t T, int64_t E, int64_t k, size_t* bytes) {
     if (!bytes) return LCE_ERR_INVALID_ARG;
     const lce_status_t st = bal_sizes(groups, T, E, k);
-    if (st == LCE_OK) *bytes = bal_ws(groups, T, E, false, nullptr, nullptr);
+    if (st == LCE_OK) *bytes = bal_ws(groups, T, E, nullptr, nullptr);
     return st;
 }
 

@@ -10,9 +10,13 @@
 // without the cancellation of two numbers near 1 when the load is even.
 //
 // The counts need only the expert indices, which are k/E of the logits'
-// size, so the loss and its gradient together take one pass over the logits.
-// Nothing is added by atomics on floats: each block writes its own sums, and
-// they are added in a fixed order.
+// size.  With them first, one pass over the logits gives loss and gradient:
+// per token both need q = sum_j (f_j - 1) p_tj, and
+//
+//   L_g = 1 + sum_t q_t / n_g.
+//
+// Nothing is added by atomics on floats: each block writes its own sum, and
+// the last block to end adds them in a fixed order.
 //
 // A row of logits is short (8 to 1024 values), so a token takes only as many
 // lanes of a warp as it has 16-byte vectors, and its sums as many shuffles.
@@ -34,9 +38,13 @@ constexpr int64_t BAL_BLOCKS = 4 * BAL_SMS;
 // Blocks of the pass on an SM, by the experts of a lane (which it keeps in registers).
 constexpr int bal_resident(int experts) { return experts <= 8 ? 4 : experts <= 16 ? 2 : 1; }
 constexpr int64_t BAL_MIN_TOKENS = 32;
-// Blocks per group of the counting by itself (the fused call): every block of
-// the pass adds their counts up, so they are few.
+// Blocks per group of the counting: every block of the pass adds their counts
+// up, so they are few.
 constexpr int64_t BAL_COUNT_PARTS = 32;
+
+// Up to so many tokens of a single group, one block counts and passes over
+// them: one launch, not two.
+constexpr int64_t BAL_ALONE_TOKENS = 512;
 
 struct BalArgs {
     const void* z;
@@ -46,14 +54,14 @@ struct BalArgs {
     const uint8_t* mask;  // nullable; [T] with group stride 0, or [G, T]
     int64_t mask_g;
     int64_t T, per_part, per_count;
-    int32_t G, E, k, parts, count_parts;
-    // workspace: per (group, part) the counts, the kept tokens and the sums of p
+    int32_t G, E, k, parts, count_parts;  // the pass may take fewer parts than these
+    bool inline_count;  // one block in all: the pass counts by itself
+    // workspace
     WsHeader* hdr;
-    unsigned* done;    // blocks of the finish that are through
-    int32_t* part_c;   // [G, count_parts, E]
+    unsigned* done;    // blocks of the pass that are through
+    int32_t* part_c;   // [G, count_parts, E] counts
     int32_t* part_n;   // [G, count_parts]: kept tokens, or -1 - kept if an index is out of range
-    float* part_p;     // [G, parts, E]
-    double* part_l;    // [G, tiles] of the finish
+    float* part_q;     // [G, parts] sums of q
     // finished counts (read by the backward)
     const int64_t* counts;
     const int64_t* n_valid;
@@ -61,18 +69,16 @@ struct BalArgs {
     const float* d_grad_output;
     int64_t groups;    // that the loss is divided by: G, or 1 for the sum over groups
     void* dz;          // [G, T, E], contiguous
-    // outputs of the finish
+    // outputs of the forward
     float *loss, *group_loss;
     int64_t *counts_out, *n_out;
 };
 
-// The pass chooses its number of parts by the form it takes (at most the
-// workspace's) and leaves it in `a` for the finish.
 enum BalMode { BAL_FORWARD, BAL_BACKWARD, BAL_FUSED };
 
-lce_status_t bal_pass_bf16(BalArgs& a, BalMode mode, cudaStream_t s);
-lce_status_t bal_pass_f16(BalArgs& a, BalMode mode, cudaStream_t s);
-lce_status_t bal_pass_f32(BalArgs& a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_bf16(const BalArgs& a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_f16(const BalArgs& a, BalMode mode, cudaStream_t s);
+lce_status_t bal_pass_f32(const BalArgs& a, BalMode mode, cudaStream_t s);
 
 namespace {
 
@@ -139,26 +145,64 @@ __device__ __forceinline__ void count_tokens(const BalArgs& a, int g, int part, 
     if (threadIdx.x == 0) a.part_n[slot] = bad ? -1 - total : total;
 }
 
-// The finish starts from a zeroed counter and status.
-__device__ __forceinline__ void open_finish(const BalArgs& a) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-        a.hdr->status = 0;
-        *a.done = 0;
+// The last block of the pass adds the loss up: a warp over a group's parts,
+// four groups at a time, then the groups in order.
+__device__ __forceinline__ void finish_loss(const BalArgs& a) {
+    __shared__ int bad;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+    bool wrong = false;
+    for (int64_t k = threadIdx.x; k < static_cast<int64_t>(a.G) * a.count_parts; k += BAL_THREADS)
+        wrong |= __ldcg(a.part_n + k) < 0;
+    if (wrong) bad = 1;
+    for (int g0 = warp * 4; g0 < a.G; g0 += BAL_WARPS * 4) {
+        float q[4];
+        int64_t n[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int g = g0 + i < a.G ? g0 + i : a.G - 1;
+            q[i] = 0.f;
+            for (int k = lane; k < a.parts; k += 32) q[i] += __ldcg(a.part_q + static_cast<int64_t>(g) * a.parts + k);
+            n[i] = __ldcg(a.n_out + g);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q[i] = warp_sum(q[i]);
+            // the group's loss takes the place of its first part's sum
+            if (lane == 0 && g0 + i < a.G) {
+                q[i] = n[i] > 0 ? 1.f + q[i] / static_cast<float>(n[i]) : 0.f;
+                if (a.group_loss) a.group_loss[g0 + i] = q[i];
+                a.part_q[static_cast<int64_t>(g0 + i) * a.parts] = q[i];
+            }
+        }
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    float total = 0.f;
+    for (int g = lane; g < a.G; g += 32) total += a.part_q[static_cast<int64_t>(g) * a.parts];
+    total = warp_sum(total);
+    if (lane == 0) {
+        a.hdr->status = bad ? STATUS_INDEX : 0u;
+        *a.loss = bad ? __int_as_float(0x7FC00000) : total / static_cast<float>(a.groups);
     }
 }
 
-// One pass over a part's logits: column sums of p, the gradient, or both.
+// One pass over a part's logits: the loss, the gradient, or both.  INLINE: the
+// only block counts first.
 // Vector i of lane l holds the experts (i lanes + l) VEC + 0 .. VEC - 1; the
 // next tokens' vectors are read while this one's are worked on.  A token that
 // the mask leaves out counts as a row of zeros with a factor of zero, so what
 // it holds is never used and the lanes of a warp stay together.
 template <typename T, int VEC, int LANES, int ITEMS, int MODE>
 __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pass_kernel(BalArgs a) {
-    constexpr bool SUM = MODE != BAL_BACKWARD, GRAD = MODE != BAL_FORWARD;
+    constexpr bool LOSS = MODE != BAL_BACKWARD, GRAD = MODE != BAL_FORWARD;
     constexpr int PAIRS = ITEMS * VEC / 2;
     constexpr float LOG2E = 1.4426950408889634f;
     using V = Vec<T, VEC>;
-    extern __shared__ float sm[];  // f [E]; histograms or the warps' sums [BAL_WARPS, E]
+    extern __shared__ float sm[];  // f [E]; with the counting inline, histograms [BAL_WARPS, E]
+    __shared__ float warp_q[BAL_WARPS];
+    __shared__ bool last;
     __shared__ float scale_s;
     __shared__ int64_t n_s;
     const int g = blockIdx.y, part = blockIdx.x;
@@ -169,21 +213,21 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
     const int n = a.E / VEC;
     const bool whole = n == LANES * ITEMS;  // no lane has a vector outside the row
     const int64_t t0 = part * a.per_part, t1 = t0 + a.per_part < a.T ? t0 + a.per_part : a.T;
-    if (MODE == BAL_FORWARD) {
-        open_finish(a);
+    if (LOSS && a.inline_count) {
+        if (threadIdx.x == 0) *a.done = 0;
         count_tokens(a, g, part, t0, t1, reinterpret_cast<int32_t*>(sm));
         __syncthreads();
     }
-    F2 f[PAIRS], sum[PAIRS];
-    float scale = 0.f;
+    F2 f[PAIRS];
+    float scale = 0.f, q_sum = 0.f;
     auto column = [&](int e) { return ((e / VEC) * LANES + l) * VEC + e % VEC; };
-    if (GRAD) {
+    {
         // f - 1 = (c E - k n) / (k n), the numerator exact in integers, from the group's
         // counts: finished (the backward), or the sums of their parts.  (In FP64 this took
         // 20 of 60 us on 2^26 logits: its rate is 1/64.)
         if (warp == 0) {
             int32_t m = 0;
-            if (MODE == BAL_FUSED)
+            if (LOSS)
                 for (int q = lane; q < a.count_parts; q += 32) {
                     const int32_t v = a.part_n[static_cast<int64_t>(g) * a.count_parts + q];
                     m += v < 0 ? -1 - v : v;
@@ -192,7 +236,8 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
             if (lane == 0) {
                 const float go = a.d_grad_output ? *a.d_grad_output : 1.f;
                 n_s = kept_n;
-                scale_s = kept_n > 0 ? a.grad_scale * go / static_cast<float>(a.groups * kept_n) : 0.f;
+                if (LOSS && part == 0) a.n_out[g] = kept_n;
+                if (GRAD) scale_s = kept_n > 0 ? a.grad_scale * go / static_cast<float>(a.groups * kept_n) : 0.f;
             }
         }
         int64_t c = 0;
@@ -210,31 +255,36 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
             }
             if (e0 == 0) __syncthreads();  // n_s
             const int64_t all = a.k * n_s;
+            if (LOSS && part == 0 && e < a.E) a.counts_out[static_cast<int64_t>(g) * a.E + e] = c;
             if (e < a.E) sm[e] = all > 0 ? static_cast<float>(c * a.E - all) / static_cast<float>(all) : 0.f;
         }
         __syncthreads();
-        scale = scale_s;
+        if (GRAD) scale = scale_s;
     }
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) {
         const int c0 = column(2 * p), c1 = column(2 * p + 1);
-        f[p] = GRAD ? f2(c0 < a.E ? sm[c0] : 0.f, c1 < a.E ? sm[c1] : 0.f) : f2(0.f);
-        sum[p] = f2(0.f);
+        f[p] = f2(c0 < a.E ? sm[c0] : 0.f, c1 < a.E ? sm[c1] : 0.f);
     }
-    if (GRAD && SUM) __syncthreads();
-    const T* zg = static_cast<const T*>(a.z) + g * a.zg;
-    T* dzg = GRAD ? static_cast<T*>(a.dz) + static_cast<int64_t>(g) * a.T * a.E : nullptr;
-    const int64_t step = BAL_WARPS * tpw;
-    int64_t t = t0 + warp * tpw + sub;
+    // from here on tokens count from the part's first, in 32 bits
+    const int tokens = t1 > t0 ? static_cast<int>(t1 - t0) : 0;
+    constexpr int step = BAL_WARPS * tpw;
+    int t = warp * tpw + sub;
+    const V* src = reinterpret_cast<const V*>(static_cast<const T*>(a.z) + g * a.zg + (t0 + t) * a.zt) + l;
+    const int64_t src_step = step * a.zt / VEC;
+    V* dst = GRAD ? reinterpret_cast<V*>(static_cast<T*>(a.dz) + (static_cast<int64_t>(g) * a.T + t0 + t) * a.E) + l : nullptr;
+    const uint8_t* keep = a.mask ? a.mask + g * a.mask_g + t0 : nullptr;
     V next[AHEAD][ITEMS];
     bool next_ok[AHEAD];
-    auto fetch = [&](int64_t at, V* to, bool* valid) {
-        *valid = at < t1 && kept(a, g, at);
+    auto fetch = [&](int at, V* to, bool* valid) {
+        *valid = at < tokens;
+        if (at < tokens) {
+            if (keep) *valid = keep[at] != 0;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            to[i] = V{};
-            if (at < t1 && (whole || i * LANES + l < n)) to[i] = reinterpret_cast<const V*>(zg + at * a.zt)[i * LANES + l];
+            for (int i = 0; i < ITEMS; ++i)
+                if (whole || i * LANES + l < n) to[i] = src[i * LANES];
         }
+        src += src_step;
     };
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) fetch(t + k * step, next[k], next_ok + k);
@@ -246,14 +296,19 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
         for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? slot[i] : V{};
         fetch(t + AHEAD * step, slot, &slot_ok);
         F2 v[PAIRS];
-        float m = -INFINITY;
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
             v[p] = z.pair(p);
             if (!whole)
                 v[p] = f2((2 * p / VEC) * LANES + l < n ? lo(v[p]) : -INFINITY,
                           ((2 * p + 1) / VEC) * LANES + l < n ? hi(v[p]) : -INFINITY);
-            m = fmaxf(m, fmaxf(lo(v[p]), hi(v[p])));
+        }
+        float m = -INFINITY;
+        if (sizeof(T) == 2 && VEC > 1 && whole) {
+            m = z.max();  // two at a time in 16 bits: a maximum does not round
+        } else {
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p) m = fmaxf(m, fmaxf(lo(v[p]), hi(v[p])));
         }
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -265,75 +320,75 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
             const F2 y = fma2(v[p], l2, m2);
             v[p] = f2(fast_exp2(lo(y)), fast_exp2(hi(y)));
             s2 = add2(s2, v[p]);
-            if (GRAD) q2 = fma2(f[p], v[p], q2);
+            q2 = fma2(f[p], v[p], q2);
         }
-        float s = lo(s2) + hi(s2), q = GRAD ? lo(q2) + hi(q2) : 0.f;
+        float s = lo(s2) + hi(s2), q = lo(q2) + hi(q2);
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) {
             s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            if (GRAD) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+            q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
         }
         const float r = ok ? fast_rcp(s) : 0.f;
-        const F2 r2 = f2(r), fp = f2(-q * r), sr = f2(scale * r);
+        q *= r;
+        if (LOSS) q_sum += q;
+        if (GRAD) {
+            const F2 fq = f2(-q), sr = f2(scale * r);
 #pragma unroll
-        for (int p = 0; p < PAIRS; ++p) {
-            if (SUM) sum[p] = fma2(v[p], r2, sum[p]);
-            if (GRAD) z.set(p, mul2(mul2(v[p], sr), add2(f[p], fp)));
+            for (int p = 0; p < PAIRS; ++p) z.set(p, mul2(mul2(v[p], sr), add2(f[p], fq)));
         }
-        if (GRAD && t < t1)
+        if (GRAD) {
+            if (t < tokens)
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
-                if (whole || i * LANES + l < n) reinterpret_cast<V*>(dzg + t * a.E)[i * LANES + l] = z.v[i];
+                for (int i = 0; i < ITEMS; ++i)
+                    if (whole || i * LANES + l < n) dst[i * LANES] = z.v[i];
+            dst += step * n;
+        }
     };
     // the warp's first subgroup has the lowest token: the warp goes on while that one has
-    while (t - sub < t1)
+    while (t - sub < tokens)
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            if (t - sub < t1) token(next[k], next_ok[k]);
+            if (t - sub < tokens) token(next[k], next_ok[k]);
             t += step;
         }
-    if (!SUM) return;
-    // the subgroups of a warp, then the warps, in a fixed order
-#pragma unroll
-    for (int p = 0; p < PAIRS; ++p)
-        for (int o = LANES; o < 32; o <<= 1)
-            sum[p] = add2(sum[p], f2(__shfl_xor_sync(0xFFFFFFFFu, lo(sum[p]), o), __shfl_xor_sync(0xFFFFFFFFu, hi(sum[p]), o)));
-    if (sub == 0)
-#pragma unroll
-        for (int e = 0; e < 2 * PAIRS; ++e) {
-            const int c = column(e);
-            if (c < a.E) sm[warp * a.E + c] = e & 1 ? hi(sum[e / 2]) : lo(sum[e / 2]);
-        }
+    if (!LOSS) return;
+    // the subgroups of a warp (each of their lanes has their sum), then the warps
+    q_sum = warp_sum(l == 0 ? q_sum : 0.f);
+    if (lane == 0) warp_q[warp] = q_sum;
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += BAL_THREADS) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < BAL_WARPS; ++w) v += sm[w * a.E + e];
-        a.part_p[(static_cast<int64_t>(g) * a.parts + part) * a.E + e] = v;
+    if (threadIdx.x == 0) {
+        q_sum = 0.f;
+        for (int w = 0; w < BAL_WARPS; ++w) q_sum += warp_q[w];
+        a.part_q[static_cast<int64_t>(g) * a.parts + part] = q_sum;
+        __threadfence();  // with the counts of part 0, which the barrier put before this
+        last = atomicAdd(a.done, 1u) == gridDim.x * gridDim.y - 1;
     }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    finish_loss(a);
 }
 
 template <typename T, int VEC, int LANES, int ITEMS>
-lce_status_t bal_pass_form(BalArgs& a, BalMode mode, cudaStream_t s) {
+lce_status_t bal_pass_form(BalArgs a, BalMode mode, cudaStream_t s) {
     const int64_t fit = BAL_SMS * bal_resident(ITEMS * VEC) / a.G;
     if (a.parts > fit) a.parts = static_cast<int32_t>(fit > 1 ? fit : 1);
-    if (mode == BAL_FORWARD) a.count_parts = a.parts;
     a.per_part = (a.T + a.parts - 1) / a.parts;
     const dim3 grid(a.parts, a.G);
-    const size_t f = static_cast<size_t>(a.E) * 4;
+    const size_t smem = static_cast<size_t>(a.E) * 4 * (a.inline_count ? BAL_WARPS : 1);
     if (mode == BAL_FORWARD)
-        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FORWARD><<<grid, BAL_THREADS, BAL_WARPS * f, s>>>(a));
+        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FORWARD><<<grid, BAL_THREADS, smem, s>>>(a));
     else if (mode == BAL_BACKWARD)
-        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_BACKWARD><<<grid, BAL_THREADS, f, s>>>(a));
+        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_BACKWARD><<<grid, BAL_THREADS, smem, s>>>(a));
     else
-        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FUSED><<<grid, BAL_THREADS, BAL_WARPS * f, s>>>(a));
+        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FUSED><<<grid, BAL_THREADS, smem, s>>>(a));
     return LCE_OK;
 }
 
 // Rows that start on 16-byte boundaries are read in 16-byte vectors, else in
 // 8-byte ones where that fits (60 experts in 16 bits), else by the element.
 template <typename T>
-lce_status_t bal_pass(BalArgs& a, BalMode mode, cudaStream_t s) {
+lce_status_t bal_pass(const BalArgs& a, BalMode mode, cudaStream_t s) {
     auto fits = [&](int vec) {
         const size_t b = vec * sizeof(T);
         return a.E % vec == 0 && a.zt % vec == 0 && a.zg % vec == 0 && aligned_to(a.z, b) && aligned_to(a.dz, b);

@@ -100,6 +100,15 @@ __device__ __forceinline__ void set_pair(__half* v, F2 a) {
     __builtin_memcpy(v, &r, 4);
 }
 
+template <typename T>
+struct Pair16 {  // fp32 has no such pair; the type only has to exist
+    using type = __half2;
+};
+template <>
+struct Pair16<__nv_bfloat16> {
+    using type = __nv_bfloat162;
+};
+
 // A thread's vectors of a row, seen as pairs: two neighbours of a vector, or
 // with single elements (VEC = 1) the elements 2p and 2p + 1 of the thread.
 template <typename T, int VEC, int ITEMS>
@@ -111,6 +120,19 @@ struct RowVectors {
             return f2(to_f32(v[2 * p].v[0]), to_f32(v[2 * p + 1].v[0]));
         else
             return pair_of(v[2 * p / VEC].v + 2 * p % VEC);
+    }
+    // The largest value (NaN only if all are), without unpacking.
+    __device__ __forceinline__ float max() const {
+        using T2 = typename Pair16<T>::type;
+        T2 m;
+        __builtin_memcpy(&m, v[0].v, 4);
+#pragma unroll
+        for (int p = 1; p < PAIRS; ++p) {
+            T2 x;
+            __builtin_memcpy(&x, v[2 * p / VEC].v + 2 * p % VEC, 4);
+            m = __hmax2(m, x);
+        }
+        return fmaxf(to_f32(m.x), to_f32(m.y));
     }
     __device__ __forceinline__ void set(int p, F2 x) {
         if constexpr (VEC == 1) {
