@@ -8,6 +8,7 @@ namespace {
 // Counts, before the pass over the logits.
 __global__ void __launch_bounds__(BAL_THREADS) bal_count_kernel(BalArgs a) {
     extern __shared__ int32_t hist[];
+    launch_dependents();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.done = 0;
     const int64_t t0 = blockIdx.x * a.per_count;
     count_tokens(a, blockIdx.y, blockIdx.x, t0, t0 + a.per_count < a.T ? t0 + a.per_count : a.T, hist);

@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
     const int n = a.E / VEC;
     const bool whole = n == LANES * ITEMS;  // no lane has a vector outside the row
     const int64_t t0 = part * a.per_part, t1 = t0 + a.per_part < a.T ? t0 + a.per_part : a.T;
+    if (LOSS && !a.inline_count) wait_for_primary();  // the counts
     if (LOSS && a.inline_count) {
         if (threadIdx.x == 0) *a.done = 0;
         count_tokens(a, g, part, t0, t1, reinterpret_cast<int32_t*>(sm));
@@ -376,12 +377,13 @@ lce_status_t bal_pass_form(BalArgs a, BalMode mode, cudaStream_t s) {
     a.per_part = (a.T + a.parts - 1) / a.parts;
     const dim3 grid(a.parts, a.G);
     const size_t smem = static_cast<size_t>(a.E) * 4 * (a.inline_count ? BAL_WARPS : 1);
-    if (mode == BAL_FORWARD)
-        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FORWARD><<<grid, BAL_THREADS, smem, s>>>(a));
-    else if (mode == BAL_BACKWARD)
-        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_BACKWARD><<<grid, BAL_THREADS, smem, s>>>(a));
+    auto kernel = mode == BAL_FORWARD    ? bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FORWARD>
+                  : mode == BAL_BACKWARD ? bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_BACKWARD>
+                                         : bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FUSED>;
+    if (mode == BAL_BACKWARD || a.inline_count)
+        LCE_PROFILED(kernel<<<grid, BAL_THREADS, smem, s>>>(a));
     else
-        LCE_PROFILED(bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FUSED><<<grid, BAL_THREADS, smem, s>>>(a));
+        LCE_PROFILED(launch_after(kernel, grid, BAL_THREADS, smem, s, a));
     return LCE_OK;
 }
 

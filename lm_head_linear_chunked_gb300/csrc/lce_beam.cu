@@ -22,13 +22,15 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int SCAN_THREADS = 256;
-constexpr int SCAN_PER = 32;                          // elements of a chunk per thread
-constexpr int SCAN_CHUNK = SCAN_THREADS * SCAN_PER;   // 8192
+constexpr int SCAN_WARPS = SCAN_THREADS / 32;
 constexpr int SCAN_CAP = 1024;                        // keys the buffer holds beside the list
 constexpr int SCAN_HIGH = 256;                        // keys that start a merge
 constexpr int SCAN_SEGS_MAX = 32;                     // parts of a row (a lane each in the join)
 constexpr int64_t SCAN_BLOCKS = 608;                  // blocks that fill the GPU
+constexpr int JOIN_WARPS = 8;
 constexpr int MAX_M = LCE_BEAM_MAX;
+constexpr int JOIN_SMEM_MAX = MAX_M * 8 * (2 * MAX_M + JOIN_WARPS * SCAN_SEGS_MAX);
+static_assert(JOIN_SMEM_MAX <= 224 * 1024, "dynamic shared memory of a block");
 
 // Logits as the selection sees them: NaN as -inf, +inf as the largest finite.
 __device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
@@ -46,23 +48,53 @@ __device__ __forceinline__ float key_logit(uint64_t key) {
 
 __device__ __forceinline__ uint32_t key_token(uint64_t key) { return 0xFFFFFFFFu - static_cast<uint32_t>(key); }
 
+// The largest of the warp's keys, by its two halves.
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+    const uint32_t h = static_cast<uint32_t>(v >> 32);
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, h);
+    const uint32_t low = __reduce_max_sync(0xFFFFFFFFu, h == top ? static_cast<uint32_t>(v) : 0u);
+    return (static_cast<uint64_t>(top) << 32) | low;
+}
+
+// A sum in two floats: the exact error of each addition of the first goes to
+// the second.  FP64 adds run at 1/64 of the rate here.
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ void add(float x, float x_lo = 0.f) {
+        const float t = hi + x, back = t - hi;
+        lo += ((hi - (t - back)) + (x - back)) + x_lo;
+        hi = t;
+    }
+    __device__ __forceinline__ void scale(float f) {
+        const float h = hi * f;
+        lo = fmaf(lo, f, fmaf(hi, f, -h));
+        hi = h;
+    }
+    // The sum over the warp, in every lane.
+    __device__ __forceinline__ void over_warp() {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            add(__shfl_xor_sync(0xFFFFFFFFu, hi, o), __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+    }
+};
+
 struct ScanArgs {
     const void* z;
     int64_t ld;
     const uint8_t* finished;  // [rows], nullable
     int32_t V, M, segs, per_seg;  // per_seg: chunks of a segment
     float* seg_m;      // [rows, segs]
-    double* seg_s;
+    float2* seg_s;     // the sum relative to seg_m, in two floats
     uint64_t* seg_key;  // [rows, segs, M], sorted down; 0: no candidate
 };
 
 struct ScanShared {
-    uint64_t buf[MAX_M + SCAN_CAP];  // the list's keys, then the new ones
+    alignas(16) uint64_t buf[MAX_M + SCAN_CAP + 2];  // the list's keys, then the new ones
     uint64_t lane_key[SCAN_THREADS];
-    uint64_t tau;
-    double red_s[SCAN_THREADS / 32];
-    float red_m[SCAN_THREADS / 32];
-    uint64_t red_k[SCAN_THREADS / 32];
+    unsigned long long tau;
+    float2 red_s[SCAN_WARPS];
+    float red_m[SCAN_WARPS];
+    uint64_t red_k[SCAN_WARPS];
     int n;
 };
 
@@ -70,6 +102,8 @@ struct ScanShared {
 // there are.  A key's place is the number of larger ones.
 __device__ int keep_best(ScanShared& sh, int n, int M) {
     constexpr int PER = (MAX_M + SCAN_CAP + SCAN_THREADS - 1) / SCAN_THREADS;
+    if (threadIdx.x == 0) sh.buf[n] = 0;  // read with the last key of an odd number
+    __syncthreads();
     uint64_t key[PER];
     int rank[PER];
 #pragma unroll
@@ -79,64 +113,108 @@ __device__ int keep_best(ScanShared& sh, int n, int M) {
         if (q * SCAN_THREADS < n && i < n) {
             key[q] = sh.buf[i];
             int r = 0;
-            for (int j = 0; j < n; ++j) r += sh.buf[j] > key[q];
+#pragma unroll 4
+            for (int j = 0; j < n; j += 2) {
+                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(sh.buf + j);
+                r += (k.x > key[q]) + (k.y > key[q]);
+            }
             rank[q] = r;
         }
     }
     __syncthreads();
+    if (n > M) n = M;
 #pragma unroll
     for (int q = 0; q < PER; ++q)
         if (rank[q] < M) sh.buf[rank[q]] = key[q];
+    if (threadIdx.x == 0) sh.n = n;
     __syncthreads();
-    return n < M ? n : M;
-}
-
-__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        v = u > v ? u : v;
-    }
-    return v;
+    return n;
 }
 
 // One thread's elements of a chunk: vector u holds the tokens
 // first + (u * SCAN_THREADS + thread) * VEC + j.  The places do not depend on
 // the alignment, so equal rows give equal sums.
-template <typename T>
-struct Chunk {
-    static constexpr int VEC = vec16<T>();
-    static constexpr int N = SCAN_PER / VEC;
-    Vec<T, VEC> v[N];
+template <typename T, int PER>
+struct Chunk : RowVectors<T, vec16<T>(), PER / vec16<T>()> {
+    static constexpr int VEC = vec16<T>(), N = PER / VEC;
+    using Base = RowVectors<T, VEC, N>;
+    using Base::v;
 
     static __device__ __forceinline__ uint32_t token(uint32_t first, int i) {
         return first + ((i / VEC) * SCAN_THREADS + threadIdx.x) * VEC + i % VEC;
     }
     __device__ __forceinline__ float at(int i) const { return v[i / VEC].f(i % VEC); }
-    __device__ __forceinline__ void load(const T* row, uint32_t first, uint32_t V, bool vec) {
+    // `shift`: bytes of the row's start past a 16-byte boundary.  A vector of
+    // such a row is cut out of the two that it lies in, where these lie in
+    // the row; at its ends, and past them (-inf), elements are read singly.
+    __device__ __forceinline__ void load(const T* row, uint32_t first, uint32_t V, uint32_t shift) {
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const uint32_t t = token(first, u * VEC);
-            if (vec && t + VEC <= V) {
-                v[u] = *reinterpret_cast<const Vec<T, VEC>*>(row + t);
+            const char* p = reinterpret_cast<const char*>(row + t);
+            if (shift == 0 && t + VEC <= V) {
+                v[u] = *reinterpret_cast<const Vec<T, VEC>*>(p);
+            } else if (shift && t >= VEC && t + 2 * VEC <= V) {
+                const uint4 a = *reinterpret_cast<const uint4*>(p - shift);
+                const uint4 b = *reinterpret_cast<const uint4*>(p - shift + 16);
+                uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                if (shift & 8)
+#pragma unroll
+                    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+                if (shift & 4)
+#pragma unroll
+                    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+                if (sizeof(T) == 2 && (shift & 2))
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+                __builtin_memcpy(&v[u], w, 16);
             } else {
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) v[u].v[j] = t + j < V ? row[t + j] : from_f32<T>(-INFINITY);
             }
         }
     }
+    // The largest logit as read (NaN only if all are).
+    __device__ __forceinline__ float largest() const {
+        if constexpr (sizeof(T) == 2) {
+            return this->max();
+        } else {
+            float m = v[0].v[0];
+#pragma unroll
+            for (int i = 1; i < PER; ++i) m = fmaxf(m, at(i));
+            return m;
+        }
+    }
+    // The sum of e^(x - m).
+    __device__ __forceinline__ float sum(float m) const {
+        F2 s0 = f2(0.f), s1 = f2(0.f);
+        const F2 m2 = f2(-m), l2 = f2(LOG2E);
+#pragma unroll
+        for (int p = 0; p < PER / 2; p += 2) {
+            const F2 a = mul2(add2(this->pair(p), m2), l2), b = mul2(add2(this->pair(p + 1), m2), l2);
+            s0 = add2(s0, f2(fast_exp2(lce::lo(a)), fast_exp2(lce::hi(a))));
+            s1 = add2(s1, f2(fast_exp2(lce::lo(b)), fast_exp2(lce::hi(b))));
+        }
+        s0 = add2(s0, s1);
+        const float s = lce::lo(s0) + lce::hi(s0);
+        if (s < INFINITY) return s;
+        float c = 0.f;  // a NaN or an infinity among them
+#pragma unroll
+        for (int i = 0; i < PER; ++i) c += fast_exp2((clean(at(i)) - m) * LOG2E);
+        return c;
+    }
 };
 
 // The M best of the chunk's own elements by rounds of a block-wide maximum,
 // appended to the buffer: for chunks whose candidates overflow it.
-template <typename T>
-__device__ void best_by_rounds(ScanShared& sh, const Chunk<T>& c, uint32_t first, uint32_t V, int M, int n) {
+template <typename T, int PER>
+__device__ void best_by_rounds(ScanShared& sh, const Chunk<T, PER>& c, uint32_t first, uint32_t V, int M, int n) {
     uint64_t below = ~0ull;
     for (int r = 0; r < M; ++r) {
         uint64_t best = 0;
 #pragma unroll
-        for (int i = 0; i < SCAN_PER; ++i) {
-            const uint32_t t = Chunk<T>::token(first, i);
+        for (int i = 0; i < PER; ++i) {
+            const uint32_t t = c.token(first, i);
             const uint64_t k = t < V ? logit_key(c.at(i), t) : 0;
             if (k < below && k > best) best = k;
         }
@@ -144,72 +222,79 @@ __device__ void best_by_rounds(ScanShared& sh, const Chunk<T>& c, uint32_t first
         __syncthreads();
         if ((threadIdx.x & 31) == 0) sh.red_k[threadIdx.x >> 5] = best;
         __syncthreads();
-        for (int w = 0; w < SCAN_THREADS / 32; ++w) best = sh.red_k[w] > best ? sh.red_k[w] : best;
+        for (int w = 0; w < SCAN_WARPS; ++w) best = sh.red_k[w] > best ? sh.red_k[w] : best;
         if (threadIdx.x == 0) sh.buf[n + r] = best;
         below = best;
     }
     __syncthreads();
 }
 
-template <typename T>
+template <typename T, int PER>
 __global__ void __launch_bounds__(SCAN_THREADS) beam_scan_kernel(ScanArgs a) {
+    constexpr uint32_t CHUNK = SCAN_THREADS * PER;
     __shared__ ScanShared sh;
+    launch_dependents();
     const int64_t row = blockIdx.y;
     const int seg = blockIdx.x;
     if (a.finished && a.finished[row]) return;  // the join does not read its parts
     const T* z = static_cast<const T*>(a.z) + row * a.ld;
-    const bool vec = aligned_dev(z);
+    const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z) & 15u);
     const uint32_t V = static_cast<uint32_t>(a.V);
-    const uint64_t begin = static_cast<uint64_t>(seg) * a.per_seg * SCAN_CHUNK;
-    uint64_t end = begin + static_cast<uint64_t>(a.per_seg) * SCAN_CHUNK;
+    const uint64_t begin = static_cast<uint64_t>(seg) * a.per_seg * CHUNK;
+    uint64_t end = begin + static_cast<uint64_t>(a.per_seg) * CHUNK;
     if (end > V) end = V;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int n = 0;        // keys in the buffer (all threads agree)
+    int n = 0;         // keys in the buffer (all threads agree)
     uint64_t tau = 0;  // the M-th best so far, 0 while there are fewer
     float m = -INFINITY;
-    double s = 0.0;
-    for (uint64_t first64 = begin; first64 < end; first64 += SCAN_CHUNK) {
+    Sum2 s{0.f, 0.f};
+    if (threadIdx.x == 0) sh.n = 0;
+    for (uint64_t first64 = begin; first64 < end; first64 += CHUNK) {
         const uint32_t first = static_cast<uint32_t>(first64);
-        Chunk<T> c;
-        c.load(z, first, V, vec);
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < SCAN_PER; ++i) mx = fmaxf(mx, clean(c.at(i)));
+        Chunk<T, PER> c;
+        c.load(z, first, V, shift);
+        const float raw = c.largest(), mx = clean(raw);
         const float m2 = fmaxf(m, mx);
         if (m2 > -INFINITY) {
-            float part = 0.f;
-#pragma unroll
-            for (int i = 0; i < SCAN_PER; ++i) part += exp2f((clean(c.at(i)) - m2) * LOG2E);
-            s = s * static_cast<double>(exp2f((m - m2) * LOG2E)) + static_cast<double>(part);
+            if (m2 > m) s.scale(fast_exp2((m - m2) * LOG2E));  // of nothing at first
+            s.add(c.sum(m2));
             m = m2;
         }
-        // candidates: in a part's first chunk those not below the M-th largest of the
-        // threads' maxima, later those above the M-th best so far (a later
+        // candidates: in a part's first chunk those not below the M-th largest of some
+        // threads' maxima (of the best warp's for few results, which takes an eighth of the
+        // comparisons of all threads'), later those above the M-th best so far (a later
         // token loses against an equal one)
         uint64_t limit = tau;
         if (tau == 0) {
-            uint64_t k = 0;
+            int at = 0;
+            if (mx > -INFINITY)
 #pragma unroll
-            for (int i = 0; i < SCAN_PER; ++i) {
-                const uint32_t t = Chunk<T>::token(first, i);
-                const uint64_t q = t < V ? logit_key(c.at(i), t) : 0;
-                k = q > k ? q : k;
-            }
+                for (int i = PER - 1; i >= 0; --i) at = c.at(i) >= raw ? i : at;
+            const uint32_t t = first + ((at / c.VEC) * SCAN_THREADS + threadIdx.x) * c.VEC + at % c.VEC;
+            const uint64_t k = t < V ? logit_key(mx, t) : 0;
             sh.lane_key[threadIdx.x] = k;
             if (threadIdx.x == 0) sh.tau = 1;  // fewer than M threads with elements: all pass
             __syncthreads();
             int rank = 0;
-            for (int j = 0; j < SCAN_THREADS; ++j) rank += sh.lane_key[j] > k;
-            if (rank == a.M - 1 && k) sh.tau = k;
+            if (a.M <= 16) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) rank += sh.lane_key[warp * 32 + j] > k;
+            } else {
+#pragma unroll 8
+                for (int j = 0; j < SCAN_THREADS; ++j) rank += sh.lane_key[j] > k;
+            }
+            if (rank == a.M - 1 && k) atomicMax(&sh.tau, k);
             __syncthreads();
             limit = sh.tau - 1;
         }
-        if (threadIdx.x == 0) sh.n = n;
-        __syncthreads();
+        // (the barrier also puts the count of the chunk before it ahead of the pushes)
+        if (!__syncthreads_or(logit_key(mx, 0) > limit)) continue;
         if (logit_key(mx, 0) > limit) {
+            const float least = key_logit(limit + 1);
 #pragma unroll
-            for (int i = 0; i < SCAN_PER; ++i) {
-                const uint32_t t = Chunk<T>::token(first, i);
+            for (int i = 0; i < PER; ++i) {
+                if (!(clean(c.at(i)) >= least) && limit) continue;
+                const uint32_t t = c.token(first, i);
                 const uint64_t k = t < V ? logit_key(c.at(i), t) : 0;
                 if (k > limit) {
                     const int at = atomicAdd(&sh.n, 1);
@@ -219,20 +304,20 @@ __global__ void __launch_bounds__(SCAN_THREADS) beam_scan_kernel(ScanArgs a) {
         }
         __syncthreads();
         const int total = sh.n;
-        __syncthreads();
         if (total > MAX_M + SCAN_CAP) {
             n = keep_best(sh, n, a.M);
-            best_by_rounds<T>(sh, c, first, V, a.M, n);
+            best_by_rounds<T, PER>(sh, c, first, V, a.M, n);
             n += a.M;
         } else {
             n = total;
         }
-        if (n > SCAN_HIGH || tau == 0) {
+        if (total > MAX_M + SCAN_CAP || n > SCAN_HIGH || tau == 0) {
             n = keep_best(sh, n, a.M);
             if (n == a.M) tau = sh.buf[n - 1];
         }
     }
-    n = keep_best(sh, n, a.M);
+    __syncthreads();
+    if (n > 0) n = keep_best(sh, n, a.M);
     const int64_t part = row * a.segs + seg;
     for (int i = threadIdx.x; i < a.M; i += SCAN_THREADS) a.seg_key[part * a.M + i] = i < n ? sh.buf[i] : 0;
     // the block's maximum and sum
@@ -241,23 +326,22 @@ __global__ void __launch_bounds__(SCAN_THREADS) beam_scan_kernel(ScanArgs a) {
     for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
     if (lane == 0) sh.red_m[warp] = bm;
     __syncthreads();
-    for (int w = 0; w < SCAN_THREADS / 32; ++w) bm = fmaxf(bm, sh.red_m[w]);
-    double bs = m > -INFINITY ? s * static_cast<double>(exp2f((m - bm) * LOG2E)) : 0.0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) bs += __shfl_xor_sync(0xFFFFFFFFu, bs, o);
-    if (lane == 0) sh.red_s[warp] = bs;
+    for (int w = 0; w < SCAN_WARPS; ++w) bm = fmaxf(bm, sh.red_m[w]);
+    if (m > -INFINITY && m < bm) s.scale(fast_exp2((m - bm) * LOG2E));
+    s.over_warp();
+    if (lane == 0) sh.red_s[warp] = make_float2(s.hi, s.lo);
     __syncthreads();
     if (threadIdx.x == 0) {
-        bs = 0.0;
-        for (int w = 0; w < SCAN_THREADS / 32; ++w) bs += sh.red_s[w];
+        Sum2 b{0.f, 0.f};
+        for (int w = 0; w < SCAN_WARPS; ++w) b.add(sh.red_s[w].x, sh.red_s[w].y);
         a.seg_m[part] = bm;
-        a.seg_s[part] = bs;
+        a.seg_s[part] = make_float2(b.hi, b.lo);
     }
 }
 
 struct JoinArgs {
     const float* seg_m;
-    const double* seg_s;
+    const float2* seg_s;
     const uint64_t* seg_key;
     const float* scores;      // [B, K]
     const uint8_t* finished;  // [B, K], nullable
@@ -268,95 +352,112 @@ struct JoinArgs {
     uint8_t* out_finished;    // nullable
 };
 
-// Doubles as integers in the same order (no NaN comes here).
+// Doubles as integers in the same order (no NaN comes here), and back.
 __device__ __forceinline__ uint64_t ordered(double x) {
     const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
     return b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
 }
+__device__ __forceinline__ double from_ordered(uint64_t o) {
+    return __longlong_as_double(static_cast<long long>((o >> 63) ? (o ^ 0x8000000000000000ull) : ~o));
+}
 
 // One block per item: a warp per beam adds its parts up and merges their
-// lists, then the first warp merges the beams, a lane holding the beams l and
-// l + 32.
-__global__ void __launch_bounds__(256) beam_join_kernel(JoinArgs a) {
-    extern __shared__ uint64_t keys[];  // [K, M] per beam, sorted down
-    __shared__ double base[MAX_M];      // score - ln(sum)
+// lists; then all scores are computed, and the first warp merges the beams, a
+// lane holding the beams l and l + 32.  A merge takes the largest head M times.
+__global__ void __launch_bounds__(32 * JOIN_WARPS) beam_join_kernel(JoinArgs a) {
+    extern __shared__ uint64_t dyn[];
+    uint64_t* keys = dyn;                // [K, M] per beam, sorted down
+    uint64_t* score = dyn + a.K * a.M;   // [K, M] as ordered integers, 0: no candidate
+    uint64_t* lists = score + a.K * a.M;  // [JOIN_WARPS, segs, M]
+    __shared__ double base[MAX_M];       // score - ln(sum)
     __shared__ float top[MAX_M];
+    __shared__ float2 sums[MAX_M];
+    __shared__ bool ended[MAX_M];
     const int64_t b = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int k = warp; k < a.K; k += 8) {
+    wait_for_primary();
+    for (int k = warp; k < a.K; k += JOIN_WARPS) {
         const int64_t row = b * a.K + k;
-        float score = a.scores[row];
-        if (!(score == score)) score = -INFINITY;
-        if (a.finished && a.finished[row]) {
-            if (lane == 0) base[k] = score;
-            continue;
+        const bool over = a.finished && a.finished[row];
+        if (lane == 0) {
+            ended[k] = over;
+            top[k] = 0.f;
+            sums[k] = make_float2(1.f, 0.f);
         }
-        const int64_t part = row * a.segs + lane;
+        if (over) continue;
+        uint64_t* list = lists + warp * a.segs * a.M;
+        const uint64_t* from = a.seg_key + row * a.segs * a.M;
+        for (int i = lane; i < a.segs * a.M; i += 32) list[i] = from[i];
         const bool have = lane < a.segs;
-        const float m = have ? a.seg_m[part] : -INFINITY;
+        const float m = have ? a.seg_m[row * a.segs + lane] : -INFINITY;
+        const float2 ms = have ? a.seg_s[row * a.segs + lane] : make_float2(0.f, 0.f);
         float bm = m;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
-        double s = have && m > -INFINITY ? a.seg_s[part] * exp(static_cast<double>(m) - static_cast<double>(bm)) : 0.0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        Sum2 s{ms.x, ms.y};
+        if (!(m > -INFINITY))
+            s = Sum2{0.f, 0.f};
+        else if (m < bm)
+            s.scale(fast_exp2((m - bm) * LOG2E));
+        s.over_warp();
         if (lane == 0) {
-            base[k] = bm > -INFINITY ? static_cast<double>(score) - log(s) : -INFINITY;
             top[k] = bm;
+            sums[k] = make_float2(s.hi, s.lo);
         }
-        // each lane holds the head of its part's list; the largest leaves
-        int at = 0;
-        uint64_t head = have ? a.seg_key[part * a.M] : 0;
+        __syncwarp();
+        int at = lane * a.M;
+        const int stop = at + a.M;
+        uint64_t head = have ? list[at] : 0;
         for (int r = 0; r < a.M; ++r) {
             const uint64_t best = warp_max(head);
             if (lane == 0) keys[k * a.M + r] = best;
-            if (head == best && best) {
-                ++at;
-                head = at < a.M ? a.seg_key[part * a.M + at] : 0;
-            }
+            if (head == best && best) head = ++at < stop ? list[at] : 0;
         }
+        __syncwarp();
+    }
+    __syncthreads();
+    // one logarithm per beam, in FP64
+    if (threadIdx.x < a.K) {
+        float sc = a.scores[b * a.K + threadIdx.x];
+        if (!(sc == sc)) sc = -INFINITY;
+        const float2 v = sums[threadIdx.x];
+        base[threadIdx.x] = ended[threadIdx.x]           ? static_cast<double>(sc)
+                            : top[threadIdx.x] > -INFINITY ? sc - log(static_cast<double>(v.x) + v.y)
+                                                           : -INFINITY;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.K * a.M; i += 32 * JOIN_WARPS) {
+        const int k = i / a.M, r = i - k * a.M;
+        uint64_t o = 0;
+        if (ended[k]) {
+            if (r < a.V) o = ordered(r == 0 ? base[k] : -INFINITY);
+        } else if (const uint64_t key = keys[i]) {
+            const float x = key_logit(key);
+            o = ordered(x > -INFINITY ? base[k] + (static_cast<double>(x) - static_cast<double>(top[k])) : -INFINITY);
+        }
+        score[i] = o;
     }
     __syncthreads();
     if (warp != 0) return;
-    // (score as an integer, 0 when the beam has no more candidates)
-    auto candidate = [&](int k, int r, double* score, int64_t* token) -> uint64_t {
-        if (k >= a.K || r >= a.M) return 0;
-        if (a.finished && a.finished[b * a.K + k]) {
-            if (r >= a.V) return 0;
-            *score = r == 0 ? base[k] : -INFINITY;
-            *token = a.pad;
-            return ordered(*score);
-        }
-        const uint64_t key = keys[k * a.M + r];
-        if (!key) return 0;
-        const float x = key_logit(key);
-        *score = x > -INFINITY ? base[k] + (static_cast<double>(x) - static_cast<double>(top[k])) : -INFINITY;
-        *token = key_token(key);
-        return ordered(*score);
-    };
-    int at0 = 0, at1 = 0;
-    double s0 = 0.0, s1 = 0.0;
-    int64_t t0 = 0, t1 = 0;
-    uint64_t k0 = candidate(lane, 0, &s0, &t0), k1 = candidate(lane + 32, 0, &s1, &t1);
+    int at0 = lane * a.M, at1 = (lane + 32) * a.M;
+    const int stop0 = at0 + a.M, stop1 = at1 + a.M;
+    uint64_t k0 = lane < a.K ? score[at0] : 0, k1 = lane + 32 < a.K ? score[at1] : 0;
     for (int r = 0; r < a.M; ++r) {
-        const uint64_t mine = k1 > k0 ? k1 : k0;
-        const uint64_t best = warp_max(mine);
+        const uint64_t best = warp_max(k1 > k0 ? k1 : k0);
         // the lowest beam among equals: the lanes' first beams before their second ones
         const unsigned has0 = __ballot_sync(0xFFFFFFFFu, k0 == best), has1 = __ballot_sync(0xFFFFFFFFu, k1 == best);
         const bool first = has0 != 0;
-        const int winner = __ffs(first ? has0 : has1) - 1;
-        if (lane == winner) {
-            const int k = first ? lane : lane + 32;
-            const int64_t token = first ? t0 : t1, o = b * a.M + r;
-            a.out_scores[o] = static_cast<float>(first ? s0 : s1);
+        if (lane == __ffs(first ? has0 : has1) - 1) {
+            const int k = first ? lane : lane + 32, at = first ? at0 : at1;
+            const int64_t token = ended[k] ? a.pad : static_cast<int64_t>(key_token(keys[at])), o = b * a.M + r;
+            a.out_scores[o] = static_cast<float>(from_ordered(best));
             a.out_tokens[o] = token;
             a.out_parents[o] = k;
-            if (a.out_finished)
-                a.out_finished[o] = (a.finished && a.finished[b * a.K + k]) || (a.eos >= 0 && token == a.eos);
+            if (a.out_finished) a.out_finished[o] = ended[k] || (a.eos >= 0 && token == a.eos);
             if (first)
-                k0 = candidate(lane, ++at0, &s0, &t0);
+                k0 = ++at0 < stop0 ? score[at0] : 0;
             else
-                k1 = candidate(lane + 32, ++at1, &s1, &t1);
+                k1 = ++at1 < stop1 ? score[at1] : 0;
         }
     }
 }
@@ -439,21 +540,25 @@ lce_status_t beam_sizes(int64_t items, int64_t K, int64_t V, int64_t M) {
 }
 
 struct BeamPlan {
+    bool small;  // chunks of 2048 tokens, not 8192
     int32_t segs, per_seg;
-    size_t off_s, off_m, off_key, total;
+    size_t off_m, off_key, total;
 };
 
+// A row's chunks and how they are shared out.  With few rows, chunks of 2048
+// tokens spread the work over four times the blocks (one request of four beams
+// over 32768 tokens: 64 blocks, not 16).
 BeamPlan beam_plan(int64_t rows, int64_t V, int64_t M) {
     BeamPlan p;
-    const int64_t chunks = (V + SCAN_CHUNK - 1) / SCAN_CHUNK;
+    p.small = rows * ((V + 8191) / 8192) < SCAN_BLOCKS / 4;
+    const int64_t chunk = p.small ? 2048 : 8192, chunks = (V + chunk - 1) / chunk;
     int64_t segs = (SCAN_BLOCKS + rows - 1) / rows;
     if (segs > SCAN_SEGS_MAX) segs = SCAN_SEGS_MAX;
     if (segs > chunks) segs = chunks;
     p.per_seg = static_cast<int32_t>((chunks + segs - 1) / segs);
     p.segs = static_cast<int32_t>((chunks + p.per_seg - 1) / p.per_seg);
     const size_t n = static_cast<size_t>(rows) * p.segs;
-    p.off_s = 1024;
-    p.off_m = p.off_s + n * 8;
+    p.off_m = 1024 + n * 8;
     p.off_key = (p.off_m + n * 4 + 255) / 256 * 256;
     p.total = p.off_key + n * M * 8;
     return p;
@@ -488,22 +593,29 @@ lce_status_t lce_beam_select(int64_t items, int64_t beams, int64_t V, int64_t n_
     if (ws_bytes < p.total) return LCE_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* w = static_cast<uint8_t*>(ws);
+    float2* seg_s = reinterpret_cast<float2*>(w + 1024);
     float* seg_m = reinterpret_cast<float*>(w + p.off_m);
-    double* seg_s = reinterpret_cast<double*>(w + p.off_s);
     uint64_t* seg_key = reinterpret_cast<uint64_t*>(w + p.off_key);
     const ScanArgs sa{logits, ld, finished, static_cast<int32_t>(V), static_cast<int32_t>(n_out), p.segs, p.per_seg,
                       seg_m, seg_s, seg_key};
     const dim3 grid(p.segs, static_cast<unsigned>(items * beams));
     const lce_status_t sc = with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);
-        LCE_PROFILED(beam_scan_kernel<T><<<grid, SCAN_THREADS, 0, s>>>(sa));
+        if (p.small)
+            LCE_PROFILED(beam_scan_kernel<T, 8><<<grid, SCAN_THREADS, 0, s>>>(sa));
+        else
+            LCE_PROFILED(beam_scan_kernel<T, 32><<<grid, SCAN_THREADS, 0, s>>>(sa));
         return LCE_OK;
     });
     if (sc != LCE_OK) return sc;
     const JoinArgs ja{seg_m, seg_s, seg_key, scores, finished, static_cast<int32_t>(beams), static_cast<int32_t>(n_out),
                       p.segs, static_cast<int32_t>(V), pad_token, eos_token, out_scores, out_tokens, out_parents,
                       out_finished};
-    LCE_PROFILED(beam_join_kernel<<<static_cast<unsigned>(items), 256, static_cast<size_t>(beams) * n_out * 8, s>>>(ja));
+    const size_t smem = static_cast<size_t>(n_out) * 8 * (2 * beams + JOIN_WARPS * p.segs);
+    if (smem > 40 * 1024 && cudaFuncSetAttribute(beam_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 JOIN_SMEM_MAX) != cudaSuccess)
+        return LCE_ERR_CUDA;
+    LCE_PROFILED(launch_after(beam_join_kernel, dim3(static_cast<unsigned>(items)), 32 * JOIN_WARPS, smem, s, ja));
     return LCE_OK;
 }
 

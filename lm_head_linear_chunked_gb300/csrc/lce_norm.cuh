@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_bwd_rows(NormBwd<T> a) 
     extern __shared__ __align__(16) uint8_t dyn[];  // the ring, then (WARP) the sums of the columns
     using Row = RowRegs<T, VEC, ITEMS>;
     using V = Vec<T, VEC>;
+    launch_dependents();
     constexpr bool RING = sizeof(V) >= 4;  // single 16-bit elements are read when they are needed
     static_assert(KEEP || RING, "the rows are read again from the ring");
     const int tpr = WARP ? 32 : blockDim.x;
@@ -537,24 +538,29 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_bwd_rows(NormBwd<T> a) 
 }
 
 // Adds the parts' column sums in a fixed order: 32 columns per block, 32
-// threads a column with up to four parts of each in flight.
+// threads a column with up to eight parts of each in flight.
+struct JoinArgs {
+    const float *part_w, *part_b;
+    int32_t parts, H;
+    void *dw, *db;  // each nullable
+};
 template <typename W>
-__global__ void __launch_bounds__(1024) norm_dw_join(const float* part_w, const float* part_b, int parts, int32_t H,
-                                                     W* dw, W* db) {
+__global__ void __launch_bounds__(1024) norm_dw_join(JoinArgs a) {
     __shared__ float s[32][33];
     const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + c;
-    const float* p = blockIdx.y ? part_b : part_w;
-    W* out = blockIdx.y ? db : dw;
+    const float* p = blockIdx.y ? a.part_b : a.part_w;
+    W* out = static_cast<W*>(blockIdx.y ? a.db : a.dw);
     if (!out) return;
+    wait_for_primary();
     float v = 0.f;
-    if (col < H)
-#pragma unroll 4
-        for (int j = k; j < parts; j += 32) v += p[static_cast<int64_t>(j) * H + col];
+    if (col < a.H)
+#pragma unroll 8
+        for (int j = k; j < a.parts; j += 32) v += p[static_cast<int64_t>(j) * a.H + col];
     s[k][c] = v;
     __syncthreads();
     v = warp_sum(s[c][k]);  // column k of this block
-    if (c == 0 && blockIdx.x * 32 + k < H) out[blockIdx.x * 32 + k] = from_f32<W>(v);
+    if (c == 0 && blockIdx.x * 32 + k < a.H) out[blockIdx.x * 32 + k] = from_f32<W>(v);
 }
 
 // Blocks of `kernel` that stay on the current device at once, after raising
@@ -713,8 +719,8 @@ lce_status_t norm_backward(const NormCall& c) {
         }
     }
     if (st != LCE_OK || !sums) return st;
-    LCE_PROFILED(norm_dw_join<W><<<dim3((c.H + 31) / 32, 2), 1024, 0, s>>>(a.part_w, a.part_b, parts, c.H,
-                                                                            static_cast<W*>(c.dw), static_cast<W*>(c.db)));
+    LCE_PROFILED(launch_after(norm_dw_join<W>, dim3((c.H + 31) / 32, 2), 1024, 0, s,
+                              JoinArgs{a.part_w, a.part_b, parts, c.H, c.dw, c.db}));
     return LCE_OK;
 }
 
