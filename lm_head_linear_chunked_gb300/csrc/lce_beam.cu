@@ -90,8 +90,6 @@ struct ScanArgs {
 
 struct ScanShared {
     alignas(16) uint64_t buf[MAX_M + SCAN_CAP + 2];  // the list's keys, then the new ones
-    uint64_t lane_key[SCAN_THREADS];
-    unsigned long long tau;
     float2 red_s[SCAN_WARPS];
     float red_m[SCAN_WARPS];
     uint64_t red_k[SCAN_WARPS];
@@ -144,34 +142,48 @@ struct Chunk : RowVectors<T, vec16<T>(), PER / vec16<T>()> {
         return first + ((i / VEC) * SCAN_THREADS + threadIdx.x) * VEC + i % VEC;
     }
     __device__ __forceinline__ float at(int i) const { return v[i / VEC].f(i % VEC); }
-    // `shift`: bytes of the row's start past a 16-byte boundary.  A vector of
-    // such a row is cut out of the two that it lies in, where these lie in
-    // the row; at its ends, and past them (-inf), elements are read singly.
-    __device__ __forceinline__ void load(const T* row, uint32_t first, uint32_t V, uint32_t shift) {
+    // A vector of a row that starts SHIFT bytes past a 16-byte boundary, cut
+    // out of the two that it lies in.
+    template <int SHIFT>
+    static __device__ __forceinline__ Vec<T, VEC> cut(const char* p) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p - SHIFT);
+        const uint4 b = *reinterpret_cast<const uint4*>(p - SHIFT + 16);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = SHIFT % 4 ? __funnelshift_r(w[k + SHIFT / 4], w[k + SHIFT / 4 + 1], SHIFT % 4 * 8) : w[k + SHIFT / 4];
+        Vec<T, VEC> r;
+        __builtin_memcpy(&r, o, 16);
+        return r;
+    }
+    // The chunk's vectors; at the ends of an unaligned row, and past the end of
+    // any (-inf), elements are read singly.
+    template <int SHIFT>
+    __device__ __forceinline__ void load_from(const T* row, uint32_t first, uint32_t V) {
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const uint32_t t = token(first, u * VEC);
             const char* p = reinterpret_cast<const char*>(row + t);
-            if (shift == 0 && t + VEC <= V) {
+            if (SHIFT == 0 && t + VEC <= V)
                 v[u] = *reinterpret_cast<const Vec<T, VEC>*>(p);
-            } else if (shift && t >= VEC && t + 2 * VEC <= V) {
-                const uint4 a = *reinterpret_cast<const uint4*>(p - shift);
-                const uint4 b = *reinterpret_cast<const uint4*>(p - shift + 16);
-                uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                if (shift & 8)
-#pragma unroll
-                    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
-                if (shift & 4)
-#pragma unroll
-                    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
-                if (sizeof(T) == 2 && (shift & 2))
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
-                __builtin_memcpy(&v[u], w, 16);
-            } else {
+            else if (SHIFT != 0 && t >= VEC && t + 2 * VEC <= V)
+                v[u] = cut<SHIFT>(p);
+            else
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) v[u].v[j] = t + j < V ? row[t + j] : from_f32<T>(-INFINITY);
-            }
+        }
+    }
+    __device__ __forceinline__ void load(const T* row, uint32_t first, uint32_t V, uint32_t shift) {
+        if (shift == 0) return load_from<0>(row, first, V);
+        if (shift == 4) return load_from<4>(row, first, V);
+        if (shift == 8) return load_from<8>(row, first, V);
+        if (shift == 12) return load_from<12>(row, first, V);
+        if constexpr (sizeof(T) == 2) {
+            if (shift == 2) return load_from<2>(row, first, V);
+            if (shift == 6) return load_from<6>(row, first, V);
+            if (shift == 10) return load_from<10>(row, first, V);
+            if (shift == 14) return load_from<14>(row, first, V);
         }
     }
     // The largest logit as read (NaN only if all are).
@@ -230,7 +242,7 @@ __device__ void best_by_rounds(ScanShared& sh, const Chunk<T, PER>& c, uint32_t 
 }
 
 template <typename T, int PER>
-__global__ void __launch_bounds__(SCAN_THREADS) beam_scan_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(SCAN_THREADS, 4) beam_scan_kernel(ScanArgs a) {
     constexpr uint32_t CHUNK = SCAN_THREADS * PER;
     __shared__ ScanShared sh;
     launch_dependents();
@@ -260,10 +272,9 @@ __global__ void __launch_bounds__(SCAN_THREADS) beam_scan_kernel(ScanArgs a) {
             s.add(c.sum(m2));
             m = m2;
         }
-        // candidates: in a part's first chunk those not below the M-th largest of some
-        // threads' maxima (of the best warp's for few results, which takes an eighth of the
-        // comparisons of all threads'), later those above the M-th best so far (a later
-        // token loses against an equal one)
+        // candidates: in a part's first chunk those that are at least as large as the
+        // r-th largest thread's maximum of every warp, r = M / 8 (M of them exist), later
+        // those above the M-th best so far (a later token loses against an equal one)
         uint64_t limit = tau;
         if (tau == 0) {
             int at = 0;
@@ -272,33 +283,35 @@ __global__ void __launch_bounds__(SCAN_THREADS) beam_scan_kernel(ScanArgs a) {
                 for (int i = PER - 1; i >= 0; --i) at = c.at(i) >= raw ? i : at;
             const uint32_t t = first + ((at / c.VEC) * SCAN_THREADS + threadIdx.x) * c.VEC + at % c.VEC;
             const uint64_t k = t < V ? logit_key(mx, t) : 0;
-            sh.lane_key[threadIdx.x] = k;
-            if (threadIdx.x == 0) sh.tau = 1;  // fewer than M threads with elements: all pass
-            __syncthreads();
-            int rank = 0;
-            if (a.M <= 16) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) rank += sh.lane_key[warp * 32 + j] > k;
-            } else {
-#pragma unroll 8
-                for (int j = 0; j < SCAN_THREADS; ++j) rank += sh.lane_key[j] > k;
+            const int r = (a.M + SCAN_WARPS - 1) / SCAN_WARPS;
+            uint64_t below = k, rth = 0;
+            for (int i = 0; i < r; ++i) {
+                rth = warp_max(below);
+                if (below == rth) below = 0;
             }
-            if (rank == a.M - 1 && k) atomicMax(&sh.tau, k);
+            if (lane == 0) sh.red_k[warp] = rth;
             __syncthreads();
-            limit = sh.tau - 1;
+            limit = sh.red_k[0];
+#pragma unroll
+            for (int w = 1; w < SCAN_WARPS; ++w) limit = sh.red_k[w] < limit ? sh.red_k[w] : limit;
+            if (limit) --limit;  // 0, all pass: a warp with fewer than r threads that have elements
         }
         // (the barrier also puts the count of the chunk before it ahead of the pushes)
-        if (!__syncthreads_or(logit_key(mx, 0) > limit)) continue;
-        if (logit_key(mx, 0) > limit) {
+        const bool some = logit_key(mx, 0) > limit;
+        if (!__syncthreads_or(some)) continue;
+        if (some) {
             const float least = key_logit(limit + 1);
+            uint32_t which = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (!(clean(c.at(i)) >= least) && limit) continue;
-                const uint32_t t = c.token(first, i);
-                const uint64_t k = t < V ? logit_key(c.at(i), t) : 0;
+            for (int i = 0; i < PER; ++i) which |= static_cast<uint32_t>(c.at(i) >= least) << i;
+            if (limit == 0) which = (1u << PER) - 1;
+            for (; which; which &= which - 1) {
+                const int i = __ffs(which) - 1;
+                const uint32_t t = first + ((i / c.VEC) * SCAN_THREADS + threadIdx.x) * c.VEC + i % c.VEC;
+                const uint64_t k = t < V ? logit_key(to_f32(z[t]), t) : 0;  // read again: the registers have no index
                 if (k > limit) {
-                    const int at = atomicAdd(&sh.n, 1);
-                    if (at < MAX_M + SCAN_CAP) sh.buf[at] = k;
+                    const int place = atomicAdd(&sh.n, 1);
+                    if (place < MAX_M + SCAN_CAP) sh.buf[place] = k;
                 }
             }
         }
@@ -540,19 +553,19 @@ lce_status_t beam_sizes(int64_t items, int64_t K, int64_t V, int64_t M) {
 }
 
 struct BeamPlan {
-    bool small;  // chunks of 2048 tokens, not 8192
+    bool small;  // chunks of 2048 tokens, not 4096
     int32_t segs, per_seg;
     size_t off_m, off_key, total;
 };
 
 // A row's chunks and how they are shared out.  With few rows, chunks of 2048
-// tokens spread the work over four times the blocks (one request of four beams
-// over 32768 tokens: 64 blocks, not 16).
+// tokens spread the work over twice the blocks (one request of four beams over
+// 32768 tokens: 64 blocks, not 32).
 BeamPlan beam_plan(int64_t rows, int64_t V, int64_t M) {
     BeamPlan p;
-    p.small = rows * ((V + 8191) / 8192) < SCAN_BLOCKS / 4;
-    const int64_t chunk = p.small ? 2048 : 8192, chunks = (V + chunk - 1) / chunk;
-    int64_t segs = (SCAN_BLOCKS + rows - 1) / rows;
+    p.small = rows * ((V + 4095) / 4096) < SCAN_BLOCKS / 4;
+    const int64_t chunk = p.small ? 2048 : 4096, chunks = (V + chunk - 1) / chunk;
+    int64_t segs = rows < SCAN_BLOCKS ? SCAN_BLOCKS / rows : 1;  // one round of blocks
     if (segs > SCAN_SEGS_MAX) segs = SCAN_SEGS_MAX;
     if (segs > chunks) segs = chunks;
     p.per_seg = static_cast<int32_t>((chunks + segs - 1) / segs);
@@ -604,7 +617,7 @@ lce_status_t lce_beam_select(int64_t items, int64_t beams, int64_t V, int64_t n_
         if (p.small)
             LCE_PROFILED(beam_scan_kernel<T, 8><<<grid, SCAN_THREADS, 0, s>>>(sa));
         else
-            LCE_PROFILED(beam_scan_kernel<T, 32><<<grid, SCAN_THREADS, 0, s>>>(sa));
+            LCE_PROFILED(beam_scan_kernel<T, 16><<<grid, SCAN_THREADS, 0, s>>>(sa));
         return LCE_OK;
     });
     if (sc != LCE_OK) return sc;
