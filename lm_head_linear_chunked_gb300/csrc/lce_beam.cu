@@ -23,8 +23,9 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int SCAN_THREADS = 256;
 constexpr int SCAN_WARPS = SCAN_THREADS / 32;
-constexpr int SCAN_CAP = 1024;                        // keys the buffer holds beside the list
-constexpr int SCAN_HIGH = 256;                        // keys that start a merge
+constexpr int SCAN_CAP = 448;                         // keys the buffer holds beside the list
+constexpr int SCAN_HIGH = 128;                        // keys that start a merge
+constexpr int SCAN_STAGES = 3;                        // chunks in shared memory
 constexpr int SCAN_SEGS_MAX = 32;                     // parts of a row (a lane each in the join)
 constexpr int64_t SCAN_BLOCKS = 608;                  // blocks that fill the GPU
 constexpr int JOIN_WARPS = 8;
@@ -93,7 +94,8 @@ struct ScanShared {
     float2 red_s[SCAN_WARPS];
     float red_m[SCAN_WARPS];
     uint64_t red_k[SCAN_WARPS];
-    int n;
+    int n;     // keys in the buffer, or more where they overflowed it
+    int kept;  // of them from before the last chunk with candidates
 };
 
 // Keeps the M largest of buf[0..n) at its front, sorted down; returns how many
@@ -129,105 +131,104 @@ __device__ int keep_best(ScanShared& sh, int n, int M) {
     return n;
 }
 
-// One thread's elements of a chunk: vector u holds the tokens
-// first + (u * SCAN_THREADS + thread) * VEC + j.  The places do not depend on
-// the alignment, so equal rows give equal sums.
-template <typename T, int PER>
-struct Chunk : RowVectors<T, vec16<T>(), PER / vec16<T>()> {
-    static constexpr int VEC = vec16<T>(), N = PER / VEC;
-    using Base = RowVectors<T, VEC, N>;
-    using Base::v;
+// A chunk of a row in shared memory: SCAN_THREADS x W words of 32 bits.  Word w
+// of a thread is the chunk's word w * SCAN_THREADS + thread: one fp32 logit, or
+// two neighbours in 16 bits.  A row that starts `shift` bytes past a 16-byte
+// boundary is copied with what lies before it, so the words start at `shift`;
+// the places do not depend on it, and equal rows give equal sums.
+template <typename T, int W>
+struct Chunk {
+    static constexpr int PW = 4 / sizeof(T);                 // logits of a word
+    static constexpr int PER = W * PW;                       // of a thread
+    static constexpr uint32_t TOKENS = SCAN_THREADS * PER;
+    static constexpr int BYTES = SCAN_THREADS * W * 4 + 16;  // of a stage
+    const char* base;  // the stage, past the shift
+    uint32_t first, V;
 
-    static __device__ __forceinline__ uint32_t token(uint32_t first, int i) {
-        return first + ((i / VEC) * SCAN_THREADS + threadIdx.x) * VEC + i % VEC;
+    __device__ __forceinline__ uint32_t token(int e) const {
+        return first + ((e / PW) * SCAN_THREADS + threadIdx.x) * PW + e % PW;
     }
-    __device__ __forceinline__ float at(int i) const { return v[i / VEC].f(i % VEC); }
-    // A vector of a row that starts SHIFT bytes past a 16-byte boundary, cut
-    // out of the two that it lies in.
-    template <int SHIFT>
-    static __device__ __forceinline__ Vec<T, VEC> cut(const char* p) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p - SHIFT);
-        const uint4 b = *reinterpret_cast<const uint4*>(p - SHIFT + 16);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = SHIFT % 4 ? __funnelshift_r(w[k + SHIFT / 4], w[k + SHIFT / 4 + 1], SHIFT % 4 * 8) : w[k + SHIFT / 4];
-        Vec<T, VEC> r;
-        __builtin_memcpy(&r, o, 16);
-        return r;
+    // Logit e of the thread; its token is below V.
+    __device__ __forceinline__ float at(int e) const { return to_f32(*reinterpret_cast<const T*>(base + (token(e) - first) * sizeof(T))); }
+    __device__ __forceinline__ uint32_t word(int w) const {
+        const char* p = base + (w * SCAN_THREADS + threadIdx.x) * 4;
+        if (sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(base) & 2)) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(p - 2);
+            return __funnelshift_r(q[0], q[1], 16);
+        }
+        return *reinterpret_cast<const uint32_t*>(p);
     }
-    // The chunk's vectors; at the ends of an unaligned row, and past the end of
-    // any (-inf), elements are read singly.
-    template <int SHIFT>
-    __device__ __forceinline__ void load_from(const T* row, uint32_t first, uint32_t V) {
+    // The thread's logits as pairs; -inf past the row's end.
+    __device__ __forceinline__ void read(F2 (&x)[PER / 2]) const {
+        const bool tail = first + TOKENS > V;
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const uint32_t t = token(first, u * VEC);
-            const char* p = reinterpret_cast<const char*>(row + t);
-            if (SHIFT == 0 && t + VEC <= V)
-                v[u] = *reinterpret_cast<const Vec<T, VEC>*>(p);
-            else if (SHIFT != 0 && t >= VEC && t + 2 * VEC <= V)
-                v[u] = cut<SHIFT>(p);
-            else
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) v[u].v[j] = t + j < V ? row[t + j] : from_f32<T>(-INFINITY);
+        for (int p = 0; p < PER / 2; ++p) {
+            if constexpr (sizeof(T) == 4) {
+                x[p] = f2(__uint_as_float(word(2 * p)), __uint_as_float(word(2 * p + 1)));
+            } else {
+                const uint32_t w = word(p);
+                T v[2];
+                __builtin_memcpy(v, &w, 4);
+                x[p] = pair_of(v);
+            }
+            if (tail) x[p] = f2(token(2 * p) < V ? lo(x[p]) : -INFINITY, token(2 * p + 1) < V ? hi(x[p]) : -INFINITY);
         }
     }
-    __device__ __forceinline__ void load(const T* row, uint32_t first, uint32_t V, uint32_t shift) {
-        if (shift == 0) return load_from<0>(row, first, V);
-        if (shift == 4) return load_from<4>(row, first, V);
-        if (shift == 8) return load_from<8>(row, first, V);
-        if (shift == 12) return load_from<12>(row, first, V);
-        if constexpr (sizeof(T) == 2) {
-            if (shift == 2) return load_from<2>(row, first, V);
-            if (shift == 6) return load_from<6>(row, first, V);
-            if (shift == 10) return load_from<10>(row, first, V);
-            if (shift == 14) return load_from<14>(row, first, V);
-        }
-    }
-    // The largest logit as read (NaN only if all are).
-    __device__ __forceinline__ float largest() const {
-        if constexpr (sizeof(T) == 2) {
-            return this->max();
-        } else {
-            float m = v[0].v[0];
+    // Starts the copies of the chunk that begins at token `from` into a stage.
+    // Only whole 16-byte units inside the row are copied as such.
+    static __device__ __forceinline__ void copy(char* stage, const T* row, uint32_t from, uint32_t V) {
+        const char* begin = reinterpret_cast<const char*>(row);
+        const char* end = begin + static_cast<size_t>(V) * sizeof(T);
+        const char* src = begin + static_cast<size_t>(from) * sizeof(T);
+        src -= reinterpret_cast<uintptr_t>(src) & 15u;
 #pragma unroll
-            for (int i = 1; i < PER; ++i) m = fmaxf(m, at(i));
-            return m;
-        }
-    }
-    // The sum of e^(x - m).
-    __device__ __forceinline__ float sum(float m) const {
-        F2 s0 = f2(0.f), s1 = f2(0.f);
-        const F2 m2 = f2(-m), l2 = f2(LOG2E);
+        for (int u = 0; u < (BYTES / 16 + SCAN_THREADS - 1) / SCAN_THREADS; ++u) {
+            const int at = u * SCAN_THREADS + threadIdx.x;
+            const char* p = src + at * 16;
+            if (at >= BYTES / 16 || p >= end) continue;
+            if (p >= begin && p + 16 <= end) {
+                copy_async<16>(stage + at * 16, p);
+            } else {
 #pragma unroll
-        for (int p = 0; p < PER / 2; p += 2) {
-            const F2 a = mul2(add2(this->pair(p), m2), l2), b = mul2(add2(this->pair(p + 1), m2), l2);
-            s0 = add2(s0, f2(fast_exp2(lce::lo(a)), fast_exp2(lce::hi(a))));
-            s1 = add2(s1, f2(fast_exp2(lce::lo(b)), fast_exp2(lce::hi(b))));
+                for (int j = 0; j < 16; j += sizeof(T))
+                    if (p + j >= begin && p + j < end)
+                        *reinterpret_cast<T*>(stage + at * 16 + j) = *reinterpret_cast<const T*>(p + j);
+            }
         }
-        s0 = add2(s0, s1);
-        const float s = lce::lo(s0) + lce::hi(s0);
-        if (s < INFINITY) return s;
-        float c = 0.f;  // a NaN or an infinity among them
-#pragma unroll
-        for (int i = 0; i < PER; ++i) c += fast_exp2((clean(at(i)) - m) * LOG2E);
-        return c;
     }
 };
 
-// The M best of the chunk's own elements by rounds of a block-wide maximum,
-// appended to the buffer: for chunks whose candidates overflow it.
-template <typename T, int PER>
-__device__ void best_by_rounds(ScanShared& sh, const Chunk<T, PER>& c, uint32_t first, uint32_t V, int M, int n) {
+// The sum of e^(x - m).
+template <int PAIRS>
+__device__ __forceinline__ float sum_exp(const F2 (&x)[PAIRS], float m) {
+    F2 s0 = f2(0.f), s1 = f2(0.f);
+    const F2 m2 = f2(-m), l2 = f2(LOG2E);
+#pragma unroll
+    for (int p = 0; p < PAIRS; p += 2) {
+        const F2 a = mul2(add2(x[p], m2), l2), b = mul2(add2(x[p + 1], m2), l2);
+        s0 = add2(s0, f2(fast_exp2(lo(a)), fast_exp2(hi(a))));
+        s1 = add2(s1, f2(fast_exp2(lo(b)), fast_exp2(hi(b))));
+    }
+    s0 = add2(s0, s1);
+    const float s = lo(s0) + hi(s0);
+    if (s < INFINITY) return s;
+    float c = 0.f;  // a NaN or an infinity among them
+#pragma unroll
+    for (int p = 0; p < PAIRS; ++p)
+        c += fast_exp2((clean(lo(x[p])) - m) * LOG2E) + fast_exp2((clean(hi(x[p])) - m) * LOG2E);
+    return c;
+}
+
+// The M best of the thread's chunk by rounds of a block-wide maximum, appended
+// to the buffer: for chunks whose candidates overflow it.
+template <typename T, int W>
+__device__ void best_by_rounds(ScanShared& sh, const Chunk<T, W>& c, int M, int n) {
     uint64_t below = ~0ull;
     for (int r = 0; r < M; ++r) {
         uint64_t best = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const uint32_t t = c.token(first, i);
-            const uint64_t k = t < V ? logit_key(c.at(i), t) : 0;
+        for (int e = 0; e < c.PER; ++e) {
+            const uint32_t t = c.token(e);
+            const uint64_t k = t < c.V ? logit_key(c.at(e), t) : 0;
             if (k < below && k > best) best = k;
         }
         best = warp_max(best);
@@ -241,9 +242,15 @@ __device__ void best_by_rounds(ScanShared& sh, const Chunk<T, PER>& c, uint32_t 
     __syncthreads();
 }
 
-template <typename T, int PER>
+// A part of a row.  Chunks are copied two ahead; a chunk's candidates go to the
+// buffer as they are found, and are looked at when the next chunk is there
+// (while the chunk they came from still is: if they overflowed, it is gone
+// through again).  A chunk costs a barrier, two with candidates in the one
+// before it.
+template <typename T, int W>
 __global__ void __launch_bounds__(SCAN_THREADS, 4) beam_scan_kernel(ScanArgs a) {
-    constexpr uint32_t CHUNK = SCAN_THREADS * PER;
+    using C = Chunk<T, W>;
+    extern __shared__ __align__(16) char ring[];  // [SCAN_STAGES, BYTES]
     __shared__ ScanShared sh;
     launch_dependents();
     const int64_t row = blockIdx.y;
@@ -252,24 +259,52 @@ __global__ void __launch_bounds__(SCAN_THREADS, 4) beam_scan_kernel(ScanArgs a) 
     const T* z = static_cast<const T*>(a.z) + row * a.ld;
     const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z) & 15u);
     const uint32_t V = static_cast<uint32_t>(a.V);
-    const uint64_t begin = static_cast<uint64_t>(seg) * a.per_seg * CHUNK;
-    uint64_t end = begin + static_cast<uint64_t>(a.per_seg) * CHUNK;
-    if (end > V) end = V;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c0 = static_cast<int64_t>(seg) * a.per_seg;
+    int64_t left = (V + C::TOKENS - 1) / C::TOKENS - c0;
+    const int chunks = static_cast<int>(left < a.per_seg ? left : a.per_seg);
+    auto begin_copy = [&](int c) {
+        if (c < chunks) C::copy(ring + (c % SCAN_STAGES) * C::BYTES, z, static_cast<uint32_t>((c0 + c) * C::TOKENS), V);
+        copy_async_commit();
+    };
+    auto chunk = [&](int c) {
+        return C{ring + (c % SCAN_STAGES) * C::BYTES + shift, static_cast<uint32_t>((c0 + c) * C::TOKENS), V};
+    };
     int n = 0;         // keys in the buffer (all threads agree)
     uint64_t tau = 0;  // the M-th best so far, 0 while there are fewer
     float m = -INFINITY;
     Sum2 s{0.f, 0.f};
-    if (threadIdx.x == 0) sh.n = 0;
-    for (uint64_t first64 = begin; first64 < end; first64 += CHUNK) {
-        const uint32_t first = static_cast<uint32_t>(first64);
-        Chunk<T, PER> c;
-        c.load(z, first, V, shift);
-        const float raw = c.largest(), mx = clean(raw);
-        const float m2 = fmaxf(m, mx);
+    if (threadIdx.x == 0) sh.n = sh.kept = 0;
+#pragma unroll
+    for (int k = 0; k < SCAN_STAGES - 1; ++k) begin_copy(k);
+    bool pushed = false;
+    for (int c = 0; c <= chunks; ++c) {  // the last turn only looks at the last chunk's candidates
+        copy_async_wait<SCAN_STAGES - 2>();
+        if (__syncthreads_or(pushed)) {
+            n = sh.n;
+            if (n > MAX_M + SCAN_CAP) {
+                n = keep_best(sh, sh.kept, a.M);
+                best_by_rounds<T, W>(sh, chunk(c - 1), a.M, n);
+                n = keep_best(sh, n + a.M, a.M);
+            } else if (n > SCAN_HIGH || tau == 0) {
+                n = keep_best(sh, n, a.M);
+            }
+            if (n == a.M) tau = sh.buf[n - 1] > tau ? sh.buf[n - 1] : tau;
+            if (threadIdx.x == 0) sh.kept = n;
+            __syncthreads();
+        }
+        if (c == chunks) break;
+        begin_copy(c + SCAN_STAGES - 1);
+        const C k = chunk(c);
+        F2 x[C::PER / 2];
+        k.read(x);
+        float raw = lo(x[0]);
+#pragma unroll
+        for (int p = 0; p < C::PER / 2; ++p) raw = fmaxf(raw, fmaxf(lo(x[p]), hi(x[p])));
+        const float mx = clean(raw), m2 = fmaxf(m, mx);
         if (m2 > -INFINITY) {
             if (m2 > m) s.scale(fast_exp2((m - m2) * LOG2E));  // of nothing at first
-            s.add(c.sum(m2));
+            s.add(sum_exp(x, m2));
             m = m2;
         }
         // candidates: in a part's first chunk those that are at least as large as the
@@ -280,12 +315,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 4) beam_scan_kernel(ScanArgs a) 
             int at = 0;
             if (mx > -INFINITY)
 #pragma unroll
-                for (int i = PER - 1; i >= 0; --i) at = c.at(i) >= raw ? i : at;
-            const uint32_t t = first + ((at / c.VEC) * SCAN_THREADS + threadIdx.x) * c.VEC + at % c.VEC;
-            const uint64_t k = t < V ? logit_key(mx, t) : 0;
-            const int r = (a.M + SCAN_WARPS - 1) / SCAN_WARPS;
-            uint64_t below = k, rth = 0;
-            for (int i = 0; i < r; ++i) {
+                for (int e = C::PER - 1; e >= 0; --e) at = (e & 1 ? hi(x[e / 2]) : lo(x[e / 2])) >= raw ? e : at;
+            const uint32_t t = k.token(at);
+            uint64_t below = t < V ? logit_key(mx, t) : 0, rth = 0;
+            for (int i = 0; i < (a.M + SCAN_WARPS - 1) / SCAN_WARPS; ++i) {
                 rth = warp_max(below);
                 if (below == rth) below = 0;
             }
@@ -296,41 +329,26 @@ __global__ void __launch_bounds__(SCAN_THREADS, 4) beam_scan_kernel(ScanArgs a) 
             for (int w = 1; w < SCAN_WARPS; ++w) limit = sh.red_k[w] < limit ? sh.red_k[w] : limit;
             if (limit) --limit;  // 0, all pass: a warp with fewer than r threads that have elements
         }
-        // (the barrier also puts the count of the chunk before it ahead of the pushes)
-        const bool some = logit_key(mx, 0) > limit;
-        if (!__syncthreads_or(some)) continue;
-        if (some) {
+        pushed = logit_key(mx, 0) > limit;
+        if (pushed) {
             const float least = key_logit(limit + 1);
             uint32_t which = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) which |= static_cast<uint32_t>(c.at(i) >= least) << i;
-            if (limit == 0) which = (1u << PER) - 1;
+            for (int e = 0; e < C::PER; ++e)
+                which |= static_cast<uint32_t>((e & 1 ? hi(x[e / 2]) : lo(x[e / 2])) >= least) << e;
+            if (limit == 0) which = static_cast<uint32_t>((1ull << C::PER) - 1);
             for (; which; which &= which - 1) {
-                const int i = __ffs(which) - 1;
-                const uint32_t t = first + ((i / c.VEC) * SCAN_THREADS + threadIdx.x) * c.VEC + i % c.VEC;
-                const uint64_t k = t < V ? logit_key(to_f32(z[t]), t) : 0;  // read again: the registers have no index
-                if (k > limit) {
+                const int e = __ffs(which) - 1;
+                const uint32_t t = k.token(e);
+                const uint64_t key = t < V ? logit_key(k.at(e), t) : 0;
+                if (key > limit) {
                     const int place = atomicAdd(&sh.n, 1);
-                    if (place < MAX_M + SCAN_CAP) sh.buf[place] = k;
+                    if (place < MAX_M + SCAN_CAP) sh.buf[place] = key;
                 }
             }
         }
-        __syncthreads();
-        const int total = sh.n;
-        if (total > MAX_M + SCAN_CAP) {
-            n = keep_best(sh, n, a.M);
-            best_by_rounds<T, PER>(sh, c, first, V, a.M, n);
-            n += a.M;
-        } else {
-            n = total;
-        }
-        if (total > MAX_M + SCAN_CAP || n > SCAN_HIGH || tau == 0) {
-            n = keep_best(sh, n, a.M);
-            if (n == a.M) tau = sh.buf[n - 1];
-        }
     }
-    __syncthreads();
-    if (n > 0) n = keep_best(sh, n, a.M);
+    if (n > a.M) n = keep_best(sh, n, a.M);
     const int64_t part = row * a.segs + seg;
     for (int i = threadIdx.x; i < a.M; i += SCAN_THREADS) a.seg_key[part * a.M + i] = i < n ? sh.buf[i] : 0;
     // the block's maximum and sum
@@ -553,19 +571,21 @@ lce_status_t beam_sizes(int64_t items, int64_t K, int64_t V, int64_t M) {
 }
 
 struct BeamPlan {
-    bool small;  // chunks of 2048 tokens, not 4096
+    bool small;  // chunks of 4 KB, not 16 KB
     int32_t segs, per_seg;
     size_t off_m, off_key, total;
 };
 
-// A row's chunks and how they are shared out.  With few rows, chunks of 2048
-// tokens spread the work over twice the blocks (one request of four beams over
-// 32768 tokens: 64 blocks, not 32).
-BeamPlan beam_plan(int64_t rows, int64_t V, int64_t M) {
+// A row's chunks and how they are shared out: one round of blocks where there
+// are rows for it.  With few rows, chunks of 4 KB spread the work over four
+// times the blocks (one request of four bf16 beams over 32768 tokens: 64
+// blocks, not 16).
+BeamPlan beam_plan(int64_t rows, int64_t V, int64_t M, int dtype) {
     BeamPlan p;
-    p.small = rows * ((V + 4095) / 4096) < SCAN_BLOCKS / 4;
-    const int64_t chunk = p.small ? 2048 : 4096, chunks = (V + chunk - 1) / chunk;
-    int64_t segs = rows < SCAN_BLOCKS ? SCAN_BLOCKS / rows : 1;  // one round of blocks
+    const int64_t per_kb = 1024 / static_cast<int64_t>(dtype_bytes(dtype));
+    p.small = rows * ((V + 16 * per_kb - 1) / (16 * per_kb)) < SCAN_BLOCKS / 4;
+    const int64_t chunk = (p.small ? 4 : 16) * per_kb, chunks = (V + chunk - 1) / chunk;
+    int64_t segs = rows < SCAN_BLOCKS ? SCAN_BLOCKS / rows : 1;
     if (segs > SCAN_SEGS_MAX) segs = SCAN_SEGS_MAX;
     if (segs > chunks) segs = chunks;
     p.per_seg = static_cast<int32_t>((chunks + segs - 1) / segs);
@@ -575,6 +595,17 @@ BeamPlan beam_plan(int64_t rows, int64_t V, int64_t M) {
     p.off_key = (p.off_m + n * 4 + 255) / 256 * 256;
     p.total = p.off_key + n * M * 8;
     return p;
+}
+
+template <typename T, int W>
+lce_status_t beam_scan(const ScanArgs& a, int64_t rows, cudaStream_t s) {
+    constexpr int smem = SCAN_STAGES * Chunk<T, W>::BYTES;
+    if (smem > 40 * 1024 && cudaFuncSetAttribute(beam_scan_kernel<T, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 smem) != cudaSuccess)
+        return LCE_ERR_CUDA;
+    const dim3 grid(a.segs, static_cast<unsigned>(rows));
+    LCE_PROFILED(beam_scan_kernel<T, W><<<grid, SCAN_THREADS, smem, s>>>(a));
+    return LCE_OK;
 }
 
 }  // namespace
@@ -587,7 +618,10 @@ extern "C" {
 lce_status_t lce_beam_workspace_size(int64_t items, int64_t beams, int64_t V, int64_t n_out, size_t* bytes) {
     if (!bytes) return LCE_ERR_INVALID_ARG;
     const lce_status_t st = beam_sizes(items, beams, V, n_out);
-    if (st == LCE_OK) *bytes = beam_plan(items * beams, V, n_out).total;
+    if (st == LCE_OK) {  // of either type
+        const size_t a = beam_plan(items * beams, V, n_out, LCE_BF16).total, b = beam_plan(items * beams, V, n_out, LCE_F32).total;
+        *bytes = a > b ? a : b;
+    }
     return st;
 }
 
@@ -602,7 +636,7 @@ lce_status_t lce_beam_select(int64_t items, int64_t beams, int64_t V, int64_t n_
         !aligned_to(out_tokens, 8) || !aligned_to(out_parents, 8))
         return LCE_ERR_INVALID_ARG;
     if (!ws || !aligned_to(ws, 256)) return LCE_ERR_INVALID_ARG;
-    const BeamPlan p = beam_plan(items * beams, V, n_out);
+    const BeamPlan p = beam_plan(items * beams, V, n_out, dtype);
     if (ws_bytes < p.total) return LCE_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* w = static_cast<uint8_t*>(ws);
@@ -611,14 +645,9 @@ lce_status_t lce_beam_select(int64_t items, int64_t beams, int64_t V, int64_t n_
     uint64_t* seg_key = reinterpret_cast<uint64_t*>(w + p.off_key);
     const ScanArgs sa{logits, ld, finished, static_cast<int32_t>(V), static_cast<int32_t>(n_out), p.segs, p.per_seg,
                       seg_m, seg_s, seg_key};
-    const dim3 grid(p.segs, static_cast<unsigned>(items * beams));
     const lce_status_t sc = with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);
-        if (p.small)
-            LCE_PROFILED(beam_scan_kernel<T, 8><<<grid, SCAN_THREADS, 0, s>>>(sa));
-        else
-            LCE_PROFILED(beam_scan_kernel<T, 16><<<grid, SCAN_THREADS, 0, s>>>(sa));
-        return LCE_OK;
+        return p.small ? beam_scan<T, 4>(sa, items * beams, s) : beam_scan<T, 16>(sa, items * beams, s);
     });
     if (sc != LCE_OK) return sc;
     const JoinArgs ja{seg_m, seg_s, seg_key, scores, finished, static_cast<int32_t>(beams), static_cast<int32_t>(n_out),

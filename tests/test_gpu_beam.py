@@ -89,6 +89,31 @@ def test_sizes(B, K, V, n, dtype):
     check(z, s, n, eos=int(V // 2))
 
 
+@pytest.mark.parametrize("V,n", [(30011, 16), (30011, 4), (24576, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("order", ["random", "up", "down"])
+def test_parts_of_many_chunks(V, n, dtype, order):
+    """So many rows that a block goes through several chunks of one, with candidates in all of them, in the last
+    or in the first."""
+    z, s = head(160, 4, V, V + n, dtype)
+    if order != "random":
+        z = z.sort(dim=-1, descending=order == "down").values
+    check(z[::16], s[::16], n)                    # few rows: many parts
+    from lm_head_linear_chunked_gb300.beam import beam_select
+    all_rows = beam_select(z, s, n)
+    few = beam_select(z[::16], s[::16], n)
+    near = 2 * E_LSE
+    for k in ("tokens", "parents"):
+        same = (all_rows[k][::16] == few[k])
+        gap = (all_rows["scores"][::16, 1:] - all_rows["scores"][::16, :-1]).abs() <= near
+        tied = torch.zeros_like(same)
+        tied[:, 1:] |= gap
+        tied[:, :-1] |= gap
+        assert bool((same | tied).all()), k
+    check(z[:152:19].contiguous(), s[:152:19], n)
+    assert (all_rows["scores"][::16] - few["scores"]).abs().max() <= near
+
+
 @pytest.mark.parametrize("V", [50, 8200, 33333, 65536])
 @pytest.mark.parametrize("n", [1, 7, 64])
 def test_equal_logits(V, n):
