@@ -24,7 +24,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr int SCAN_THREADS = 256;
 constexpr int SCAN_WARPS = SCAN_THREADS / 32;
 constexpr int SCAN_CAP = 448;                         // keys the buffer holds beside the list
-constexpr int SCAN_HIGH = 128;                        // keys that start a merge
+constexpr int SCAN_MORE = 16;                         // keys beside the list that start a merge
 constexpr int SCAN_STAGES = 3;                        // chunks in shared memory
 constexpr int SCAN_SEGS_MAX = 32;                     // parts of a row (a lane each in the join)
 constexpr int64_t SCAN_BLOCKS = 608;                  // blocks that fill the GPU
@@ -102,8 +102,6 @@ struct ScanShared {
 // there are.  A key's place is the number of larger ones.
 __device__ int keep_best(ScanShared& sh, int n, int M) {
     constexpr int PER = (MAX_M + SCAN_CAP + SCAN_THREADS - 1) / SCAN_THREADS;
-    if (threadIdx.x == 0) sh.buf[n] = 0;  // read with the last key of an odd number
-    __syncthreads();
     uint64_t key[PER];
     int rank[PER];
 #pragma unroll
@@ -114,10 +112,11 @@ __device__ int keep_best(ScanShared& sh, int n, int M) {
             key[q] = sh.buf[i];
             int r = 0;
 #pragma unroll 4
-            for (int j = 0; j < n; j += 2) {
+            for (int j = 0; j + 1 < n; j += 2) {
                 const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(sh.buf + j);
                 r += (k.x > key[q]) + (k.y > key[q]);
             }
+            if (n & 1) r += sh.buf[n - 1] > key[q];
             rank[q] = r;
         }
     }
@@ -181,6 +180,15 @@ struct Chunk {
         const char* end = begin + static_cast<size_t>(V) * sizeof(T);
         const char* src = begin + static_cast<size_t>(from) * sizeof(T);
         src -= reinterpret_cast<uintptr_t>(src) & 15u;
+        if (src >= begin && src + BYTES <= end) {  // inside the row
+            const char* p = src + threadIdx.x * 16;
+            char* to = stage + threadIdx.x * 16;
+#pragma unroll
+            for (int u = 0; u < BYTES / 16 / SCAN_THREADS; ++u)
+                copy_async<16>(to + u * SCAN_THREADS * 16, p + u * SCAN_THREADS * 16);
+            if (threadIdx.x == 0) copy_async<16>(stage + BYTES - 16, src + BYTES - 16);
+            return;
+        }
 #pragma unroll
         for (int u = 0; u < (BYTES / 16 + SCAN_THREADS - 1) / SCAN_THREADS; ++u) {
             const int at = u * SCAN_THREADS + threadIdx.x;
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 4) beam_scan_kernel(ScanArgs a) 
                 n = keep_best(sh, sh.kept, a.M);
                 best_by_rounds<T, W>(sh, chunk(c - 1), a.M, n);
                 n = keep_best(sh, n + a.M, a.M);
-            } else if (n > SCAN_HIGH || tau == 0) {
+            } else if (n > a.M + SCAN_MORE || tau == 0) {
                 n = keep_best(sh, n, a.M);
             }
             if (n == a.M) tau = sh.buf[n - 1] > tau ? sh.buf[n - 1] : tau;
@@ -393,8 +401,9 @@ __device__ __forceinline__ double from_ordered(uint64_t o) {
 }
 
 // One block per item: a warp per beam adds its parts up and merges their
-// lists; then all scores are computed, and the first warp merges the beams, a
-// lane holding the beams l and l + 32.  A merge takes the largest head M times.
+// lists; then all scores are computed, and the beams are merged: by counting
+// where a thread can take each candidate, else by the first warp, a lane
+// holding the beams l and l + 32.  A merge takes the largest head M times.
 __global__ void __launch_bounds__(32 * JOIN_WARPS) beam_join_kernel(JoinArgs a) {
     extern __shared__ uint64_t dyn[];
     uint64_t* keys = dyn;                // [K, M] per beam, sorted down
@@ -409,6 +418,13 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) beam_join_kernel(JoinArgs a) 
     wait_for_primary();
     for (int k = warp; k < a.K; k += JOIN_WARPS) {
         const int64_t row = b * a.K + k;
+        // (a finished beam's parts were not written; what is read there is not used)
+        uint64_t* list = a.segs > 1 ? lists + warp * a.segs * a.M : keys + k * a.M;
+        const uint64_t* from = a.seg_key + row * a.segs * a.M;
+        for (int i = lane; i < a.segs * a.M; i += 32) list[i] = from[i];
+        const bool have = lane < a.segs;
+        const float m = have ? a.seg_m[row * a.segs + lane] : -INFINITY;
+        const float2 ms = have ? a.seg_s[row * a.segs + lane] : make_float2(0.f, 0.f);
         const bool over = a.finished && a.finished[row];
         if (lane == 0) {
             ended[k] = over;
@@ -416,12 +432,6 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) beam_join_kernel(JoinArgs a) 
             sums[k] = make_float2(1.f, 0.f);
         }
         if (over) continue;
-        uint64_t* list = lists + warp * a.segs * a.M;
-        const uint64_t* from = a.seg_key + row * a.segs * a.M;
-        for (int i = lane; i < a.segs * a.M; i += 32) list[i] = from[i];
-        const bool have = lane < a.segs;
-        const float m = have ? a.seg_m[row * a.segs + lane] : -INFINITY;
-        const float2 ms = have ? a.seg_s[row * a.segs + lane] : make_float2(0.f, 0.f);
         float bm = m;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
@@ -435,6 +445,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) beam_join_kernel(JoinArgs a) 
             top[k] = bm;
             sums[k] = make_float2(s.hi, s.lo);
         }
+        if (a.segs == 1) continue;  // the part's list is the beam's
         __syncwarp();
         int at = lane * a.M;
         const int stop = at + a.M;
@@ -457,7 +468,8 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) beam_join_kernel(JoinArgs a) 
                                                            : -INFINITY;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.K * a.M; i += 32 * JOIN_WARPS) {
+    const int all = a.K * a.M;
+    for (int i = threadIdx.x; i < all; i += 32 * JOIN_WARPS) {
         const int k = i / a.M, r = i - k * a.M;
         uint64_t o = 0;
         if (ended[k]) {
@@ -469,28 +481,48 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) beam_join_kernel(JoinArgs a) 
         score[i] = o;
     }
     __syncthreads();
+    // candidate i of the item as its result r
+    auto write = [&](int i, int r) {
+        const int k = i / a.M;
+        const int64_t token = ended[k] ? a.pad : static_cast<int64_t>(key_token(keys[i])), o = b * a.M + r;
+        a.out_scores[o] = static_cast<float>(from_ordered(score[i]));
+        a.out_tokens[o] = token;
+        a.out_parents[o] = k;
+        if (a.out_finished) a.out_finished[o] = ended[k] || (a.eos >= 0 && token == a.eos);
+    };
+    if (all <= 32 * JOIN_WARPS) {
+        // a thread per candidate: its place is the number of better ones, among equals those before it
+        const int i = threadIdx.x;
+        if (i < all && score[i]) {
+            const uint64_t mine = score[i];
+            int r = 0;
+#pragma unroll 8
+            for (int j = 0; j < all; ++j) r += score[j] > mine || (score[j] == mine && j < i);
+            if (r < a.M) write(i, r);
+        }
+        return;
+    }
     if (warp != 0) return;
     int at0 = lane * a.M, at1 = (lane + 32) * a.M;
     const int stop0 = at0 + a.M, stop1 = at1 + a.M;
     uint64_t k0 = lane < a.K ? score[at0] : 0, k1 = lane + 32 < a.K ? score[at1] : 0;
+    int mine[2] = {0, 0};  // results `lane` and `lane + 32`
     for (int r = 0; r < a.M; ++r) {
         const uint64_t best = warp_max(k1 > k0 ? k1 : k0);
         // the lowest beam among equals: the lanes' first beams before their second ones
         const unsigned has0 = __ballot_sync(0xFFFFFFFFu, k0 == best), has1 = __ballot_sync(0xFFFFFFFFu, k1 == best);
-        const bool first = has0 != 0;
-        if (lane == __ffs(first ? has0 : has1) - 1) {
-            const int k = first ? lane : lane + 32, at = first ? at0 : at1;
-            const int64_t token = ended[k] ? a.pad : static_cast<int64_t>(key_token(keys[at])), o = b * a.M + r;
-            a.out_scores[o] = static_cast<float>(from_ordered(best));
-            a.out_tokens[o] = token;
-            a.out_parents[o] = k;
-            if (a.out_finished) a.out_finished[o] = ended[k] || (a.eos >= 0 && token == a.eos);
-            if (first)
+        const int winner = __ffs(has0 ? has0 : has1) - 1;
+        const int at = __shfl_sync(0xFFFFFFFFu, has0 ? at0 : at1, winner);
+        if (lane == (r & 31)) mine[r >> 5] = at;
+        if (lane == winner) {
+            if (has0)
                 k0 = ++at0 < stop0 ? score[at0] : 0;
             else
                 k1 = ++at1 < stop1 ? score[at1] : 0;
         }
     }
+    if (lane < a.M) write(mine[0], lane);
+    if (lane + 32 < a.M) write(mine[1], lane + 32);
 }
 
 // ---------------------------------------------------------------- states

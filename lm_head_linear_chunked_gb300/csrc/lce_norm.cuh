@@ -607,8 +607,10 @@ lce_status_t fwd_rows(const NormFwd<T>& a, cudaStream_t s) {
 // The forward's form by the row's width in vectors (16 bytes where rows start
 // on 16-byte boundaries; else 4 bytes; else one element), measured on 2^29
 // bf16 elements against the copy rate:
-//  - up to 128 vectors (1024 bf16): a warp per row, 6.25 TB/s at 1024 (a
-//    block of two warps: 4.7);
+//  - up to 64 vectors (512 bf16): a warp per row, 6.1 TB/s at 512;
+//  - up to 128: the same with the next rows copied ahead and weight and bias
+//    kept, 6.1 TB/s at 1024 (a block of two warps: 4.7).  16384 rows of it with
+//    fp32 weights take 14 us, against 19 where each warp ends with its row;
 //  - up to 2048: a block per row, four vectors a thread, 6.4 TB/s at 4096 (a
 //    warp per row: 5.7, two vectors: 5.3);
 //  - where a quarter of such a block would be idle, two rows of two vectors a
@@ -634,7 +636,7 @@ lce_status_t norm_forward(const NormCall& c) {
         } else if (n <= 64) {
             LCE_PROFILED(norm_fwd_warp<T, W, V, 2><<<blocks, 128, 0, s>>>(a));
         } else if (n <= 128) {
-            LCE_PROFILED(norm_fwd_warp<T, W, V, 4><<<blocks, 128, 0, s>>>(a));
+            return fwd_rows<T, W, V, 4, 1, 3, 1, 12>(a, s);
         } else if (n <= 512 && 4 * threads_for(n, 4) > n + n / 8) {
             return fwd_rows<T, W, V, 2, 2, 2, 8, 2>(a, s);
         } else if (n <= 512) {
