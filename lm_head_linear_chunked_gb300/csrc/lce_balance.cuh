@@ -146,7 +146,7 @@ __device__ __forceinline__ void count_tokens(const BalArgs& a, int g, int part, 
 }
 
 // The last block of the pass adds the loss up: a warp over a group's parts,
-// four groups at a time, then the groups in order.
+// then the groups in order.
 __device__ __forceinline__ void finish_loss(const BalArgs& a) {
     __shared__ int bad;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -156,25 +156,22 @@ __device__ __forceinline__ void finish_loss(const BalArgs& a) {
     for (int64_t k = threadIdx.x; k < static_cast<int64_t>(a.G) * a.count_parts; k += BAL_THREADS)
         wrong |= __ldcg(a.part_n + k) < 0;
     if (wrong) bad = 1;
-    for (int g0 = warp * 4; g0 < a.G; g0 += BAL_WARPS * 4) {
-        float q[4];
-        int64_t n[4];
+    for (int g = warp; g < a.G; g += BAL_WARPS) {
+        const float* from = a.part_q + static_cast<int64_t>(g) * a.parts;
+        const int64_t n = __ldcg(a.n_out + g);
+        float q = 0.f;
+        for (int k0 = lane; k0 < a.parts; k0 += 8 * 32) {
+            float v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int g = g0 + i < a.G ? g0 + i : a.G - 1;
-            q[i] = 0.f;
-            for (int k = lane; k < a.parts; k += 32) q[i] += __ldcg(a.part_q + static_cast<int64_t>(g) * a.parts + k);
-            n[i] = __ldcg(a.n_out + g);
+            for (int i = 0; i < 8; ++i) v[i] = k0 + i * 32 < a.parts ? __ldcg(from + k0 + i * 32) : 0.f;
+            q += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            q[i] = warp_sum(q[i]);
-            // the group's loss takes the place of its first part's sum
-            if (lane == 0 && g0 + i < a.G) {
-                q[i] = n[i] > 0 ? 1.f + q[i] / static_cast<float>(n[i]) : 0.f;
-                if (a.group_loss) a.group_loss[g0 + i] = q[i];
-                a.part_q[static_cast<int64_t>(g0 + i) * a.parts] = q[i];
-            }
+        q = warp_sum(q);
+        // the group's loss takes the place of its first part's sum
+        if (lane == 0) {
+            q = n > 0 ? 1.f + q / static_cast<float>(n) : 0.f;
+            if (a.group_loss) a.group_loss[g] = q;
+            a.part_q[static_cast<int64_t>(g) * a.parts] = q;
         }
     }
     __syncthreads();
@@ -249,7 +246,7 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
                 if (MODE == BAL_BACKWARD) {
                     c = a.counts[static_cast<int64_t>(g) * a.E + e];
                 } else {
-#pragma unroll 8
+#pragma unroll 16
                     for (int q = 0; q < a.count_parts; ++q)
                         c += a.part_c[(static_cast<int64_t>(g) * a.count_parts + q) * a.E + e];
                 }
@@ -276,11 +273,11 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
     V* dst = GRAD ? reinterpret_cast<V*>(static_cast<T*>(a.dz) + (static_cast<int64_t>(g) * a.T + t0 + t) * a.E) + l : nullptr;
     const uint8_t* keep = a.mask ? a.mask + g * a.mask_g + t0 : nullptr;
     V next[AHEAD][ITEMS];
-    bool next_ok[AHEAD];
-    auto fetch = [&](int at, V* to, bool* valid) {
+    uint32_t next_ok[AHEAD];  // the mask's byte as read: a comparison here would wait for it
+    auto fetch = [&](int at, V* to, uint32_t* valid) {
         *valid = at < tokens;
         if (at < tokens) {
-            if (keep) *valid = keep[at] != 0;
+            if (keep) *valid = keep[at];
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i)
                 if (whole || i * LANES + l < n) to[i] = src[i * LANES];
@@ -290,9 +287,9 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) fetch(t + k * step, next[k], next_ok + k);
     // one token of each subgroup, from slot k of the tokens read ahead
-    auto token = [&](V (&slot)[ITEMS], bool& slot_ok) {
+    auto token = [&](V (&slot)[ITEMS], uint32_t& slot_ok) {
         RowVectors<T, VEC, ITEMS> z;
-        const bool ok = slot_ok;
+        const bool ok = slot_ok != 0;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? slot[i] : V{};
         fetch(t + AHEAD * step, slot, &slot_ok);
