@@ -33,8 +33,15 @@ constexpr int BAL_THREADS = 32 * BAL_WARPS;
 // at most four on each of 152 SMs, which all run at once (sixteen more than
 // that took a second round, and half as long again); and the fewest tokens
 // that are worth one.
+// Tokens of a lane group in the ring of the pass: one in work, the others on their way.
+constexpr int BAL_STAGES = 4;
 constexpr int64_t BAL_SMS = 152;
 constexpr int64_t BAL_BLOCKS = 4 * BAL_SMS;
+// Whether the tokens read ahead wait in shared memory (2^26 bf16 logits of 128
+// experts: 44 us, against 57 from registers, where the waits could not be
+// hidden) or, with several vectors a lane, in registers (2^25 fp32 logits of
+// 256: 38 us against 40).
+constexpr bool bal_ring(size_t vec, int items) { return vec >= 4 && items == 1; }
 // Blocks of the pass on an SM, by the experts of a lane (which it keeps in registers).
 constexpr int bal_resident(int experts) { return experts <= 8 ? 4 : experts <= 16 ? 2 : 1; }
 constexpr int64_t BAL_MIN_TOKENS = 32;
@@ -55,6 +62,7 @@ struct BalArgs {
     int64_t mask_g;
     int64_t T, per_part, per_count;
     int32_t G, E, k, parts, count_parts;  // the pass may take fewer parts than these
+    uint32_t ring_at;   // byte offset of the pass's ring in its shared memory
     bool inline_count;  // one block in all: the pass counts by itself
     // workspace
     WsHeader* hdr;
@@ -105,9 +113,25 @@ __device__ __forceinline__ void count_tokens(const BalArgs& a, int g, int part, 
     const int per = a.idx64 ? 2 : 4;
     const bool vec = a.k % per == 0 && aligned_dev(a.idx);
     for (int64_t t = t0 + threadIdx.x; t < t1; t += BAL_THREADS) {
+        const int64_t at = (static_cast<int64_t>(g) * a.T + t) * a.k;
+        if (vec && a.idx64 && a.k <= 8) {  // the mask and all indices are read together
+            const longlong2* p = reinterpret_cast<const longlong2*>(static_cast<const int64_t*>(a.idx) + at);
+            longlong2 e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (2 * j < a.k) e[j] = p[j];
+            if (!kept(a, g, t)) continue;
+            ++n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (2 * j < a.k) {
+                    count(e[j].x);
+                    count(e[j].y);
+                }
+            continue;
+        }
         if (!kept(a, g, t)) continue;
         ++n;
-        const int64_t at = (static_cast<int64_t>(g) * a.T + t) * a.k;
         if (vec && a.idx64) {
             const longlong2* p = reinterpret_cast<const longlong2*>(static_cast<const int64_t*>(a.idx) + at);
 #pragma unroll 4
@@ -197,14 +221,15 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
     constexpr int PAIRS = ITEMS * VEC / 2;
     constexpr float LOG2E = 1.4426950408889634f;
     using V = Vec<T, VEC>;
-    extern __shared__ float sm[];  // f [E]; with the counting inline, histograms [BAL_WARPS, E]
+    extern __shared__ __align__(16) float sm[];  // f [E]; with the counting inline, histograms [BAL_WARPS, E]; the ring
     __shared__ float warp_q[BAL_WARPS];
     __shared__ bool last;
     __shared__ float scale_s;
     __shared__ int64_t n_s;
     const int g = blockIdx.y, part = blockIdx.x;
     constexpr int tpw = 32 / LANES;                 // tokens of a warp at a time
-    constexpr int AHEAD = ITEMS * sizeof(V) <= 32 ? 2 : 1;  // tokens read ahead
+    constexpr bool RING = bal_ring(sizeof(V), ITEMS);
+    constexpr int AHEAD = RING ? BAL_STAGES - 1 : 1;  // tokens read ahead
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane & (LANES - 1), sub = lane / LANES;
     const int n = a.E / VEC;
@@ -272,27 +297,48 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
     const int64_t src_step = step * a.zt / VEC;
     V* dst = GRAD ? reinterpret_cast<V*>(static_cast<T*>(a.dz) + (static_cast<int64_t>(g) * a.T + t0 + t) * a.E) + l : nullptr;
     const uint8_t* keep = a.mask ? a.mask + g * a.mask_g + t0 : nullptr;
-    V next[AHEAD][ITEMS];
-    uint32_t next_ok[AHEAD];  // the mask's byte as read: a comparison here would wait for it
-    auto fetch = [&](int at, V* to, uint32_t* valid) {
+    // a thread's own vectors of the next tokens, in shared memory; or in registers
+    // (RING); the mask's bytes wait as they were read
+    V* ring = reinterpret_cast<V*>(reinterpret_cast<char*>(sm) + a.ring_at) + threadIdx.x;
+    V next[RING ? 1 : ITEMS];
+    uint32_t next_ok[AHEAD];
+    auto fetch = [&](int at, int slot, uint32_t* valid) {
         *valid = at < tokens;
         if (at < tokens) {
             if (keep) *valid = keep[at];
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i)
-                if (whole || i * LANES + l < n) to[i] = src[i * LANES];
+                if (whole || i * LANES + l < n) {
+                    if constexpr (RING)
+                        copy_async<sizeof(V)>(ring + (slot * ITEMS + i) * BAL_THREADS, src + i * LANES);
+                    else
+                        next[i] = src[i * LANES];
+                }
         }
+        if constexpr (RING) copy_async_commit();
         src += src_step;
     };
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) fetch(t + k * step, next[k], next_ok + k);
-    // one token of each subgroup, from slot k of the tokens read ahead
-    auto token = [&](V (&slot)[ITEMS], uint32_t& slot_ok) {
+    for (int k = 0; k < AHEAD; ++k) fetch(t + k * step, k, next_ok + k);
+    int slot = 0;
+    // the warp's first subgroup has the lowest token: the warp goes on while that one has
+    for (; t - sub < tokens; t += step) {
         RowVectors<T, VEC, ITEMS> z;
-        const bool ok = slot_ok != 0;
+        const bool ok = next_ok[0] != 0;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? slot[i] : V{};
-        fetch(t + AHEAD * step, slot, &slot_ok);
+        for (int k = 0; k + 1 < AHEAD; ++k) next_ok[k] = next_ok[k + 1];
+        if constexpr (RING) {
+            // into the stage that the last token was read from
+            fetch(t + AHEAD * step, slot == 0 ? BAL_STAGES - 1 : slot - 1, next_ok + AHEAD - 1);
+            copy_async_wait<AHEAD>();
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? ring[(slot * ITEMS + i) * BAL_THREADS] : V{};
+            if (++slot == BAL_STAGES) slot = 0;
+        } else {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) z.v[i] = ok ? next[i] : V{};
+            fetch(t + step, 0, next_ok);
+        }
         F2 v[PAIRS];
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
@@ -341,14 +387,7 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
                     if (whole || i * LANES + l < n) dst[i * LANES] = z.v[i];
             dst += step * n;
         }
-    };
-    // the warp's first subgroup has the lowest token: the warp goes on while that one has
-    while (t - sub < tokens)
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            if (t - sub < tokens) token(next[k], next_ok[k]);
-            t += step;
-        }
+    }
     if (!LOSS) return;
     // the subgroups of a warp (each of their lanes has their sum), then the warps
     q_sum = warp_sum(l == 0 ? q_sum : 0.f);
@@ -373,10 +412,15 @@ lce_status_t bal_pass_form(BalArgs a, BalMode mode, cudaStream_t s) {
     if (a.parts > fit) a.parts = static_cast<int32_t>(fit > 1 ? fit : 1);
     a.per_part = (a.T + a.parts - 1) / a.parts;
     const dim3 grid(a.parts, a.G);
-    const size_t smem = static_cast<size_t>(a.E) * 4 * (a.inline_count ? BAL_WARPS : 1);
+    a.ring_at = (static_cast<uint32_t>(a.E) * 4 * (a.inline_count ? BAL_WARPS : 1) + 15u) / 16u * 16u;
+    constexpr size_t vec = sizeof(Vec<T, VEC>);
+    const size_t smem = a.ring_at + (bal_ring(vec, ITEMS) ? BAL_STAGES * BAL_THREADS * vec : 0);
     auto kernel = mode == BAL_FORWARD    ? bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FORWARD>
                   : mode == BAL_BACKWARD ? bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_BACKWARD>
                                          : bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FUSED>;
+    if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(smem)) != cudaSuccess)
+        return LCE_ERR_CUDA;
     if (mode == BAL_BACKWARD || a.inline_count)
         LCE_PROFILED(kernel<<<grid, BAL_THREADS, smem, s>>>(a));
     else
