@@ -21,119 +21,40 @@ from typing import Optional
 import torch
 
 from . import LCEError, _flags, lce_check_status
-from ._tensors import address, balance_workspace, call, check_cuda, check_shape, dtype_code, stream_handle
+from ._native import native
 
 
-def _shapes(logits: torch.Tensor, mask):
-    """(groups, tokens, experts, type code, logits with rows in place, group stride, token stride, mask, mask
-    group stride)."""
-    code = dtype_code(logits, "router_logits")
-    dim, shape = logits.dim(), logits.shape
-    if dim not in (2, 3):
-        raise ValueError(f"router_logits must be [tokens, experts] or [groups, tokens, experts], got {list(shape)}")
-    T, E = shape[-2], shape[-1]
-    G = shape[0] if dim == 3 else 1
-    if not (G and T and E):
-        raise ValueError(f"router_logits is empty: {list(shape)}")
-    if logits.is_contiguous():
-        zg, zt = T * E, E
-    else:
-        if logits.stride(-1) != 1 or (T > 1 and logits.stride(-2) < E):
-            logits = logits.contiguous()
-        zg = logits.stride(0) if dim == 3 else 0
-        zt = logits.stride(-2) if T > 1 else E
-    mg = 0
-    if mask is not None:
-        if mask.dtype != torch.bool:
-            raise TypeError(f"mask must be bool, got {mask.dtype}")
-        if mask.dim() == 2 and dim == 3:
-            check_shape(mask, (G, T), "mask")
-            mg = T
-        else:
-            check_shape(mask, (T,), "mask")
-        if not mask.is_contiguous():
-            mask = mask.contiguous()
-    return G, T, E, code, logits, zg, zt, mask, mg
-
-
-def _check_grad_output(grad_output, dev):
-    if grad_output is not None:
-        if grad_output.numel() != 1 or grad_output.dtype != torch.float32:
-            raise TypeError("grad_output must be one float32 value")
-        check_cuda(dev, grad_output)
-
-
-def _loss_call(router_logits, experts, mask, reduction, stream, grad, grad_scale, grad_output):
+def _loss_call(router_logits, experts, mask, reduction, grad, grad_scale, grad_output):
     flags = _flags(reduction, False)
-    G, T, E, code, z, zg, zt, mask, mg = _shapes(router_logits, mask)
-    if experts.dtype == torch.int64:
-        index_bytes = 8
-    elif experts.dtype == torch.int32:
-        index_bytes = 4
-    else:
-        raise TypeError(f"experts must be int32 or int64, got {experts.dtype}")
-    lead = router_logits.shape[:-1]
-    if experts.shape[:-1] != lead or experts.shape[-1] == 0:
-        raise ValueError(f"experts must have shape {list(lead)} + [slots], got {list(experts.shape)}")
-    if not experts.is_contiguous():
-        experts = experts.contiguous()
-    k = experts.shape[-1]
-    dev = z.device
-    check_cuda(dev, experts, mask)
-    _check_grad_output(grad_output, dev)
-    nws = balance_workspace(G, T, E, k)
-    loss = torch.empty(1, dtype=torch.float32, device=dev)
-    group_loss = torch.empty(G, dtype=torch.float32, device=dev)
-    counts = torch.empty(lead[:-1] + (E,), dtype=torch.int64, device=dev)
-    n_valid = torch.empty(G, dtype=torch.int64, device=dev)
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev)
-    out = {"loss": loss, "group_loss": group_loss, "counts": counts, "n_valid": n_valid, "ws": ws}
+    r = native().balance_call(router_logits, experts, mask, bool(flags), grad, grad_scale, grad_output)
+    out = {"loss": r[0], "group_loss": r[1], "counts": r[2], "n_valid": r[3], "ws": r[4]}
     if grad:
-        out["grad_logits"] = dz = torch.empty_like(z, memory_format=torch.contiguous_format)
-        call("lce_balance_fused", G, T, E, k, code, z.data_ptr(), zg, zt, experts.data_ptr(), index_bytes,
-             address(mask), mg, grad_scale, address(grad_output), loss.data_ptr(), group_loss.data_ptr(),
-             counts.data_ptr(), n_valid.data_ptr(), dz.data_ptr(), ws.data_ptr(), nws, stream_handle(stream, dev), flags)
-    else:
-        call("lce_balance_forward", G, T, E, k, code, z.data_ptr(), zg, zt, experts.data_ptr(), index_bytes,
-             address(mask), mg, loss.data_ptr(), group_loss.data_ptr(), counts.data_ptr(), n_valid.data_ptr(),
-             ws.data_ptr(), nws, stream_handle(stream, dev), flags)
+        out["grad_logits"] = r[5]
     return out
 
 
 def balance_forward(router_logits: torch.Tensor, experts: torch.Tensor, mask: Optional[torch.Tensor] = None,
-                    reduction: str = "mean", stream=None) -> dict:
+                    reduction: str = "mean") -> dict:
     """loss [1], group_loss [groups], counts [groups, experts], n_valid [groups] and ws (whose device status
     lce_check_status reads) of router_logits [(groups,) tokens, experts] and experts [(groups,) tokens, slots]
     (-1: an unused slot); mask [tokens] or [groups, tokens] is False where a token is left out.  The loss is the
     mean over the groups, or with reduction="sum" their sum."""
-    return _loss_call(router_logits, experts, mask, reduction, stream, False, 1.0, None)
+    return _loss_call(router_logits, experts, mask, reduction, False, 1.0, None)
 
 
 def balance_fused(router_logits: torch.Tensor, experts: torch.Tensor, mask: Optional[torch.Tensor] = None,
-                  grad_scale: float = 1.0, grad_output: Optional[torch.Tensor] = None, reduction: str = "mean",
-                  stream=None) -> dict:
+                  grad_scale: float = 1.0, grad_output: Optional[torch.Tensor] = None, reduction: str = "mean") -> dict:
     """What balance_forward gives, and grad_logits: the gradient of grad_scale * grad_output * loss."""
-    return _loss_call(router_logits, experts, mask, reduction, stream, True, grad_scale, grad_output)
+    return _loss_call(router_logits, experts, mask, reduction, True, grad_scale, grad_output)
 
 
 def balance_backward(router_logits: torch.Tensor, counts: torch.Tensor, n_valid: torch.Tensor, slots: int,
                      mask: Optional[torch.Tensor] = None, grad_scale: float = 1.0,
-                     grad_output: Optional[torch.Tensor] = None, reduction: str = "mean", stream=None) -> dict:
+                     grad_output: Optional[torch.Tensor] = None, reduction: str = "mean") -> dict:
     """{"grad_logits"} of grad_scale * grad_output * loss from a forward's counts and n_valid."""
     flags = _flags(reduction, False)
-    G, T, E, code, z, zg, zt, mask, mg = _shapes(router_logits, mask)
-    dev = z.device
-    check_shape(counts, tuple(router_logits.shape[:-2]) + (E,), "counts")
-    check_shape(n_valid, (G,), "n_valid")
-    for what, t in (("counts", counts), ("n_valid", n_valid)):
-        if t.dtype != torch.int64 or not t.is_contiguous():
-            raise TypeError(f"{what} must be a contiguous int64 tensor")
-    check_cuda(dev, counts, n_valid, mask)
-    _check_grad_output(grad_output, dev)
-    grad = torch.empty_like(z, memory_format=torch.contiguous_format)
-    call("lce_balance_backward", G, T, E, slots, code, z.data_ptr(), zg, zt, counts.data_ptr(), n_valid.data_ptr(),
-         address(mask), mg, grad_scale, address(grad_output), grad.data_ptr(), stream_handle(stream, dev), flags)
-    return {"grad_logits": grad}
+    return {"grad_logits": native().balance_backward(router_logits, counts, n_valid, slots, mask, bool(flags), grad_scale,
+                                                     grad_output)}
 
 
 class _BalanceLoss(torch.autograd.Function):

@@ -7,6 +7,9 @@ Each .cu file is compiled separately (in parallel) with nvcc and linked
 into one shared library with the CUDA runtime linked statically, so that
 loading it needs no GPU and no driver (the driver is only touched when a
 function enqueues work).
+
+The torch side of the operators beside the head (lce_torch.cpp) is compiled
+with the host compiler into _lce_torch.so, against the installed torch.
 """
 from __future__ import annotations
 
@@ -23,6 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblce.so")
 LIB_DEBUG = os.path.join(PKG, "liblce_debug.so")
+TORCH_SRC = os.path.join(CSRC, "lce_torch.cpp")
+TORCH_LIB = os.path.join(PKG, "_lce_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -41,7 +46,7 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
     return files + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [__file__]
 
 
@@ -81,10 +86,51 @@ def _link(nvcc: str, lib: str, objs: list[str]) -> None:
     os.replace(tmp, lib)
 
 
+def build_torch(force: bool = False, verbose: bool = False) -> str:
+    """Builds _lce_torch.so unless it is newer than its sources and was made
+    for the installed torch."""
+    import sysconfig
+
+    import torch
+
+    tag = TORCH_LIB + ".for"
+    made_for = f"torch {torch.__version__} python {sys.version}"
+    deps = [TORCH_SRC, os.path.join(INCLUDE, "lce.h"), __file__]
+    if not force and os.path.exists(TORCH_LIB) and os.path.exists(tag) and open(tag).read() == made_for \
+            and all(os.path.getmtime(f) <= os.path.getmtime(TORCH_LIB) for f in deps):
+        return TORCH_LIB
+    root = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"), INCLUDE]
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", TORCH_SRC, "-o", tmp,
+           *(f"-I{i}" for i in include), f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode:
+        raise RuntimeError("g++ failed on lce_torch.cpp")
+    os.replace(tmp, TORCH_LIB)
+    with open(tag, "w") as f:
+        f.write(made_for)
+    return TORCH_LIB
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False, both: bool = False) -> str:
     """Builds the release library (or, with debug, the bounds-checking one;
     with both, the two together in one pool of compiler processes) unless it
     is newer than every source.  Returns the path of the (release) library."""
+    with ThreadPoolExecutor(max_workers=1) as beside:  # the host compiler beside nvcc
+        binding = beside.submit(build_torch, force, verbose)
+        lib = _build_library(force, verbose, debug, both)
+        binding.result()
+    return lib
+
+
+def _build_library(force: bool, verbose: bool, debug: bool, both: bool) -> str:
     variants = [False, True] if both else [debug]
     todo = [v for v in variants if force or not up_to_date(v)]
     if todo:

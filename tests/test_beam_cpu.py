@@ -4,7 +4,8 @@ import torch
 
 import __graft_entry__
 import lm_head_linear_chunked_gb300 as lce
-from lm_head_linear_chunked_gb300.beam import _layout, _overlap, beam_reorder, beam_select
+from lm_head_linear_chunked_gb300._native import native
+from lm_head_linear_chunked_gb300.beam import beam_reorder, beam_select
 
 A = 1 << 20
 
@@ -97,31 +98,28 @@ def test_front_end_refusals(call, error):
         call()
 
 
-def test_overlap_is_refused(monkeypatch):
-    import lm_head_linear_chunked_gb300.beam as beam
-    monkeypatch.setattr(beam, "check_cuda", lambda *a, **k: None)
+def test_overlap_is_refused():
     both = torch.zeros(10, 4, 5)
     for a, b in ((both[:6], both[:6]), (both[:6], both[4:]), (both[4:], both[:6])):
         with pytest.raises(ValueError, match="overlaps"):
-            beam.beam_reorder([a], P, out=[b])
+            beam_reorder([a], P, out=[b])
 
 
 def test_ranges():
-    assert not _overlap([]) and not _overlap([(0, 8, 0), (8, 16, 1), (16, 24, 0)])
-    assert not _overlap([(0, 8, 0), (4, 12, 0), (12, 20, 1)])
-    assert _overlap([(0, 100, 0), (4, 12, 0), (50, 60, 1)]) and _overlap([(5, 6, 1), (5, 6, 0)])
-
-
-def layout(a, b):
-    return _layout(tuple(a.shape), a.stride(), b.stride(), 1)
+    overlap = native().overlap
+    assert not overlap([]) and not overlap([(0, 8, 0), (8, 16, 1), (16, 24, 0)])
+    assert not overlap([(0, 8, 0), (4, 12, 0), (12, 20, 1)])
+    assert overlap([(0, 100, 0), (4, 12, 0), (50, 60, 1)]) and overlap([(5, 6, 1), (5, 6, 0)])
 
 
 def test_layout_of_a_row():
+    """(outer runs, strides, inner runs, strides, run) in bytes, of 4-byte elements."""
     x = torch.zeros(6, 8, 40, 16)
     y = torch.zeros(6, 8, 64, 16)
-    assert layout(x, torch.zeros(6, 8, 40, 16)) == (1, 0, 0, 1, 0, 0, 8 * 40 * 16)
-    assert layout(x[:, :, :7], y[:, :, :7]) == (1, 0, 0, 8, 640, 1024, 7 * 16)
-    assert layout(x[:, :, :1, :1], y[:, :, :1, :1]) == (1, 0, 0, 8, 640, 1024, 1)
-    assert layout(x[:, :, :, ::2], y[:, :, :40, ::2]) == (8, 640, 1024, 320, 2, 2, 1)
+    layout = native().layout
+    assert layout(x, torch.zeros(6, 8, 40, 16)) == (1, 0, 0, 1, 0, 0, 4 * 8 * 40 * 16)
+    assert layout(x[:, :, :7], y[:, :, :7]) == (1, 0, 0, 8, 4 * 640, 4 * 1024, 4 * 7 * 16)
+    assert layout(x[:, :, :1, :1], y[:, :, :1, :1]) == (1, 0, 0, 8, 4 * 640, 4 * 1024, 4)
+    assert layout(x[:, :, :, ::2], y[:, :, :40, ::2]) == (8, 4 * 640, 4 * 1024, 320, 8, 8, 4)
     assert layout(x[:, ::2, ::2, ::3], x[:, ::2, ::2, ::3]) is None
-    assert _layout((6, 8, 5), (40, 5, 1), (80, 10, 1), 2) == (1, 0, 0, 8, 10, 20, 10)
+    assert layout(x[:, 0].bfloat16(), y[:, 0, :40].bfloat16()) == (1, 0, 0, 1, 0, 0, 2 * 40 * 16)
