@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(128) norm_fwd_warp(NormFwd<T> a) {
 // put together as  M2 = sum_w M2_w + sum_w n_w (mean_w - mean)^2.
 template <typename T, typename W, int VEC, int ITEMS, int R, int STAGES, int MAX_WARPS, int BLOCKS>
 __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) norm_fwd_rows(NormFwd<T> a) {
-    constexpr bool RING = sizeof(Vec<T, VEC>) >= 4;  // single 16-bit elements are read when they are needed
+    constexpr bool RING = sizeof(Vec<T, VEC>) >= 4;  // single 16-bit elements wait in registers
     using Row = RowRegs<T, VEC, ITEMS>;
     using V = Vec<T, VEC>;
     __shared__ float2 part[2][R][MAX_WARPS];
@@ -201,6 +201,8 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) norm_fwd_rows(NormFwd<
     const float weight = other < warps ? share_of(other) * inv : 0.f;
     const bool whole = ITEMS * threads == n;
     int stage = 0, flip = 0;
+    Row next;
+    if constexpr (!RING) next.load(a.x + blockIdx.x * a.ldx, t, threads, n);
     for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
         int ahead = stage + STAGES - 1;
         if (ahead >= STAGES) ahead -= STAGES;
@@ -218,8 +220,9 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) norm_fwd_rows(NormFwd<
                     if (i * threads + t < n) x.v[i] = ring[((stage * R + k) * ITEMS + i) * threads + t];
                 }
             } else {
-                const int64_t r = g * R + k < a.rows ? g * R + k : a.rows - 1;
-                x.load(a.x + r * a.ldx, t, threads, n);
+                static_assert(RING || R == 1, "the next row waits in registers");
+                x = next;
+                if (g + gridDim.x < groups) next.load(a.x + (g + gridDim.x) * a.ldx, t, threads, n);
             }
             F2 s[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_bwd_rows(NormBwd<T> a) 
     using Row = RowRegs<T, VEC, ITEMS>;
     using V = Vec<T, VEC>;
     launch_dependents();
-    constexpr bool RING = sizeof(V) >= 4;  // single 16-bit elements are read when they are needed
+    constexpr bool RING = sizeof(V) >= 4;  // single 16-bit elements wait in registers
     static_assert(KEEP || RING, "the rows are read again from the ring");
     const int tpr = WARP ? 32 : blockDim.x;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
@@ -432,6 +435,12 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_bwd_rows(NormBwd<T> a) 
         mean_next = a.mean[r0];
         rstd_next = a.rstd[r0];
     }
+    Row x_next, d_next;  // without a ring, the next row waits in registers
+    if constexpr (!RING)
+        if (r0 < a.rows) {
+            x_next.load(a.x + r0 * a.ldx, t, tpr, n);
+            d_next.load(a.dy + r0 * a.ldd, t, tpr, n);
+        }
     for (int64_t r = r0; r < a.rows; r += step) {
         const float mean = mean_next, rstd = rstd_next;
         if (r + step < a.rows) {
@@ -456,8 +465,12 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) norm_bwd_rows(NormBwd<T> a) 
             copy_async_wait<STAGES - 1>();
             from_ring();
         } else {
-            x.load(a.x + r * a.ldx, t, tpr, n);
-            d.load(a.dy + r * a.ldd, t, tpr, n);
+            x = x_next;
+            d = d_next;
+            if (r + step < a.rows) {
+                x_next.load(a.x + (r + step) * a.ldx, t, tpr, n);
+                d_next.load(a.dy + (r + step) * a.ldd, t, tpr, n);
+            }
         }
         // outside the row dy = 0, so nothing is added
         F2 s2 = f2(0.f), q2 = f2(0.f), kx[KEEP ? Row::PAIRS : 1], kg[KEEP ? Row::PAIRS : 1];
