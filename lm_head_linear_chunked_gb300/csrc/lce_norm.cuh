@@ -628,7 +628,10 @@ lce_status_t fwd_rows(const NormFwd<T>& a, cudaStream_t s) {
 //    warp per row: 5.7, two vectors: 5.3);
 //  - where a quarter of such a block would be idle, two rows of two vectors a
 //    thread: 5.9 TB/s at 2560 against 4.9;
-//  - narrower vectors: eight a thread, or sixteen single elements;
+//  - narrower vectors: eight a thread, or sixteen single elements; 2.6 TB/s at
+//    1601 fp16, bound by the instructions per element.  16-byte vectors
+//    counted from each row's own start reached 2.4: a row's two ends cost the
+//    warp that has them more than the vectors save;
 //  - wider rows: the row is read again.
 template <typename T, typename W>
 lce_status_t norm_forward(const NormCall& c) {
@@ -691,7 +694,8 @@ lce_status_t bwd_rows(const NormBwd<T>& a, int* parts, cudaStream_t s) {
 //  - up to 1024: a block per row, two vectors a thread, 6.6 TB/s at 4096 (one
 //    vector: 4.3, as the sums over a row then cost as much as the row);
 //  - up to 2048: four vectors a thread, read twice from the ring;
-//  - narrower vectors: eight a thread, or sixteen single elements;
+//  - narrower vectors: eight a thread, or sixteen single elements (3.0 TB/s at
+//    1601 fp16);
 //  - wider rows: dx, reading the row again, and the column sums by themselves.
 template <typename T, typename W>
 lce_status_t norm_backward(const NormCall& c) {
