@@ -29,18 +29,18 @@ namespace lce {
 
 constexpr int BAL_WARPS = 8;
 constexpr int BAL_THREADS = 32 * BAL_WARPS;
+// Tokens of a lane group in the ring of the pass: one in work, the others on their way.
+constexpr int BAL_STAGES = 4;
 // Blocks of the pass over all groups (a group's blocks share its tokens out):
 // at most four on each of 152 SMs, which all run at once (sixteen more than
 // that took a second round, and half as long again); and the fewest tokens
 // that are worth one.
-// Tokens of a lane group in the ring of the pass: one in work, the others on their way.
-constexpr int BAL_STAGES = 4;
 constexpr int64_t BAL_SMS = 152;
 constexpr int64_t BAL_BLOCKS = 4 * BAL_SMS;
-// Whether the tokens read ahead wait in shared memory (2^26 bf16 logits of 128
-// experts: 44 us, against 57 from registers, where the waits could not be
-// hidden) or, with several vectors a lane, in registers (2^25 fp32 logits of
-// 256: 38 us against 40).
+// Whether the tokens read ahead wait in shared memory (24 x 16384 x 128 bf16,
+// loss and gradient with the counting: 54 us, against 66 from registers, where
+// the waits could not be hidden) or, with several vectors a lane, in registers
+// (2^25 fp32 logits of 256: 38 us against 40).
 constexpr bool bal_ring(size_t vec, int items) { return vec >= 4 && items == 1; }
 // Blocks of the pass on an SM, by the experts of a lane (which it keeps in registers).
 constexpr int bal_resident(int experts) { return experts <= 8 ? 4 : experts <= 16 ? 2 : 1; }
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
     auto column = [&](int e) { return ((e / VEC) * LANES + l) * VEC + e % VEC; };
     {
         // f - 1 = (c E - k n) / (k n), the numerator exact in integers, from the group's
-        // counts: finished (the backward), or the sums of their parts.  (In FP64 this took
-        // 20 of 60 us on 2^26 logits: its rate is 1/64.)
+        // counts: finished (the backward), or the sums of their parts.  (In FP64, at 1/64
+        // of the rate, 24 x 16384 x 128 took 80 us, not 76.)
         if (warp == 0) {
             int32_t m = 0;
             if (LOSS)
