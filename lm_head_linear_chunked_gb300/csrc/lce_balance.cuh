@@ -235,6 +235,40 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
     const int n = a.E / VEC;
     const bool whole = n == LANES * ITEMS;  // no lane has a vector outside the row
     const int64_t t0 = part * a.per_part, t1 = t0 + a.per_part < a.T ? t0 + a.per_part : a.T;
+    // from here on tokens count from the part's first, in 32 bits
+    const int tokens = t1 > t0 ? static_cast<int>(t1 - t0) : 0;
+    constexpr int step = BAL_WARPS * tpw;
+    int t = warp * tpw + sub;
+    const V* src = reinterpret_cast<const V*>(static_cast<const T*>(a.z) + g * a.zg + (t0 + t) * a.zt) + l;
+    const int64_t src_step = step * a.zt / VEC;
+    V* dst = GRAD ? reinterpret_cast<V*>(static_cast<T*>(a.dz) + (static_cast<int64_t>(g) * a.T + t0 + t) * a.E) + l : nullptr;
+    const uint8_t* keep = a.mask ? a.mask + g * a.mask_g + t0 : nullptr;
+    // a thread's own vectors of the next tokens, in shared memory; or in registers
+    // (RING); the mask's bytes wait as they were read
+    V* ring = reinterpret_cast<V*>(reinterpret_cast<char*>(sm) + a.ring_at) + threadIdx.x;
+    V next[RING ? 1 : ITEMS];
+    uint32_t next_ok[AHEAD];
+    auto fetch = [&](int at, int slot, uint32_t* valid) {
+        *valid = at < tokens;
+        if (at < tokens) {
+            if (keep) *valid = keep[at];
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+                if (whole || i * LANES + l < n) {
+                    if constexpr (RING)
+                        copy_async<sizeof(V)>(ring + (slot * ITEMS + i) * BAL_THREADS, src + i * LANES);
+                    else
+                        next[i] = src[i * LANES];
+                }
+        }
+        if constexpr (RING) copy_async_commit();
+        src += src_step;
+    };
+    // the first tokens are on their way while the counts are waited for and added up:
+    // the logits and the mask were there before the counting began (24 x 16384 x 128
+    // 53.5 -> 52.9 us, 131072 x 256 fp32 gradient 46.6 -> 46.0; small calls alike)
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) fetch(t + k * step, k, next_ok + k);
     if (LOSS && !a.inline_count) wait_for_primary();  // the counts
     if (LOSS && a.inline_count) {
         if (threadIdx.x == 0) *a.done = 0;
@@ -289,37 +323,6 @@ __global__ void __launch_bounds__(BAL_THREADS, bal_resident(ITEMS * VEC)) bal_pa
         const int c0 = column(2 * p), c1 = column(2 * p + 1);
         f[p] = f2(c0 < a.E ? sm[c0] : 0.f, c1 < a.E ? sm[c1] : 0.f);
     }
-    // from here on tokens count from the part's first, in 32 bits
-    const int tokens = t1 > t0 ? static_cast<int>(t1 - t0) : 0;
-    constexpr int step = BAL_WARPS * tpw;
-    int t = warp * tpw + sub;
-    const V* src = reinterpret_cast<const V*>(static_cast<const T*>(a.z) + g * a.zg + (t0 + t) * a.zt) + l;
-    const int64_t src_step = step * a.zt / VEC;
-    V* dst = GRAD ? reinterpret_cast<V*>(static_cast<T*>(a.dz) + (static_cast<int64_t>(g) * a.T + t0 + t) * a.E) + l : nullptr;
-    const uint8_t* keep = a.mask ? a.mask + g * a.mask_g + t0 : nullptr;
-    // a thread's own vectors of the next tokens, in shared memory; or in registers
-    // (RING); the mask's bytes wait as they were read
-    V* ring = reinterpret_cast<V*>(reinterpret_cast<char*>(sm) + a.ring_at) + threadIdx.x;
-    V next[RING ? 1 : ITEMS];
-    uint32_t next_ok[AHEAD];
-    auto fetch = [&](int at, int slot, uint32_t* valid) {
-        *valid = at < tokens;
-        if (at < tokens) {
-            if (keep) *valid = keep[at];
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
-                if (whole || i * LANES + l < n) {
-                    if constexpr (RING)
-                        copy_async<sizeof(V)>(ring + (slot * ITEMS + i) * BAL_THREADS, src + i * LANES);
-                    else
-                        next[i] = src[i * LANES];
-                }
-        }
-        if constexpr (RING) copy_async_commit();
-        src += src_step;
-    };
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) fetch(t + k * step, k, next_ok + k);
     int slot = 0;
     // the warp's first subgroup has the lowest token: the warp goes on while that one has
     for (; t - sub < tokens; t += step) {
