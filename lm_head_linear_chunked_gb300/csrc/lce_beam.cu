@@ -344,11 +344,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 4) beam_scan_kernel(ScanArgs a) 
         }
         pushed = logit_key(mx, 0) > limit;
         if (pushed) {
+            // what is not below the least candidate: a NaN stays, for its key to decide as -inf
             const float least = key_logit(limit + 1);
             uint32_t which = 0;
 #pragma unroll
             for (int e = 0; e < C::PER; ++e)
-                which |= static_cast<uint32_t>((e & 1 ? hi(x[e / 2]) : lo(x[e / 2])) >= least) << e;
+                which |= static_cast<uint32_t>(!((e & 1 ? hi(x[e / 2]) : lo(x[e / 2])) < least)) << e;
             if (limit == 0) which = static_cast<uint32_t>((1ull << C::PER) - 1);
             for (; which; which &= which - 1) {
                 const int e = __ffs(which) - 1;

@@ -307,3 +307,49 @@ def test_offsets_beyond_32_bits():
     y = beam_reorder([x], torch.tensor([[4, 0, 3, 4, 2]], device="cuda"))[0]
     for i, want in enumerate((5, 1, 4, 5, 3)):
         assert int(y[i].min()) == int(y[i].max()) == want
+
+
+def select_into(z, s, n, finished=None, pad=0):
+    """beam_select through the C ABI into outputs filled beforehand: a result that is not written shows."""
+    B, K, V = z.shape
+    code = {torch.bfloat16: lce.BF16, torch.float16: lce.F16, torch.float32: lce.F32}[z.dtype]
+    scores = torch.full((B, n), 12345.0, device="cuda")
+    tokens, parents = (torch.full((B, n), -77, dtype=torch.int64, device="cuda") for _ in range(2))
+    size = lce.lce_beam_workspace_size(B, K, V, n)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    lce.lce_beam_select(B, K, V, n, code, z, V, s, finished, pad, -1, scores, tokens, parents, None, ws, size,
+                        torch.cuda.current_stream())
+    return {"scores": scores, "tokens": tokens, "parents": parents}
+
+
+@pytest.mark.parametrize("K,n", [(1, 1), (1, 4), (4, 4), (1, 64), (4, 64), (5, 64), (64, 64)])  # K n on both sides of 256
+@pytest.mark.parametrize("V", [100, 600, 9001, 32768, 50257])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_an_item_of_nan_alone(K, n, V, dtype):
+    """NaN counts as -inf: scores of -inf, the lowest tokens of the first beam."""
+    z = torch.full((2, K, V), float("nan"), dtype=DTYPES[dtype], device="cuda")
+    s = torch.zeros((2, K), device="cuda")
+    got = select_into(z, s, n)
+    assert torch.isneginf(got["scores"]).all() and not got["parents"].any()
+    assert torch.equal(got["tokens"], torch.arange(n, device="cuda").expand(2, n))
+    # the second beam alone is alive
+    if K > 1:
+        z[:, 1] = torch.linspace(-3, 3, V, device="cuda")
+        check(z, s, n, exact=True)
+
+
+@pytest.mark.parametrize("rows", [1, 160])  # a row in many parts, and in one
+@pytest.mark.parametrize("n", [1, 8, 64])
+@pytest.mark.parametrize("V", [700, 9001, 24576])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_nan_and_minus_infinity_beside_few_tokens(rows, n, V, dtype):
+    """Fewer finite logits than results: what follows them goes by the token, NaN and -inf alike."""
+    z = torch.full((rows, 4, V), -float("inf"), dtype=DTYPES[dtype], device="cuda")
+    z[normal(z.shape, 131) > 0] = float("nan")
+    for k, at in enumerate((0, V // 3, V // 2, V - 1)):
+        z[:, k, at] = 0.5 * k
+    z[:, 3, :at // 2] = float("nan")
+    s = torch.tensor([0.0, -4.0, -8.0, -12.0], device="cuda").expand(rows, 4).contiguous()
+    check(z[:2], s[:2], n, exact=True)
+    got, want = select_into(z, s, n), select_into(z[:1].contiguous(), s[:1].contiguous(), n)
+    assert all(torch.equal(got[k][:1], want[k]) for k in want)
