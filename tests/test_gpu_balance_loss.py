@@ -218,3 +218,37 @@ def test_side_stream_repeats_and_graph_capture():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(out[k], ref[k]) for k in names)
+
+
+@pytest.mark.parametrize("E", [7, 60, 64, 128, 200, 1024])  # single elements, 8- and 16-byte vectors, one and several a lane
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_of_large_logits(E, dtype):
+    """Rows of one large value have the softmax of a row of zeros, 1 / E, exactly as that row does (the largest is
+    subtracted first, so nothing is rounded); a row with one expert far above the rest has 1 and 0."""
+    t = DTYPES[dtype]
+    small, experts, _ = problem(1, 300, E, 2, dtype, 43)
+    large = small.clone()
+    low, high = torch.finfo(t).min, torch.finfo(t).max
+    for i, v in enumerate((low, high, -1e30, 1e30, -1e10, 1e10, 3e9, -2.0 ** 40)):
+        small[0, 7 * i] = 0
+        large[0, 7 * i] = v
+    # e^-x is 0 in 64 bits for x > 745, so the small row stands for all of these
+    for i, (rest, one) in enumerate(((low, 0.0), (low, high), (-1e10, 1e10), (-1e10, -1e9), (1e9, 1e10))):
+        small[0, 100 + i], large[0, 100 + i] = -1000, rest
+        small[0, 100 + i, E // 2], large[0, 100 + i, E // 2] = 0, one
+    from lm_head_linear_chunked_gb300.balance_loss import balance_backward, balance_forward, balance_fused
+    f = balance_forward(large, experts)
+    b = balance_backward(large, f["counts"], f["n_valid"], 2)
+    plain = small.clone()
+    plain[0, 100:105] = plain[0, 100:105].clamp(min=-16)  # only for the size of the tolerance
+    a = float(plain.abs().max())
+    for got in ({**f, **b}, balance_fused(large, experts)):
+        for k in ("loss", "group_loss", "grad_logits"):
+            assert not torch.isnan(got[k]).any(), k
+        r = formulas(small, experts, None)
+        e_p = (8 * a + 64 + E / 32) * U32
+        e = e_p + (300 + 16) * U32
+        assert_within(got["loss"].reshape(()), r["loss"], (e + U32) * r["loss"].abs(), "loss")
+        u = half_step(t)
+        assert_within(got["grad_logits"].reshape(small.shape), r["grad"],
+                      u * r["grad"].abs() + (1 + u) * (3 * e_p + 8 * U32) * r["size"] + tiny(t), "grad_logits")
