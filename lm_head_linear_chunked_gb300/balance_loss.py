@@ -12,7 +12,7 @@ coefficient, to the head's cross-entropy:
 `balance_forward`, `balance_backward` and `balance_fused` are the library's
 calls on their own; the fused one gives loss and gradient in one pass over
 the logits when the coefficient is known beforehand.  The shares f take no
-gradient.
+gradient.  There is no forward-mode derivative: a tangent is refused.
 """
 from __future__ import annotations
 

@@ -8,6 +8,7 @@
 `beam_select` is one lce_beam_select call (two kernels: a scan of the
 vocabulary and the joining of its parts), `beam_reorder` one
 lce_beam_reorder call for all states; torch only allocates the outputs.
+Neither is differentiable; a forward-mode tangent is refused.
 """
 from __future__ import annotations
 

@@ -100,6 +100,19 @@ void on_device(const OptTensor& t, const at::Device& device, const char* what) {
     if (t) on_device(*t, device, what);
 }
 
+// The calls below work on addresses, where a forward-mode tangent would be
+// lost without a word; there are no forward-mode derivatives.
+void no_tangent(const Tensor& t, const char* what) {
+    if (t._fw_grad(/*level=*/0).defined()) {
+        PyErr_SetString(PyExc_NotImplementedError,
+                        (std::string(what) + " has a forward-mode tangent: this operator has no forward-mode derivative").c_str());
+        throw py::error_already_set();
+    }
+}
+void no_tangent(const OptTensor& t, const char* what) {
+    if (t) no_tangent(*t, what);
+}
+
 // The current stream: outputs and workspaces belong to it.
 lce_stream_t stream_of(const at::Device& device) {
     return reinterpret_cast<lce_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
@@ -142,6 +155,9 @@ void check_affine(const Tensor& x, int64_t H, const Tensor& t, const char* what)
 
 std::tuple<Tensor, OptTensor, OptTensor> norm_forward(const Tensor& x_in, const OptTensor& weight, const OptTensor& bias,
                                                       double eps, bool stats) {
+    no_tangent(x_in, "x");
+    no_tangent(weight, "weight");
+    no_tangent(bias, "bias");
     const int code = type_code(x_in, "x");
     const int64_t H = width(x_in);
     int wcode = code;
@@ -179,6 +195,11 @@ std::tuple<OptTensor, OptTensor, OptTensor> norm_backward(const Tensor& dy_in, c
                                                           const Tensor& mean, const Tensor& rstd, bool want_x,
                                                           bool want_w, bool want_b,
                                                           std::optional<at::ScalarType> grad_type) {
+    no_tangent(dy_in, "grad_y");
+    no_tangent(x_in, "x");
+    no_tangent(weight, "weight");
+    no_tangent(mean, "mean");
+    no_tangent(rstd, "rstd");
     const int code = type_code(x_in, "x");
     const int64_t H = width(x_in);
     check_shape(dy_in, x_in.sizes(), "grad_y");
@@ -232,6 +253,7 @@ struct Router {
 };
 
 Router router_of(const Tensor& logits, const OptTensor& mask) {
+    no_tangent(logits, "router_logits");
     Router r;
     r.code = type_code(logits, "router_logits");
     const int64_t dim = logits.dim();
@@ -269,6 +291,7 @@ const float* grad_output_of(const OptTensor& t, const at::Device& dev) {
 // loss, group_loss, counts, n_valid, ws and (with grad) grad_logits
 std::vector<Tensor> balance_call(const Tensor& logits, const Tensor& experts_in, const OptTensor& mask, bool sum, bool grad,
                                  double grad_scale, const OptTensor& grad_output) {
+    no_tangent(grad_output, "grad_output");
     const Router r = router_of(logits, mask);
     const int index_bytes = experts_in.scalar_type() == at::kLong ? 8 : experts_in.scalar_type() == at::kInt ? 4 : 0;
     if (!index_bytes) throw py::type_error(std::string("experts must be int32 or int64, got ") + toString(experts_in.scalar_type()));
@@ -309,6 +332,7 @@ std::vector<Tensor> balance_call(const Tensor& logits, const Tensor& experts_in,
 
 Tensor balance_backward(const Tensor& logits, const Tensor& counts, const Tensor& n_valid, int64_t slots, const OptTensor& mask,
                         bool sum, double grad_scale, const OptTensor& grad_output) {
+    no_tangent(grad_output, "grad_output");
     const Router r = router_of(logits, mask);
     if (logits.dim() == 3)
         check_shape(counts, {r.G, r.E}, "counts");
@@ -340,6 +364,8 @@ Tensor balance_backward(const Tensor& logits, const Tensor& counts, const Tensor
 // scores, tokens, parents and, with eos >= 0, finished
 std::vector<Tensor> beam_select(const Tensor& logits_in, const Tensor& scores_in, int64_t n, const OptTensor& finished,
                                 int64_t pad, int64_t eos) {
+    no_tangent(logits_in, "logits");
+    no_tangent(scores_in, "scores");
     const int code = type_code(logits_in, "logits");
     if (logits_in.dim() != 3 || logits_in.numel() == 0)
         throw py::value_error("logits must be [items, beams, V] and not empty, got " + text(logits_in.sizes()));
@@ -450,6 +476,7 @@ std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor
     std::vector<Range> ranges;
     for (size_t i = 0; i < states.size(); ++i) {
         Tensor a = states[i];
+        no_tangent(a, "a state");
         if (a.dim() == 0 || a.size(0) != rows)
             throw py::value_error("states must have " + std::to_string(rows) + " rows each, states[" + std::to_string(i) +
                                   "] has shape " + text(a.sizes()));
@@ -459,6 +486,7 @@ std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor
         Tensor b;
         if (given) {
             b = (*given)[i];
+            no_tangent(b, "an output");
             check_shape(b, shape, ("out[" + std::to_string(i) + "]").c_str());
             check_type(b, a.scalar_type(), ("out[" + std::to_string(i) + "]").c_str());
             if (b.device() != dev) throw py::value_error("states and outputs must be on " + dev.str());
