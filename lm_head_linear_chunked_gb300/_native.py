@@ -8,7 +8,7 @@ import ctypes
 import importlib.util
 import os
 
-import torch  # noqa: F401  (the module below links against it)
+import torch  # the module below links against it
 
 from . import LCEError, lib
 
@@ -32,3 +32,10 @@ def native():
         module.init({n: ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in _NAMES}, LCEError)
         _module = module
     return _module
+
+
+def not_traced(name: str) -> None:
+    """Refuses a call under torch.jit.trace: the trace sees the allocation of
+    the outputs but not the call that fills them."""
+    if torch.jit.is_tracing():
+        raise RuntimeError(f"{name} cannot be traced")

@@ -21,7 +21,7 @@ from typing import Optional
 import torch
 
 from . import LCEError, _flags, lce_check_status
-from ._native import native
+from ._native import native, not_traced
 
 
 def _loss_call(router_logits, experts, mask, reduction, grad, grad_scale, grad_output):
@@ -39,12 +39,14 @@ def balance_forward(router_logits: torch.Tensor, experts: torch.Tensor, mask: Op
     lce_check_status reads) of router_logits [(groups,) tokens, experts] and experts [(groups,) tokens, slots]
     (-1: an unused slot); mask [tokens] or [groups, tokens] is False where a token is left out.  The loss is the
     mean over the groups, or with reduction="sum" their sum."""
+    not_traced("balance_forward")
     return _loss_call(router_logits, experts, mask, reduction, False, 1.0, None)
 
 
 def balance_fused(router_logits: torch.Tensor, experts: torch.Tensor, mask: Optional[torch.Tensor] = None,
                   grad_scale: float = 1.0, grad_output: Optional[torch.Tensor] = None, reduction: str = "mean") -> dict:
     """What balance_forward gives, and grad_logits: the gradient of grad_scale * grad_output * loss."""
+    not_traced("balance_fused")
     return _loss_call(router_logits, experts, mask, reduction, True, grad_scale, grad_output)
 
 
@@ -52,6 +54,7 @@ def balance_backward(router_logits: torch.Tensor, counts: torch.Tensor, n_valid:
                      mask: Optional[torch.Tensor] = None, grad_scale: float = 1.0,
                      grad_output: Optional[torch.Tensor] = None, reduction: str = "mean") -> dict:
     """{"grad_logits"} of grad_scale * grad_output * loss from a forward's counts and n_valid."""
+    not_traced("balance_backward")
     flags = _flags(reduction, False)
     return {"grad_logits": native().balance_backward(router_logits, counts, n_valid, slots, mask, bool(flags), grad_scale,
                                                      grad_output)}
@@ -60,7 +63,7 @@ def balance_backward(router_logits: torch.Tensor, counts: torch.Tensor, n_valid:
 class _BalanceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, router_logits, experts, mask, reduction):
-        out = balance_forward(router_logits, experts, mask, reduction)
+        out = _loss_call(router_logits, experts, mask, reduction, False, 1.0, None)
         ctx.save_for_backward(router_logits, mask, out["counts"], out["n_valid"])
         ctx.slots, ctx.reduction = experts.shape[-1], reduction
         ctx.mark_non_differentiable(out["counts"], out["ws"])
@@ -79,8 +82,9 @@ def balance_loss(router_logits: torch.Tensor, experts: torch.Tensor, mask: Optio
                  reduction: str = "mean", check: bool = False):
     """(loss, counts): the balance loss, differentiable in router_logits, and the int64 counts
     [(groups,) experts].  Arguments as balance_forward's.  check=True synchronises and raises on an expert index
-    outside [-1, experts); without it such an index makes the loss NaN."""
-    if torch.is_grad_enabled() and router_logits.requires_grad:
+    outside [-1, experts); without it such an index makes the loss NaN.  torch.jit.trace records it
+    as one call."""
+    if (torch.is_grad_enabled() and router_logits.requires_grad) or torch.jit.is_tracing():
         loss, counts, ws = _BalanceLoss.apply(router_logits, experts, mask, reduction)
     else:
         out = balance_forward(router_logits, experts, mask, reduction)

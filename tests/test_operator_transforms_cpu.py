@@ -1,6 +1,6 @@
 """What torch's transforms may not do with the operators beside the head,
 without a GPU: their calls work on addresses, so a forward-mode tangent is
-refused instead of lost."""
+refused instead of lost, and a trace would record outputs that nothing fills."""
 import pytest
 import torch
 import torch.autograd.forward_ad as fw
@@ -53,3 +53,17 @@ def test_forward_mode_tangents_are_refused(t, call):
             call(fw.make_dual(t.clone(), torch.ones_like(t)))
         with pytest.raises(ValueError, match="CUDA"):  # without a tangent it is only the device that is wrong
             call(t.clone())
+
+
+@pytest.mark.parametrize("inputs,call", [
+    ((X,), lambda x: layer_norm_forward(x, stats=False)["y"]),
+    ((X,), lambda x: layer_norm_backward(x, x, None, S, S)["grad_x"]),
+    ((Z, E), lambda z, e: balance_forward(z, e)["loss"]),
+    ((Z, E), lambda z, e: balance_fused(z, e)["loss"]),
+    ((Z,), lambda z: balance_backward(z, C, N, 2)["grad_logits"]),
+    ((L, B), lambda z, s: beam_select(z, s)["tokens"]),
+    ((T, P), lambda t, p: beam_reorder([t], p)[0]),
+])
+def test_traces_of_the_calls_on_their_own_are_refused(inputs, call):
+    with pytest.raises(RuntimeError, match="cannot be traced"):
+        torch.jit.trace(call, tuple(t.clone() for t in inputs), check_trace=False)
