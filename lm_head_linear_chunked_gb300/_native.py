@@ -8,11 +8,17 @@ import ctypes
 import importlib.util
 import os
 
-import torch  # the module below links against it
+import torch  # noqa: F401  (the module below links against it)
 
 from . import LCEError, lib
 
 _module = None
+
+
+class Traced(RuntimeError):
+    """A call under torch.jit.trace, which would see the allocation of the
+    outputs but not the call that fills them."""
+
 
 _NAMES = ("lce_layer_norm_forward", "lce_layer_norm_backward", "lce_layer_norm_workspace_size", "lce_balance_forward",
           "lce_balance_fused", "lce_balance_backward", "lce_balance_workspace_size", "lce_beam_select",
@@ -29,13 +35,6 @@ def native():
         spec = importlib.util.spec_from_file_location("_lce_torch", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.init({n: ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in _NAMES}, LCEError)
+        module.init({n: ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in _NAMES}, LCEError, Traced)
         _module = module
     return _module
-
-
-def not_traced(name: str) -> None:
-    """Refuses a call under torch.jit.trace: the trace sees the allocation of
-    the outputs but not the call that fills them."""
-    if torch.jit.is_tracing():
-        raise RuntimeError(f"{name} cannot be traced")

@@ -21,12 +21,12 @@ from typing import Optional
 import torch
 
 from . import LCEError, _flags, lce_check_status
-from ._native import native, not_traced
+from ._native import Traced, native
 
 
-def _loss_call(router_logits, experts, mask, reduction, grad, grad_scale, grad_output):
+def _loss_call(router_logits, experts, mask, reduction, grad, grad_scale, grad_output, recorded=False):
     flags = _flags(reduction, False)
-    r = native().balance_call(router_logits, experts, mask, bool(flags), grad, grad_scale, grad_output)
+    r = native().balance_call(router_logits, experts, mask, bool(flags), grad, grad_scale, grad_output, recorded)
     out = {"loss": r[0], "group_loss": r[1], "counts": r[2], "n_valid": r[3], "ws": r[4]}
     if grad:
         out["grad_logits"] = r[5]
@@ -39,14 +39,12 @@ def balance_forward(router_logits: torch.Tensor, experts: torch.Tensor, mask: Op
     lce_check_status reads) of router_logits [(groups,) tokens, experts] and experts [(groups,) tokens, slots]
     (-1: an unused slot); mask [tokens] or [groups, tokens] is False where a token is left out.  The loss is the
     mean over the groups, or with reduction="sum" their sum."""
-    not_traced("balance_forward")
     return _loss_call(router_logits, experts, mask, reduction, False, 1.0, None)
 
 
 def balance_fused(router_logits: torch.Tensor, experts: torch.Tensor, mask: Optional[torch.Tensor] = None,
                   grad_scale: float = 1.0, grad_output: Optional[torch.Tensor] = None, reduction: str = "mean") -> dict:
     """What balance_forward gives, and grad_logits: the gradient of grad_scale * grad_output * loss."""
-    not_traced("balance_fused")
     return _loss_call(router_logits, experts, mask, reduction, True, grad_scale, grad_output)
 
 
@@ -54,7 +52,6 @@ def balance_backward(router_logits: torch.Tensor, counts: torch.Tensor, n_valid:
                      mask: Optional[torch.Tensor] = None, grad_scale: float = 1.0,
                      grad_output: Optional[torch.Tensor] = None, reduction: str = "mean") -> dict:
     """{"grad_logits"} of grad_scale * grad_output * loss from a forward's counts and n_valid."""
-    not_traced("balance_backward")
     flags = _flags(reduction, False)
     return {"grad_logits": native().balance_backward(router_logits, counts, n_valid, slots, mask, bool(flags), grad_scale,
                                                      grad_output)}
@@ -63,7 +60,7 @@ def balance_backward(router_logits: torch.Tensor, counts: torch.Tensor, n_valid:
 class _BalanceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, router_logits, experts, mask, reduction):
-        out = _loss_call(router_logits, experts, mask, reduction, False, 1.0, None)
+        out = _loss_call(router_logits, experts, mask, reduction, False, 1.0, None, True)
         ctx.save_for_backward(router_logits, mask, out["counts"], out["n_valid"])
         ctx.slots, ctx.reduction = experts.shape[-1], reduction
         ctx.mark_non_differentiable(out["counts"], out["ws"])
@@ -78,17 +75,22 @@ class _BalanceLoss(torch.autograd.Function):
         return d["grad_logits"], None, None, None
 
 
+def _loss(router_logits, experts, mask, reduction):
+    out = balance_forward(router_logits, experts, mask, reduction)
+    return out["loss"].reshape(()), out["counts"], out["ws"]
+
+
 def balance_loss(router_logits: torch.Tensor, experts: torch.Tensor, mask: Optional[torch.Tensor] = None,
                  reduction: str = "mean", check: bool = False):
     """(loss, counts): the balance loss, differentiable in router_logits, and the int64 counts
     [(groups,) experts].  Arguments as balance_forward's.  check=True synchronises and raises on an expert index
     outside [-1, experts); without it such an index makes the loss NaN.  torch.jit.trace records it
     as one call."""
-    if (torch.is_grad_enabled() and router_logits.requires_grad) or torch.jit.is_tracing():
+    call = _BalanceLoss.apply if torch.is_grad_enabled() and router_logits.requires_grad else _loss
+    try:
+        loss, counts, ws = call(router_logits, experts, mask, reduction)
+    except Traced:
         loss, counts, ws = _BalanceLoss.apply(router_logits, experts, mask, reduction)
-    else:
-        out = balance_forward(router_logits, experts, mask, reduction)
-        loss, counts, ws = out["loss"].reshape(()), out["counts"], out["ws"]
     if check:
         st = lce_check_status(ws, torch.cuda.current_stream(ws.device))
         if st != 0:

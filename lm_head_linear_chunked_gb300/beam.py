@@ -18,7 +18,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import LCEError, lce_check_status
-from ._native import native, not_traced
+from ._native import native
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = None,
@@ -31,7 +31,6 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
     beam)}, each [items, n], best first; equal scores go to the lower beam, then the larger logit, then the
     lower token.  With eos_token also "finished" [items, n]: the parent was finished or the token is
     eos_token."""
-    not_traced("beam_select")
     n = (logits.shape[1] if logits.dim() == 3 else 0) if n is None else n
     if n <= 0 and logits.dim() == 3 and logits.numel():
         raise ValueError("n must be positive")
@@ -53,7 +52,6 @@ def beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor,
     item * beams + parents[item, j] of the state.  `out` gives the buffers (such as a second set of caches, or
     views of their used part: strides are kept, and only the elements of the views move); they must not overlap
     the states.  A parent outside [0, beams) gives a row of zeros; check=True synchronises and raises on one."""
-    not_traced("beam_reorder")
     status = torch.zeros(64, dtype=torch.int32, device=parents.device) if check else None
     out = native().beam_reorder(list(states), parents, None if out is None else list(out), status)
     if check and out:

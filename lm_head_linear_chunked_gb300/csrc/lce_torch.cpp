@@ -9,10 +9,12 @@
 // stride or type is refused here (TypeError, ValueError); a status other than
 // LCE_OK raises the package's LCEError.
 #include <ATen/core/Tensor.h>
+#include <ATen/TracerMode.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <algorithm>
@@ -39,9 +41,9 @@ struct Library {
     decltype(&lce_beam_workspace_size) beam_workspace;
     decltype(&lce_beam_reorder) beam_reorder;
 } lib;
-PyObject* lce_error = nullptr;  // kept for the life of the process
+PyObject *lce_error = nullptr, *traced_error = nullptr;  // kept for the life of the process
 
-void init(const py::dict& at, const py::object& error) {
+void init(const py::dict& at, const py::object& error, const py::object& traced) {
     auto get = [&](const char* name, auto& f) {
         f = reinterpret_cast<std::decay_t<decltype(f)>>(at[name].cast<uintptr_t>());
     };
@@ -56,6 +58,7 @@ void init(const py::dict& at, const py::object& error) {
     get("lce_beam_workspace_size", lib.beam_workspace);
     get("lce_beam_reorder", lib.beam_reorder);
     lce_error = error.inc_ref().ptr();
+    traced_error = traced.inc_ref().ptr();
 }
 
 void check(lce_status_t status, const char* where) {
@@ -100,10 +103,11 @@ void on_device(const OptTensor& t, const at::Device& device, const char* what) {
     if (t) on_device(*t, device, what);
 }
 
-// The calls below work on addresses, where a forward-mode tangent would be
-// lost without a word; there are no forward-mode derivatives.
+// The calls below work on addresses.  A forward-mode tangent would be lost
+// without a word (there are no forward-mode derivatives), and torch.jit.trace
+// would record the allocation of the outputs without the call that fills them.
 void no_tangent(const Tensor& t, const char* what) {
-    if (t._fw_grad(/*level=*/0).defined()) {
+    if (t.unsafeGetTensorImpl()->autograd_meta() && t._fw_grad(/*level=*/0).defined()) {
         PyErr_SetString(PyExc_NotImplementedError,
                         (std::string(what) + " has a forward-mode tangent: this operator has no forward-mode derivative").c_str());
         throw py::error_already_set();
@@ -111,6 +115,12 @@ void no_tangent(const Tensor& t, const char* what) {
 }
 void no_tangent(const OptTensor& t, const char* what) {
     if (t) no_tangent(*t, what);
+}
+void not_traced(const char* name) {
+    if (at::tracer::impl::is_dispatch_enabled()) {
+        PyErr_SetString(traced_error, (std::string(name) + " cannot be traced").c_str());
+        throw py::error_already_set();
+    }
 }
 
 // The current stream: outputs and workspaces belong to it.
@@ -142,6 +152,8 @@ Tensor rows_of(const Tensor& t, int64_t* stride) {
 
 // ---------------------------------------------------------------- layer norm
 
+// recorded: called by an autograd function, which a trace records as one call
+
 int64_t width(const Tensor& x) {
     if (x.dim() == 0 || x.size(-1) == 0) throw py::value_error("x needs a last dimension of at least one element");
     return x.size(-1);
@@ -154,7 +166,8 @@ void check_affine(const Tensor& x, int64_t H, const Tensor& t, const char* what)
 }
 
 std::tuple<Tensor, OptTensor, OptTensor> norm_forward(const Tensor& x_in, const OptTensor& weight, const OptTensor& bias,
-                                                      double eps, bool stats) {
+                                                      double eps, bool stats, bool recorded) {
+    if (!recorded) not_traced("layer_norm_forward");
     no_tangent(x_in, "x");
     no_tangent(weight, "weight");
     no_tangent(bias, "bias");
@@ -195,6 +208,7 @@ std::tuple<OptTensor, OptTensor, OptTensor> norm_backward(const Tensor& dy_in, c
                                                           const Tensor& mean, const Tensor& rstd, bool want_x,
                                                           bool want_w, bool want_b,
                                                           std::optional<at::ScalarType> grad_type) {
+    not_traced("layer_norm_backward");
     no_tangent(dy_in, "grad_y");
     no_tangent(x_in, "x");
     no_tangent(weight, "weight");
@@ -290,7 +304,8 @@ const float* grad_output_of(const OptTensor& t, const at::Device& dev) {
 
 // loss, group_loss, counts, n_valid, ws and (with grad) grad_logits
 std::vector<Tensor> balance_call(const Tensor& logits, const Tensor& experts_in, const OptTensor& mask, bool sum, bool grad,
-                                 double grad_scale, const OptTensor& grad_output) {
+                                 double grad_scale, const OptTensor& grad_output, bool recorded) {
+    if (!recorded) not_traced(grad ? "balance_fused" : "balance_forward");
     no_tangent(grad_output, "grad_output");
     const Router r = router_of(logits, mask);
     const int index_bytes = experts_in.scalar_type() == at::kLong ? 8 : experts_in.scalar_type() == at::kInt ? 4 : 0;
@@ -332,6 +347,7 @@ std::vector<Tensor> balance_call(const Tensor& logits, const Tensor& experts_in,
 
 Tensor balance_backward(const Tensor& logits, const Tensor& counts, const Tensor& n_valid, int64_t slots, const OptTensor& mask,
                         bool sum, double grad_scale, const OptTensor& grad_output) {
+    not_traced("balance_backward");
     no_tangent(grad_output, "grad_output");
     const Router r = router_of(logits, mask);
     if (logits.dim() == 3)
@@ -364,6 +380,7 @@ Tensor balance_backward(const Tensor& logits, const Tensor& counts, const Tensor
 // scores, tokens, parents and, with eos >= 0, finished
 std::vector<Tensor> beam_select(const Tensor& logits_in, const Tensor& scores_in, int64_t n, const OptTensor& finished,
                                 int64_t pad, int64_t eos) {
+    not_traced("beam_select");
     no_tangent(logits_in, "logits");
     no_tangent(scores_in, "scores");
     const int code = type_code(logits_in, "logits");
@@ -461,6 +478,7 @@ bool overlap(std::vector<Range> ranges) {
 
 std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor& parents_in,
                                  std::optional<std::vector<Tensor>> given, const OptTensor& status) {
+    not_traced("beam_reorder");
     if (parents_in.dim() != 2 || parents_in.scalar_type() != at::kLong || parents_in.numel() == 0)
         throw py::value_error("parents must be int64 [items, n] and not empty");
     const int64_t B = parents_in.size(0), n = parents_in.size(1);
@@ -474,9 +492,11 @@ std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor
     std::vector<Tensor> out, copies;  // copies live until the launch is enqueued
     std::vector<lce_beam_state_t> moves;
     std::vector<Range> ranges;
+    // many of these are views, whose answer takes 35 ns each: not outside a dual level
+    const bool dual = torch::autograd::ForwardADLevel::try_get_by_idx(0) != nullptr;
     for (size_t i = 0; i < states.size(); ++i) {
         Tensor a = states[i];
-        no_tangent(a, "a state");
+        if (dual) no_tangent(a, "a state");
         if (a.dim() == 0 || a.size(0) != rows)
             throw py::value_error("states must have " + std::to_string(rows) + " rows each, states[" + std::to_string(i) +
                                   "] has shape " + text(a.sizes()));
@@ -486,7 +506,7 @@ std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor
         Tensor b;
         if (given) {
             b = (*given)[i];
-            no_tangent(b, "an output");
+            if (dual) no_tangent(b, "an output");
             check_shape(b, shape, ("out[" + std::to_string(i) + "]").c_str());
             check_type(b, a.scalar_type(), ("out[" + std::to_string(i) + "]").c_str());
             if (b.device() != dev) throw py::value_error("states and outputs must be on " + dev.str());

@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from ._native import native, not_traced
+from ._native import Traced, native
 
 
 def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -24,8 +24,7 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, b
     """{"y", "mean", "rstd"}: the output and, with `stats`, each row's float32
     mean and reciprocal standard deviation [number of rows], which the
     backward reads."""
-    not_traced("layer_norm_forward")
-    y, mean, rstd = native().norm_forward(x, weight, bias, eps, stats)
+    y, mean, rstd = native().norm_forward(x, weight, bias, eps, stats, False)
     return {"y": y, "mean": mean, "rstd": rstd}
 
 
@@ -35,7 +34,6 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[
     """{"grad_x", "grad_weight", "grad_bias"} (None where not wanted) from a
     forward's mean and rstd.  The sums over the rows are of weight's type
     (`grad_dtype`, or x's type, without a weight)."""
-    not_traced("layer_norm_backward")
     dx, dw, db = native().norm_backward(grad_y, x, weight, mean, rstd, want_grad_x, want_grad_weight, want_grad_bias,
                                         grad_dtype)
     return {"grad_x": dx, "grad_weight": dw, "grad_bias": db}
@@ -44,7 +42,7 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
-        y, mean, rstd = native().norm_forward(x, weight, bias, eps, True)
+        y, mean, rstd = native().norm_forward(x, weight, bias, eps, True, True)
         ctx.save_for_backward(x, weight, mean, rstd)
         ctx.bias_dtype = bias.dtype if bias is not None else None
         return y
@@ -61,10 +59,13 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
                eps: float = 1e-5) -> torch.Tensor:
     """Layer norm of x over its last dimension, differentiable in x, weight and bias.  torch.jit.trace records it
     as one call."""
-    if (torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
-                                     or (bias is not None and bias.requires_grad))) or torch.jit.is_tracing():
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
+                                    or (bias is not None and bias.requires_grad)):
         return _LayerNorm.apply(x, weight, bias, eps)
-    return native().norm_forward(x, weight, bias, eps, False)[0]
+    try:
+        return native().norm_forward(x, weight, bias, eps, False, False)[0]
+    except Traced:
+        return _LayerNorm.apply(x, weight, bias, eps)
 
 
 class LayerNorm(torch.nn.Module):

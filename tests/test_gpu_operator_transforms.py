@@ -47,3 +47,16 @@ def test_a_trace_computes_with_its_own_inputs(grad):
         if grad:
             a, b = (torch.autograd.grad(r[0].sum() + r[1], (x, z, w)) for r in (got, want))
             assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.filterwarnings("ignore::torch.jit.TracerWarning", "ignore::DeprecationWarning")
+def test_gradients_inside_a_trace_are_refused():
+    """The trace has no node for an autograd function's backward."""
+    from lm_head_linear_chunked_gb300.balance_loss import balance_loss
+    from lm_head_linear_chunked_gb300.layer_norm import layer_norm
+    x, z = (normal(s, 7).requires_grad_(True) for s in ((5, 64), (1, 30, 8)))
+    experts = z.detach().topk(2, dim=-1).indices
+    for f, t in ((lambda x: torch.autograd.grad(layer_norm(x).sum(), x)[0], x),
+                 (lambda z: torch.autograd.grad(balance_loss(z, experts)[0], z)[0], z)):
+        with pytest.raises(RuntimeError, match="cannot be traced"):
+            torch.jit.trace(f, (t,), check_trace=False)
