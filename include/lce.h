@@ -429,7 +429,7 @@ LCE_API lce_status_t lce_balance_fused(int64_t groups, int64_t T, int64_t E, int
  * (int64).  A state's row is n1 x n2 runs of run_bytes bytes, with strides in
  * bytes between rows, outer and inner runs, so a cache whose used part is
  * shorter than its room moves only that part.  All states move in one launch
- * per 24.  src and dst must not overlap.  A parent outside [0, beams) gives a
+ * per 24.  No dst may overlap a src, another dst or itself.  A parent outside [0, beams) gives a
  * row of zero bytes and, with `status` (a device word that the caller has
  * zeroed, such as a workspace's first; may be NULL), LCE_ERR_INDEX_RANGE from
  * lce_check_status(status).  A row of a state has at most 2 GB. */

@@ -51,7 +51,7 @@ def beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor,
     row's beams by their index within the item.  Returns tensors [items * n, ...] whose row item * n + j is row
     item * beams + parents[item, j] of the state.  `out` gives the buffers (such as a second set of caches, or
     views of their used part: strides are kept, and only the elements of the views move); they must not overlap
-    the states.  A parent outside [0, beams) gives a row of zeros; check=True synchronises and raises on one."""
+    the states, each other or themselves.  A parent outside [0, beams) gives a row of zeros; check=True synchronises and raises on one."""
     status = torch.zeros(64, dtype=torch.int32, device=parents.device) if check else None
     out = native().beam_reorder(list(states), parents, None if out is None else list(out), status)
     if check and out:

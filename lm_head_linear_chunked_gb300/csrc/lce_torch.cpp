@@ -14,6 +14,7 @@
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/SmallVector.h>
 #include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -455,14 +456,15 @@ bool layout_of(const Tensor& src, const Tensor& dst, lce_beam_state_t* s) {
 struct Range {
     uintptr_t first, end;
     int whose;  // 0: a state, 1: an output
+    size_t at;  // its place among them
     bool operator<(const Range& o) const { return first < o.first; }
 };
 
-Range range_of(const Tensor& t, int whose) {
+Range range_of(const Tensor& t, int whose, size_t at) {
     uintptr_t last = 0;
     for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
     const uintptr_t first = reinterpret_cast<uintptr_t>(t.data_ptr());
-    return {first, first + (last + 1) * t.element_size(), whose};
+    return {first, first + (last + 1) * t.element_size(), whose, at};
 }
 
 // Whether a state's range of addresses meets an output's.
@@ -474,6 +476,94 @@ bool overlap(std::vector<Range> ranges) {
         ends[r.whose] = std::max(ends[r.whose], r.end);
     }
     return false;
+}
+
+// Where a tensor's elements lie, in bytes: n[k] blocks s[k] apart, each of the
+// next dimension's, the last of one element; the widest steps first.
+struct Places {
+    c10::SmallVector<int64_t, 6> n, s, reach;  // reach[k]: from the first to past the last byte of dimensions k, k + 1, ...
+    bool nested;  // no dimension's step is shorter than what it steps over: no element lies on another
+};
+
+Places places_of(const Tensor& t) {
+    Places p;
+    const int64_t size = t.element_size();
+    for (int64_t i = 0; i < t.dim(); ++i) {
+        if (t.size(i) <= 1) continue;
+        p.s.push_back(t.stride(i) * size);
+        p.n.push_back(t.size(i));
+        for (size_t k = p.s.size() - 1; k > 0 && p.s[k - 1] < p.s[k]; --k) {
+            std::swap(p.s[k - 1], p.s[k]);
+            std::swap(p.n[k - 1], p.n[k]);
+        }
+    }
+    p.reach.assign(p.s.size() + 1, size);
+    p.nested = true;
+    for (size_t k = p.s.size(); k-- > 0;) {
+        p.nested &= p.s[k] >= p.reach[k + 1];
+        p.reach[k] = p.reach[k + 1] + (p.n[k] - 1) * p.s[k];
+    }
+    return p;
+}
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }
+
+// Whether an element of a's dimensions i, i + 1, ... and one of b's j, j + 1, ...
+// share a byte, b starting d bytes after a; both nested.  Equal steps, as two views
+// of one buffer have, leave two distances to look at; of unequal ones the wider is
+// gone through, and where that takes too long the two count as sharing.
+bool share(const Places& a, size_t i, const Places& b, size_t j, int64_t d, int* budget) {
+    if (d >= a.reach[i] || d + b.reach[j] <= 0) return false;
+    if (i == a.n.size() && j == b.n.size()) return true;
+    if (--*budget < 0) return true;
+    const int64_t sa = i < a.n.size() ? a.s[i] : 0, sb = j < b.n.size() ? b.s[j] : 0;
+    if (sa == sb) {
+        // block v of b starts (q + v - u) sa + r bytes after block u of a, and a block reaches no further than sa
+        const int64_t q = floor_div(d, sa), r = d - q * sa;
+        const int64_t least = -(b.n[j] - 1), most = a.n[i] - 1;  // of u - v
+        return (q >= least && q <= most && share(a, i + 1, b, j + 1, r, budget)) ||
+               (q + 1 >= least && q + 1 <= most && share(a, i + 1, b, j + 1, r - sa, budget));
+    }
+    if (sa < sb) return share(b, j, a, i, -d, budget);
+    int64_t u = floor_div(d - a.reach[i + 1], sa) + 1;
+    if (u < 0) u = 0;
+    for (; u < a.n[i] && u * sa < d + b.reach[j]; ++u)
+        if (share(a, i + 1, b, j, d - u * sa, budget)) return true;
+    return false;
+}
+
+// No output lies on another one, or on itself.
+void outputs_apart(const std::vector<Tensor>& out, std::vector<Range> ranges) {
+    for (size_t i = 0; i < out.size(); ++i) {
+        const Tensor& t = out[i];
+        int64_t reach = t.numel() ? 1 : 0;
+        bool nested = true;  // in the order of its dimensions, as nearly all are
+        for (int64_t k = t.dim(); k-- > 0 && reach;) {
+            if (t.size(k) == 1) continue;
+            nested &= t.stride(k) >= reach;
+            reach += (t.size(k) - 1) * t.stride(k);
+        }
+        if (!nested && !places_of(t).nested)
+            throw py::value_error("out[" + std::to_string(i) + "] overlaps itself: strides " + text(t.strides()));
+    }
+    std::sort(ranges.begin(), ranges.end());
+    std::vector<const Range*> open;  // outputs that reach past the current one's start
+    std::vector<std::optional<Places>> places;
+    auto at = [&](const Range& r) -> const Places& {
+        places.resize(out.size());
+        if (!places[r.at]) places[r.at] = places_of(out[r.at]);
+        return *places[r.at];
+    };
+    for (const Range& r : ranges) {
+        if (!r.whose) continue;
+        open.erase(std::remove_if(open.begin(), open.end(), [&](const Range* o) { return o->end <= r.first; }), open.end());
+        for (const Range* o : open) {
+            int budget = 1 << 16;
+            if (share(at(*o), 0, at(r), 0, static_cast<int64_t>(r.first - o->first), &budget))
+                throw py::value_error("out[" + std::to_string(o->at) + "] overlaps out[" + std::to_string(r.at) + "]");
+        }
+        open.push_back(&r);
+    }
 }
 
 std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor& parents_in,
@@ -516,8 +606,8 @@ std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor
         out.push_back(b);
         if (a.numel() == 0) continue;
         if (given) {
-            ranges.push_back(range_of(a, 0));
-            ranges.push_back(range_of(b, 1));
+            ranges.push_back(range_of(a, 0, i));
+            ranges.push_back(range_of(b, 1, i));
         }
         lce_beam_state_t s;
         if (!layout_of(a, b, &s)) {
@@ -528,6 +618,7 @@ std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor
         moves.push_back(s);
     }
     if (overlap(ranges)) throw py::value_error("out overlaps the states");
+    if (given) outputs_apart(out, std::move(ranges));
     on_cuda(dev);
     const c10::cuda::CUDAGuard guard(dev);
     on_device(parents_in, dev, "parents");
@@ -548,7 +639,7 @@ py::object layout_for_test(const Tensor& src, const Tensor& dst) {
 
 bool overlap_for_test(const std::vector<std::tuple<uintptr_t, uintptr_t, int>>& ranges) {
     std::vector<Range> r;
-    for (const auto& [first, end, whose] : ranges) r.push_back({first, end, whose});
+    for (const auto& [first, end, whose] : ranges) r.push_back({first, end, whose, 0});
     return overlap(std::move(r));
 }
 

@@ -123,3 +123,68 @@ def test_layout_of_a_row():
     assert layout(x[:, :, :, ::2], y[:, :, :40, ::2]) == (8, 4 * 640, 4 * 1024, 320, 8, 8, 4)
     assert layout(x[:, ::2, ::2, ::3], x[:, ::2, ::2, ::3]) is None
     assert layout(x[:, 0].bfloat16(), y[:, 0, :40].bfloat16()) == (1, 0, 0, 1, 0, 0, 2 * 40 * 16)
+
+
+def test_outputs_that_share_memory_are_refused():
+    """Two blocks would write the same element: an output with itself, and two outputs, their ranges interleaved or not."""
+    room = torch.zeros(20, 4, 5)
+    wide = torch.zeros(6, 3, 4, 5)
+    one = torch.zeros(4, 5)
+    for outs in ([one.expand(6, 4, 5)], [torch.zeros(6, 1, 5).expand(6, 4, 5)],
+                 [torch.zeros(100).as_strided((6, 4, 5), (10, 5, 1))], [torch.zeros(100).as_strided((6, 4, 5), (8, 2, 2))],
+                 [room[:6], room[:6]], [room[:6], room[5:11]], [room[6:12], room[:6], room[11:17]],
+                 [wide[:, 0], wide[:, 0]], [wide[:, 0], wide[:, 1], wide[:, 1]],
+                 [wide[:, 0], wide.flatten(1)[:, 19:39].unflatten(1, (4, 5))],
+                 [wide[:, 0], wide[:, 0].transpose(1, 2).contiguous().transpose(1, 2), wide[:, 0]]):
+        with pytest.raises(ValueError, match="overlap"):
+            beam_reorder([X] * len(outs), P, out=outs)
+
+
+def test_outputs_beside_each_other_go_on():
+    """Views of one buffer that share no element: only the device is wrong."""
+    wide = torch.zeros(6, 3, 4, 5)
+    last = torch.zeros(6, 4, 5, 2)
+    inner = torch.zeros(6, 4, 3, 5)
+    part = torch.zeros(6, 4, 9, 5)
+    for outs in ([wide[:, 0], wide[:, 1], wide[:, 2]], [last[..., 0], last[..., 1]], [inner[:, :, 0], inner[:, :, 2]],
+                 [wide.flatten(1)[:, 1:21].unflatten(1, (4, 5)), wide.flatten(1)[:, 21:41].unflatten(1, (4, 5))],
+                 [part[:, :, 0], part[:, :, 1]], [torch.zeros(12, 4, 5)[::2], torch.zeros(6, 4, 5)]):
+        with pytest.raises(ValueError, match="CUDA"):
+            beam_reorder([X] * len(outs), P, out=outs)
+    # of another width, and of one element a row
+    both = torch.zeros(6, 21)
+    with pytest.raises(ValueError, match="CUDA"):
+        beam_reorder([X, X[:, 0, 0]], P, out=[both[:, 1:].unflatten(1, (4, 5)), both[:, 0]])
+    with pytest.raises(ValueError, match="overlap"):
+        beam_reorder([X, X[:, 0, 0]], P, out=[both[:, 1:].unflatten(1, (4, 5)), both[:, 20]])
+
+
+def test_overlap_against_all_addresses():
+    """Random strided outputs in one buffer: refused exactly where two elements share an address (where the strides
+    of an output nest, as those of views do; others are refused)."""
+    import itertools
+    import random
+    rng = random.Random(5)
+    seen = {True: 0, False: 0}
+    for _ in range(400):
+        buf = torch.zeros(2000)
+        rows, outs, cells, nested = 2, [], [], True
+        for _ in range(rng.randint(1, 3)):
+            shape = (rows, *(rng.randint(1, 3) for _ in range(rng.randint(0, 2))))
+            steps = [rng.choice((1, 2, 3, 4, 6, 12, 24, 40)) for _ in shape]
+            if rng.random() < 0.5:
+                steps.sort(reverse=True)
+            start = rng.randint(0, 60)
+            outs.append(buf.as_strided(shape, steps, start))
+            cells += [start + sum(i * s for i, s in zip(at, steps)) for at in itertools.product(*map(range, shape))]
+            reach = 1
+            for s, n in sorted((s, n) for s, n in zip(steps, shape) if n > 1):
+                nested &= s >= reach
+                reach += (n - 1) * s
+        shared = len(set(cells)) < len(cells)
+        with pytest.raises(ValueError) as e:
+            beam_reorder([torch.zeros(2, *o.shape[1:]) for o in outs], torch.zeros(1, 2, dtype=torch.int64), out=outs)
+        refused = "overlap" in str(e.value)
+        assert refused == (shared or not nested), ([(o.shape, o.stride(), o.storage_offset()) for o in outs])
+        seen[refused] += 1
+    assert min(seen.values()) > 50
