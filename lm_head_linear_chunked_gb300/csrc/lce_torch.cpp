@@ -479,17 +479,19 @@ bool overlap(std::vector<Range> ranges) {
 }
 
 // Where a tensor's elements lie, in bytes: n[k] blocks s[k] apart, each of the
-// next dimension's, the last of one element; the widest steps first.
+// next dimension's, the last of one element; the widest steps first.  Of a
+// tensor that is only read (`reads`), what an expanded dimension repeats lies
+// where it lies.
 struct Places {
     c10::SmallVector<int64_t, 6> n, s, reach;  // reach[k]: from the first to past the last byte of dimensions k, k + 1, ...
     bool nested;  // no dimension's step is shorter than what it steps over: no element lies on another
 };
 
-Places places_of(const Tensor& t) {
+Places places_of(const Tensor& t, bool reads = false) {
     Places p;
     const int64_t size = t.element_size();
     for (int64_t i = 0; i < t.dim(); ++i) {
-        if (t.size(i) <= 1) continue;
+        if (t.size(i) <= 1 || (reads && t.stride(i) == 0)) continue;
         p.s.push_back(t.stride(i) * size);
         p.n.push_back(t.size(i));
         for (size_t k = p.s.size() - 1; k > 0 && p.s[k - 1] < p.s[k]; --k) {
@@ -566,6 +568,18 @@ void outputs_apart(const std::vector<Tensor>& out, std::vector<Range> ranges) {
     }
 }
 
+// Whether an element of an output is one of a state's, whose ranges may meet.
+bool states_meet(const std::vector<Tensor>& states, const std::vector<Tensor>& out, const std::vector<Range>& ranges) {
+    for (const Range& a : ranges)
+        for (const Range& b : ranges) {
+            if (a.whose || !b.whose || a.end <= b.first || b.end <= a.first) continue;
+            const Places x = places_of(states[a.at], true), y = places_of(out[b.at]);
+            int budget = 1 << 16;
+            if (!x.nested || !y.nested || share(x, 0, y, 0, static_cast<int64_t>(b.first - a.first), &budget)) return true;
+        }
+    return false;
+}
+
 std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor& parents_in,
                                  std::optional<std::vector<Tensor>> given, const OptTensor& status) {
     not_traced("beam_reorder");
@@ -617,7 +631,7 @@ std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor
         }
         moves.push_back(s);
     }
-    if (overlap(ranges)) throw py::value_error("out overlaps the states");
+    if (overlap(ranges) && states_meet(states, out, ranges)) throw py::value_error("out overlaps the states");
     if (given) outputs_apart(out, std::move(ranges));
     on_cuda(dev);
     const c10::cuda::CUDAGuard guard(dev);

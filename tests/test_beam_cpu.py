@@ -188,3 +188,56 @@ def test_overlap_against_all_addresses():
         assert refused == (shared or not nested), ([(o.shape, o.stride(), o.storage_offset()) for o in outs])
         seen[refused] += 1
     assert min(seen.values()) > 50
+
+
+def test_outputs_between_the_states_go_on():
+    """One buffer that holds both sets, in any dimension: no element of an output is one of a state's."""
+    for d in range(1, 5):
+        both = torch.zeros(6, 4, 3, 5).unsqueeze(d).expand(*(2 if i == d else -1 for i in range(5))).contiguous()
+        a, b = both.unbind(d)
+        for s, o in ((a, b), (b, a)):
+            with pytest.raises(ValueError, match="CUDA"):
+                beam_reorder([s], P, out=[o])
+        for s, o in ((a, a), (b, b)):
+            with pytest.raises(ValueError, match="overlaps the states"):
+                beam_reorder([s], P, out=[o])
+    both = torch.zeros(6, 2, 9, 5)
+    with pytest.raises(ValueError, match="CUDA"):
+        beam_reorder([both[:, 0, :1].expand(6, 4, 5)], P, out=[both[:, 1, :4]])  # a state of one row, read four times
+    with pytest.raises(ValueError, match="overlaps the states"):
+        beam_reorder([both[:, 0, :1].expand(6, 4, 5)], P, out=[both[:, 0, :4]])
+
+
+def test_states_and_outputs_against_all_addresses():
+    """Random strided states and outputs in one buffer: refused where an element of an output is one of a state's
+    (or, for a state whose strides do not nest, where their ranges meet)."""
+    import itertools
+    import random
+    rng = random.Random(6)
+    seen = {True: 0, False: 0}
+    while min(seen.values()) < 150:
+        buf = torch.zeros(3000)
+        inner = tuple(rng.randint(1, 3) for _ in range(rng.randint(0, 2)))
+        sides, cells, nested, ranges = [], [], [], []
+        for side in range(2):
+            shape = (2, *inner)
+            steps = [rng.choice((0, 1, 2, 3, 4, 6, 12, 24, 40)[side:]) for _ in shape]
+            if side or rng.random() < 0.5:
+                steps.sort(reverse=True)
+            start = rng.randint(0, 60)
+            sides.append(buf.as_strided(shape, steps, start))
+            cells.append({start + sum(i * s for i, s in zip(at, steps)) for at in itertools.product(*map(range, shape))})
+            reach, ok = 1, True
+            for s, n in sorted((s, n) for s, n in zip(steps, shape) if n > 1 and s):
+                ok &= s >= reach
+                reach += (n - 1) * s
+            nested.append(ok)
+            ranges.append((min(cells[-1]), max(cells[-1])))
+        if not nested[1] or any(n > 1 and s == 0 for s, n in zip(sides[1].stride(), sides[1].shape)):
+            continue
+        with pytest.raises(ValueError) as e:
+            beam_reorder([sides[0]], torch.zeros(1, 2, dtype=torch.int64), out=[sides[1]])
+        refused = "overlaps the states" in str(e.value)
+        meet = ranges[0][0] <= ranges[1][1] and ranges[1][0] <= ranges[0][1]
+        assert refused == bool(cells[0] & cells[1] if nested[0] else meet), [(o.shape, o.stride(), o.storage_offset()) for o in sides]
+        seen[refused] += 1

@@ -353,3 +353,16 @@ def test_nan_and_minus_infinity_beside_few_tokens(rows, n, V, dtype):
     check(z[:2], s[:2], n, exact=True)
     got, want = select_into(z, s, n), select_into(z[:1].contiguous(), s[:1].contiguous(), n)
     assert all(torch.equal(got[k][:1], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("d", [1, 2, 3, 4])
+def test_both_sets_of_states_in_one_buffer(d):
+    from lm_head_linear_chunked_gb300.beam import beam_reorder
+    shape = [6, 4, 3, 5]
+    shape.insert(d, 2)
+    both = normal(tuple(shape), 17)
+    parents = torch.tensor([[2, 0, 1], [1, 1, 2]], device="cuda")
+    a, b = both.unbind(d)
+    before, want = a.clone(), moved(a, parents)
+    beam_reorder([a], parents, out=[b])
+    assert torch.equal(a, before) and torch.equal(b, want)
