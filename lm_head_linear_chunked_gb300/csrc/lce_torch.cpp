@@ -607,6 +607,10 @@ std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor
         std::vector<int64_t> shape = a.sizes().vec();
         shape[0] = B * n;
         if (a.device() != dev) throw py::value_error("states and outputs must be on " + dev.str());
+        if (a.is_conj() || a.is_neg()) {  // memory that stands for other values
+            a = a.resolve_conj().resolve_neg();
+            copies.push_back(a);
+        }
         Tensor b;
         if (given) {
             b = (*given)[i];
@@ -614,6 +618,7 @@ std::vector<Tensor> beam_reorder(const std::vector<Tensor>& states, const Tensor
             check_shape(b, shape, ("out[" + std::to_string(i) + "]").c_str());
             check_type(b, a.scalar_type(), ("out[" + std::to_string(i) + "]").c_str());
             if (b.device() != dev) throw py::value_error("states and outputs must be on " + dev.str());
+            if (b.is_conj() || b.is_neg()) throw py::value_error("out[" + std::to_string(i) + "] is a conjugate or negative view");
         } else {
             b = empty(shape, a.scalar_type(), dev);
         }

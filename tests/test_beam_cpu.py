@@ -241,3 +241,10 @@ def test_states_and_outputs_against_all_addresses():
         meet = ranges[0][0] <= ranges[1][1] and ranges[1][0] <= ranges[0][1]
         assert refused == bool(cells[0] & cells[1] if nested[0] else meet), [(o.shape, o.stride(), o.storage_offset()) for o in sides]
         seen[refused] += 1
+
+
+def test_conjugate_and_negative_views_as_outputs_are_refused():
+    z = torch.zeros(6, 4, dtype=torch.complex64)
+    for state, out in ((z, z.clone().conj()), (z.real, z.clone().conj().imag)):
+        with pytest.raises(ValueError, match="view"):
+            beam_reorder([state], P, out=[out])

@@ -366,3 +366,15 @@ def test_both_sets_of_states_in_one_buffer(d):
     before, want = a.clone(), moved(a, parents)
     beam_reorder([a], parents, out=[b])
     assert torch.equal(a, before) and torch.equal(b, want)
+
+
+def test_conjugate_and_negative_views_as_states():
+    """Views whose memory stands for other values."""
+    from lm_head_linear_chunked_gb300.beam import beam_reorder
+    z = torch.complex(normal((6, 4), 18), normal((6, 4), 19))
+    parents = torch.tensor([[2, 0, 1], [1, 1, 2]], device="cuda")
+    for x in (z.conj(), z.conj().imag, z.imag):
+        assert torch.equal(beam_reorder([x], parents)[0], moved(x, parents))
+        out = torch.empty_like(x.resolve_conj().resolve_neg())
+        beam_reorder([x], parents, out=[out])
+        assert torch.equal(out, moved(x, parents))
