@@ -418,15 +418,13 @@ lce_status_t bal_pass_form(BalArgs a, BalMode mode, cudaStream_t s) {
     if (a.parts > fit) a.parts = static_cast<int32_t>(fit > 1 ? fit : 1);
     a.per_part = (a.T + a.parts - 1) / a.parts;
     const dim3 grid(a.parts, a.G);
+    // at most 32 KB: histograms of 1024 experts without a ring, or of 256 beside one of 16 KB
     a.ring_at = (static_cast<uint32_t>(a.E) * 4 * (a.inline_count ? BAL_WARPS : 1) + 15u) / 16u * 16u;
     constexpr size_t vec = sizeof(Vec<T, VEC>);
     const size_t smem = a.ring_at + (bal_ring(vec, ITEMS) ? BAL_STAGES * BAL_THREADS * vec : 0);
     auto kernel = mode == BAL_FORWARD    ? bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FORWARD>
                   : mode == BAL_BACKWARD ? bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_BACKWARD>
                                          : bal_pass_kernel<T, VEC, LANES, ITEMS, BAL_FUSED>;
-    if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem)) != cudaSuccess)
-        return LCE_ERR_CUDA;
     if (mode == BAL_BACKWARD || a.inline_count)
         LCE_PROFILED(kernel<<<grid, BAL_THREADS, smem, s>>>(a));
     else

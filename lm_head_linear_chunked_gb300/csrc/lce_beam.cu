@@ -550,7 +550,6 @@ struct MoveState {
 struct MoveArgs {
     MoveState st[MOVE_STATES];
     uint32_t end[MOVE_STATES];  // pieces before the next tensor, over all out rows
-    int32_t n;
     const int64_t* parents;     // [items, out_beams]
     uint32_t out_beams, beams;
     unsigned* status;           // nullable
@@ -719,11 +718,11 @@ lce_status_t lce_beam_reorder(int64_t items, int64_t beams, int64_t out_beams, c
     a.out_beams = static_cast<uint32_t>(out_beams);
     a.beams = static_cast<uint32_t>(beams);
     a.status = static_cast<unsigned*>(status);
-    a.n = 0;
+    int n = 0;
     uint64_t pieces = 0;
     auto flush = [&]() -> lce_status_t {
-        if (a.n) LCE_PROFILED(beam_move_kernel<<<static_cast<unsigned>(pieces), MOVE_THREADS, 0, s>>>(a));
-        a.n = 0;
+        if (n) LCE_PROFILED(beam_move_kernel<<<static_cast<unsigned>(pieces), MOVE_THREADS, 0, s>>>(a));
+        n = 0;
         pieces = 0;
         return LCE_OK;
     };
@@ -753,13 +752,13 @@ lce_status_t lce_beam_reorder(int64_t items, int64_t beams, int64_t out_beams, c
         m.pieces = (m.vectors + MOVE_THREADS * MOVE_PER - 1) / (MOVE_THREADS * MOVE_PER);
         const uint64_t more = static_cast<uint64_t>(m.pieces) * rows;
         if (more > INT32_MAX) return LCE_ERR_UNSUPPORTED;
-        if (a.n == MOVE_STATES || pieces + more > INT32_MAX) {
+        if (n == MOVE_STATES || pieces + more > INT32_MAX) {
             const lce_status_t st = flush();
             if (st != LCE_OK) return st;
         }
         pieces += more;
-        a.st[a.n] = m;
-        a.end[a.n++] = static_cast<uint32_t>(pieces);
+        a.st[n] = m;
+        a.end[n++] = static_cast<uint32_t>(pieces);
     }
     return flush();
 }
