@@ -252,3 +252,22 @@ def test_rows_of_large_logits(E, dtype):
         u = half_step(t)
         assert_within(got["grad_logits"].reshape(small.shape), r["grad"],
                       u * r["grad"].abs() + (1 + u) * (3 * e_p + 8 * U32) * r["size"] + tiny(t), "grad_logits")
+
+
+@pytest.mark.parametrize("kind", ["unused slots", "unlikely experts"])
+def test_losses_far_below_one(kind):
+    """The loss is 1 + sum_e (f_e - 1) P_e, whose terms add up to at most 1 + loss in size."""
+    z, experts, mask = problem(3, 257, 16, 2, "fp32", 47, True)
+    if kind == "unused slots":
+        experts[normal(experts.shape, 48) > -2.5] = -1
+    else:
+        z[:, :, 0] += 15
+        experts[:] = 1 + experts % 15
+    r = formulas(z, experts, mask)
+    assert 0 <= float(r["group_loss"].max()) < 0.05
+    a = float(z[:, mask].abs().max())
+    e = (8 * a + 64 + 16 / 32 + 257 + 16) * U32
+    from lm_head_linear_chunked_gb300.balance_loss import balance_fused
+    f = balance_fused(z, experts, mask)
+    assert_within(f["group_loss"], r["group_loss"], e * (1 + r["group_loss"]), "group_loss")
+    assert_within(f["loss"].reshape(()), r["loss"], (e + U32) * (1 + r["loss"]), "loss")
