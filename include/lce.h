@@ -328,8 +328,9 @@ LCE_API int lce_gemm_pair_slots(void);
  * and from grad_y, with g = grad_y weight:
  *   grad_x = rstd (g - mean_h(g) - xh mean_h(g xh)),
  *   grad_weight = sum_rows grad_y xh,  grad_bias = sum_rows grad_y.
- * Sums are FP32 and in an order fixed by the sizes, so equal calls give
- * equal bits.
+ * Sums are FP32 and in an order fixed by the sizes, types, strides, the
+ * alignment of the pointers and the device, so calls equal in these give equal
+ * bits.
  *  - dtype (LCE_BF16, LCE_F16, LCE_F32) is the type of x, y, grad_y and
  *    grad_x; wtype, the type of weight, bias and their gradients, is dtype
  *    or LCE_F32 (another pair is LCE_ERR_UNSUPPORTED).
@@ -369,7 +370,9 @@ LCE_API lce_status_t lce_layer_norm_backward(int64_t rows, int64_t H, int dtype,
  * loss = the mean over all groups, or with LCE_REDUCTION_SUM their sum.
  * With s = grad_scale * *d_grad_output (NULL: 1), / groups for the mean,
  *   grad_logits[t,e] = s p_te (f_e - sum_j f_j p_tj) / n, 0 for masked tokens
- * (f takes no gradient).
+ * (f takes no gradient).  The loss is summed as 1 + sum_e (f_e - 1) P_e, so its
+ * error is a few 2^-24 of 1 + loss: a loss far below 1, as where slots are
+ * unused or name experts that the router hardly gives a share, has fewer digits.
  *  - Logits have strides (elements) for groups and tokens, experts are
  *    contiguous; grad_logits is contiguous, of the logits' type.
  *  - experts: int32 or int64 (index_bytes 4 or 8).  -1 is an unused slot;

@@ -32,15 +32,15 @@ constexpr int BAL_THREADS = 32 * BAL_WARPS;
 // Tokens of a lane group in the ring of the pass: one in work, the others on their way.
 constexpr int BAL_STAGES = 4;
 // Blocks of the pass over all groups (a group's blocks share its tokens out):
-// at most four on each of 152 SMs, which all run at once (sixteen more than
-// that took a second round, and half as long again); and the fewest tokens
-// that are worth one.
+// at most four on each of 152 SMs, which all run at once (one more a group
+// takes a second round: 24 x 16384 x 128 63 us, not 51.5); and the fewest
+// tokens that are worth one.
 constexpr int64_t BAL_SMS = 152;
 constexpr int64_t BAL_BLOCKS = 4 * BAL_SMS;
 // Whether the tokens read ahead wait in shared memory (24 x 16384 x 128 bf16,
-// loss and gradient with the counting: 54 us, against 66 from registers, where
-// the waits could not be hidden) or, with several vectors a lane, in registers
-// (2^25 fp32 logits of 256: 38 us against 40).
+// loss and gradient with the counting: 51.5 us, against 62.6 from registers,
+// where the waits could not be hidden) or, with several vectors a lane, in
+// registers (gradient of 2^25 fp32 logits of 256: 44.7 us against 46.0).
 constexpr bool bal_ring(size_t vec, int items) { return vec >= 4 && items == 1; }
 // Blocks of the pass on an SM, by the experts of a lane (which it keeps in registers).
 constexpr int bal_resident(int experts) { return experts <= 8 ? 4 : experts <= 16 ? 2 : 1; }
@@ -50,7 +50,14 @@ constexpr int64_t BAL_MIN_TOKENS = 32;
 constexpr int64_t BAL_COUNT_PARTS = 32;
 
 // Up to so many tokens of a single group, one block counts and passes over
-// them: one launch, not two.
+// them: one launch, not two.  Device time in us, one block against two
+// launches, forward of fp32 logits:
+//    experts \ tokens      64          128          512
+//         8            5.9  6.4     5.5  7.1     6.3  6.9
+//        64            6.7  6.9     7.7  7.9    14.0  7.1
+//       256            8.3  7.9    10.8  8.4    25.0  8.2
+// so the two launches are faster for many experts; the rule does not look at
+// them yet.
 constexpr int64_t BAL_ALONE_TOKENS = 512;
 
 struct BalArgs {

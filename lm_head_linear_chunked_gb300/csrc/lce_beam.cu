@@ -13,10 +13,12 @@
 // beams, comparing scores in FP64: two candidates of different beams compare
 // as their exact scores do unless these are within a few 2^-24.
 //
-// The scan is bound by its instructions (26 per logit, issue 57%) where rows
-// are many: 512 x 50257 fp32 take 36 us, 2.6 TB/s, and the join of 64 items
-// 8.6.  A call of one item is two latencies, 4.8 and 6.4 us.  The copy of the
-// states is bound by memory: 16 states of 32 rows of 3 MB take 363 us.
+// Where rows are many the scan issues in 56 of 100 cycles, 26 instructions per
+// logit, with a third of the warps: 461 unfinished rows of 50257 fp32 logits
+// take 36 us, 2.6 TB/s; what its warps wait for most are the barriers between
+// chunks.  The join of 64 items takes 8.6 us.  A call of one item is two
+// latencies, 5 to 6 and 6 to 8 us one by one and cold.  The copy of the states
+// is bound by memory: 16 states of 32 rows of 3 MB take 361 us.
 #include <float.h>
 
 #include "lce_internal.cuh"
@@ -62,8 +64,8 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
     return (static_cast<uint64_t>(top) << 32) | low;
 }
 
-// A sum in two floats: the exact error of each addition of the first goes to
-// the second.  FP64 adds run at 1/64 of the rate here.
+// A sum in two floats: the exact error of each addition of the first, by
+// Knuth's TwoSum, goes to the second.  FP64 adds run at 1/64 of the rate here.
 struct Sum2 {
     float hi, lo;
     __device__ __forceinline__ void add(float x, float x_lo = 0.f) {

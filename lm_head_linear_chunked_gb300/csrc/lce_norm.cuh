@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(128) norm_fwd_warp(NormFwd<T> a) {
 // next ones ahead, each thread its own vectors, so that only the sums over a
 // row wait for the other warps, once per R rows: each warp centres its share
 // of a row on the share's own mean, and the shares' means and squares are
-// put together as  M2 = sum_w M2_w + sum_w n_w (mean_w - mean)^2.
+// put together as  M2 = sum_w M2_w + sum_w n_w (mean_w - mean)^2  (Chan, Golub
+// and LeVeque's joining of variances).
 template <typename T, typename W, int VEC, int ITEMS, int R, int STAGES, int MAX_WARPS, int BLOCKS>
 __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) norm_fwd_rows(NormFwd<T> a) {
     constexpr bool RING = sizeof(Vec<T, VEC>) >= 4;  // single 16-bit elements wait in registers
@@ -623,15 +624,16 @@ lce_status_t fwd_rows(const NormFwd<T>& a, cudaStream_t s) {
 //  - up to 64 vectors (512 bf16): a warp per row, 6.1 TB/s at 512;
 //  - up to 128: the same with the next rows copied ahead and weight and bias
 //    kept, 6.1 TB/s at 1024 (a block of two warps: 4.7).  16384 rows of it with
-//    fp32 weights take 14 us, against 19 where each warp ends with its row;
+//    fp32 weights take 13 us, against 18 where each warp ends with its row;
 //  - up to 2048: a block per row, four vectors a thread, 6.4 TB/s at 4096 (a
 //    warp per row: 5.7, two vectors: 5.3);
 //  - where a quarter of such a block would be idle, two rows of two vectors a
 //    thread: 5.9 TB/s at 2560 against 4.9;
 //  - narrower vectors: eight a thread, or sixteen single elements; 2.6 TB/s at
-//    1601 fp16, bound by the instructions per element.  16-byte vectors
-//    counted from each row's own start reached 2.4: a row's two ends cost the
-//    warp that has them more than the vectors save;
+//    1601 fp16, where the warps (29% of them) issue in 58 of 100 cycles and
+//    wait for shared memory and shuffles.  16-byte vectors counted from each
+//    row's own start reached 2.4: a row's two ends cost the warp that has them
+//    more than the vectors save;
 //  - wider rows: the row is read again.
 template <typename T, typename W>
 lce_status_t norm_forward(const NormCall& c) {

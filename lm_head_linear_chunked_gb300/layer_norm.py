@@ -7,8 +7,8 @@
 own (one lce_layer_norm_forward or lce_layer_norm_backward call each; torch
 only allocates the outputs).  x is bfloat16, float16 or float32 with any
 number of leading dimensions; weight and bias are of x's type or float32,
-and each may be None.  Sums are float32 in a fixed order, so equal calls
-give equal bits.  There is no forward-mode derivative: a tangent is refused.
+and each may be None.  Sums are float32 in an order fixed by the sizes,
+types, strides, alignment and device, so equal calls give equal bits.  There is no forward-mode derivative: a tangent is refused.
 """
 from __future__ import annotations
 
