@@ -357,6 +357,136 @@ LCE_API lce_status_t lce_layer_norm_backward(int64_t rows, int64_t H, int dtype,
                                      void* grad_weight, void* grad_bias, void* ws, size_t ws_bytes,
                                      lce_stream_t stream);
 
+/* ---- RMS norm -----------------------------------------------------------
+ *
+ * The norm of models without a mean, with the addition of the residual in
+ * front of it.  For each row of x [rows, H]:
+ *   s = x + residual, rounded to dtype (x itself without a residual),
+ *   rstd = 1 / sqrt(sum_h s^2 / H + eps),  y = s rstd weight,
+ * and from grad_y, with xh = s rstd and g = grad_y weight:
+ *   grad_x = rstd (g - xh mean_h(g xh)) + grad_sum,
+ *   grad_weight = sum_rows grad_y xh.
+ * grad_x is x's gradient and the residual's alike; grad_sum (may be NULL) is
+ * what arrives at s from behind the norm.
+ * lce_rms_norm_fp8 gives the output in 8 bits: for each row's groups of
+ * `group` columns (0: the whole row, or LCE_FP8_GROUP; the last may be
+ * shorter), with y not rounded in between,
+ *   scale = max(max |y|, 2^-100) / 448,  q = e4m3(y / scale),
+ * scales [rows, ceil(H / group)] float, contiguous.  A group that holds a NaN
+ * has a NaN scale.
+ * Sums are FP32 and in an order fixed by the sizes, types, strides, the
+ * alignment of the pointers and the device, so calls equal in these give equal
+ * bits.  A row whose sum of squares passes FP32's range has rstd 0.
+ *  - dtype is the type of x, residual, sum, y and their gradients; wtype, of
+ *    weight and its gradient, is dtype or LCE_F32 (another pair is
+ *    LCE_ERR_UNSUPPORTED).  weight may be NULL (1).
+ *  - Rows are contiguous, each matrix with its own stride in elements (>= H).
+ *    Pointers need only the alignment of their element type; rows that start
+ *    on 16-byte boundaries (q: H a multiple of 16) are read in vectors.
+ *  - sum (s) is written where a residual is given: both or neither.  rstd
+ *    [rows] (may be NULL) is written by the forward and read by the backward,
+ *    whose x is s.
+ *  - 1 <= H <= LCE_NORM_MAX_H, 0 <= rows < 2^31 (no rows: nothing is read,
+ *    grad_weight becomes zero).
+ *  - grad_x and grad_weight may each be NULL; ws (256-byte aligned,
+ *    lce_rms_norm_workspace_size() bytes) is needed for the latter.
+ *  - Outputs must not overlap inputs. */
+#define LCE_FP8_GROUP 128
+LCE_API lce_status_t lce_rms_norm_forward(int64_t rows, int64_t H, int dtype, int wtype, const void* x, int64_t ldx,
+                                  const void* residual, int64_t ldr, const void* weight, float eps, void* sum,
+                                  int64_t lds, void* y, int64_t ldy, float* rstd, lce_stream_t stream);
+LCE_API lce_status_t lce_rms_norm_fp8(int64_t rows, int64_t H, int dtype, int wtype, const void* x, int64_t ldx,
+                              const void* residual, int64_t ldr, const void* weight, float eps, void* sum,
+                              int64_t lds, uint8_t* q, int64_t ldq, float* scales, int64_t group,
+                              lce_stream_t stream);
+LCE_API lce_status_t lce_rms_norm_workspace_size(int64_t rows, int64_t H, size_t* bytes);
+LCE_API lce_status_t lce_rms_norm_backward(int64_t rows, int64_t H, int dtype, int wtype, const void* grad_y,
+                                   int64_t ldg, const void* x, int64_t ldx, const void* weight, const float* rstd,
+                                   const void* grad_sum, int64_t ldgs, void* grad_x, int64_t ldgx,
+                                   void* grad_weight, void* ws, size_t ws_bytes, lce_stream_t stream);
+
+/* ---- embedding ----------------------------------------------------------
+ *
+ * y_i = scale weight[token_i] (rounded once), and
+ * grad_weight[v] = scale * sum over the i with token_i = v of grad_y_i.
+ * The rows of a token are added in FP32 in an order fixed by N, V, H, the
+ * types, strides, alignment and the tokens, so equal calls give equal bits.
+ *  - weight [V, H], y and grad_y [N, H], grad_weight [V, H], each with its own
+ *    stride in elements; tokens [N] int32 or int64 (index_bytes 4 or 8).
+ *  - A token equal to padding_token (LCE_NO_PADDING: none) gives no gradient;
+ *    its y is its row of the weight, or zero where it lies outside [0, V).
+ *    Another token outside [0, V) gives a row of NaN and no gradient, and
+ *    LCE_ERR_INDEX_RANGE from lce_check_status: of `status` (a device word
+ *    that the caller has zeroed; may be NULL) after the forward, of ws after
+ *    the backward.
+ *  - gtype, grad_weight's type, is dtype or LCE_F32.  All of grad_weight is
+ *    written, zeros where no token names a row.  With LCE_ACCUMULATE (flags;
+ *    gtype LCE_F32) the sums are added to what it holds, and rows that no token
+ *    names are left alone: with tied weights, grad_W_acc of the head's backward.
+ *  - 0 <= N < 2^31, 1 <= V < 2^31 - 1, 1 <= H <= LCE_NORM_MAX_H.
+ *  - Outputs must not overlap inputs. */
+#define LCE_NO_PADDING INT64_MIN
+LCE_API lce_status_t lce_embedding_forward(int64_t N, int64_t V, int64_t H, int dtype, const void* tokens,
+                                   int index_bytes, const void* weight, int64_t ldw, float scale,
+                                   int64_t padding_token, void* y, int64_t ldy, void* status,
+                                   lce_stream_t stream);
+LCE_API lce_status_t lce_embedding_workspace_size(int64_t N, int64_t V, int64_t H, size_t* bytes);
+LCE_API lce_status_t lce_embedding_backward(int64_t N, int64_t V, int64_t H, int dtype, int gtype, const void* tokens,
+                                    int index_bytes, const void* grad_y, int64_t ldg, float scale,
+                                    int64_t padding_token, void* grad_weight, int64_t ldgw, void* ws,
+                                    size_t ws_bytes, lce_stream_t stream, uint32_t flags);
+
+/* ---- rows sorted by expert ------------------------------------------------
+ *
+ * What a mixture does around its experts' products: T tokens name k experts
+ * each (slot (t, j) has the number t k + j), and every expert's rows are to lie
+ * side by side.
+ * lce_expert_plan sorts the slots by expert, in the order of their numbers:
+ *   counts[e] = slots that name e;  the rows of e start at offsets[e], a
+ *   multiple of `align`, and offsets[E] is one past the last segment;
+ *   positions[t, j] = the row of slot (t, j), -1 for none;
+ *   slots[r] = the number of row r's slot, -1 for none.
+ * lce_expert_rows() says how many rows that can take: R = T k + E (align - 1),
+ * rounded up to a multiple of align.
+ *   dispatch: rows[positions[t, j]] = x[t], rows without a slot are zero;
+ *     grad_x[t] = sum_j grad_rows[positions[t, j]];
+ *   combine: y[t] = sum_j weights[t, j] rows[positions[t, j]];
+ *     grad_rows[positions[t, j]] = weights[t, j] grad_y[t], zero without a slot;
+ *     grad_weights[t, j] = sum_h grad_y[t, h] rows[positions[t, j], h], 0 for
+ *     none.
+ * Sums are FP32 in a fixed order, rounded once.
+ *  - experts [T, k] int32 or int64 (index_bytes 4 or 8), contiguous.  -1 is an
+ *    unused slot, and a token whose byte in mask ([T]; NULL: none) is 0 has no
+ *    slots.  Another index outside [0, E) counts as unused and gives
+ *    LCE_ERR_INDEX_RANGE from lce_check_status(ws).
+ *  - weights [T, k] (wtype: dtype or LCE_F32), contiguous; NULL: 1.  x, y and
+ *    the rows have strides (elements).  grad_rows and grad_weights may each be
+ *    NULL; rows of the backward are read for grad_weights only.
+ *  - The moves take a plan's positions and slots with the R they were made
+ *    for; positions outside [0, R) count as none.
+ *  - 0 <= T, R < 2^31, 1 <= k <= E <= LCE_BALANCE_MAX_E,
+ *    1 <= align <= LCE_EXPERT_MAX_ALIGN, 1 <= H <= LCE_NORM_MAX_H.
+ *  - Outputs must not overlap inputs. */
+#define LCE_EXPERT_MAX_ALIGN 1024
+LCE_API lce_status_t lce_expert_rows(int64_t T, int64_t k, int64_t E, int64_t align, int64_t* rows);
+LCE_API lce_status_t lce_expert_plan_workspace_size(int64_t T, int64_t k, int64_t E, size_t* bytes);
+LCE_API lce_status_t lce_expert_plan(int64_t T, int64_t k, int64_t E, int64_t align, const void* experts,
+                             int index_bytes, const uint8_t* mask, int32_t* positions, int32_t* slots,
+                             int64_t* counts, int64_t* offsets, void* ws, size_t ws_bytes, lce_stream_t stream);
+LCE_API lce_status_t lce_expert_dispatch(int64_t T, int64_t k, int64_t H, int64_t R, int dtype, const void* x,
+                                 int64_t ldx, const int32_t* positions, const int32_t* slots, void* rows,
+                                 int64_t ldr, lce_stream_t stream);
+LCE_API lce_status_t lce_expert_dispatch_backward(int64_t T, int64_t k, int64_t H, int64_t R, int dtype,
+                                          const void* grad_rows, int64_t ldr, const int32_t* positions,
+                                          void* grad_x, int64_t ldx, lce_stream_t stream);
+LCE_API lce_status_t lce_expert_combine(int64_t T, int64_t k, int64_t H, int64_t R, int dtype, int wtype,
+                                const void* rows, int64_t ldr, const void* weights, const int32_t* positions,
+                                void* y, int64_t ldy, lce_stream_t stream);
+LCE_API lce_status_t lce_expert_combine_backward(int64_t T, int64_t k, int64_t H, int64_t R, int dtype, int wtype,
+                                         const void* grad_y, int64_t ldg, const void* rows, int64_t ldr,
+                                         const void* weights, const int32_t* positions, const int32_t* slots,
+                                         void* grad_rows, int64_t ldgr, void* grad_weights, lce_stream_t stream);
+
 /* ---- balance loss of a mixture of experts --------------------------------
  *
  * The auxiliary loss that a mixture-of-experts model adds to the head's

@@ -31,6 +31,10 @@ __all__ = [
     "BF16", "F16", "F32", "lce_layer_norm_forward", "lce_layer_norm_workspace_size", "lce_layer_norm_backward",
     "lce_balance_workspace_size", "lce_balance_forward", "lce_balance_backward", "lce_balance_fused",
     "BeamState", "lce_beam_workspace_size", "lce_beam_select", "lce_beam_reorder",
+    "FP8_GROUP", "lce_rms_norm_forward", "lce_rms_norm_fp8", "lce_rms_norm_workspace_size", "lce_rms_norm_backward",
+    "NO_PADDING", "lce_embedding_forward", "lce_embedding_workspace_size", "lce_embedding_backward",
+    "lce_expert_rows", "lce_expert_plan_workspace_size", "lce_expert_plan", "lce_expert_dispatch",
+    "lce_expert_dispatch_backward", "lce_expert_combine", "lce_expert_combine_backward",
 ]
 
 IGNORE_INDEX = -100
@@ -102,6 +106,26 @@ _SIGS = {
     "lce_beam_select": [_I64, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _P,
                         ctypes.c_size_t, _P],
     "lce_beam_reorder": [_I64, _I64, _I64, _P, ctypes.POINTER(BeamState), _I64, _P, _P],
+    "lce_rms_norm_forward": [_I64, _I64, ctypes.c_int, ctypes.c_int, _P, _I64, _P, _I64, _P, ctypes.c_float, _P, _I64,
+                             _P, _I64, _P, _P],
+    "lce_rms_norm_fp8": [_I64, _I64, ctypes.c_int, ctypes.c_int, _P, _I64, _P, _I64, _P, ctypes.c_float, _P, _I64,
+                         _P, _I64, _P, _I64, _P],
+    "lce_rms_norm_workspace_size": [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "lce_rms_norm_backward": [_I64, _I64, ctypes.c_int, ctypes.c_int, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64,
+                              _P, _P, ctypes.c_size_t, _P],
+    "lce_embedding_forward": [_I64, _I64, _I64, ctypes.c_int, _P, ctypes.c_int, _P, _I64, ctypes.c_float, _I64, _P,
+                              _I64, _P, _P],
+    "lce_embedding_workspace_size": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "lce_embedding_backward": [_I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P, ctypes.c_int, _P, _I64, ctypes.c_float,
+                               _I64, _P, _I64, _P, ctypes.c_size_t, _P, ctypes.c_uint32],
+    "lce_expert_rows": [_I64, _I64, _I64, _I64, ctypes.POINTER(_I64)],
+    "lce_expert_plan_workspace_size": [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "lce_expert_plan": [_I64, _I64, _I64, _I64, _P, ctypes.c_int, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "lce_expert_dispatch": [_I64, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _P, _P, _P, _I64, _P],
+    "lce_expert_dispatch_backward": [_I64, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _P, _P, _I64, _P],
+    "lce_expert_combine": [_I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P, _I64, _P, _P, _P, _I64, _P],
+    "lce_expert_combine_backward": [_I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P, _I64, _P, _I64, _P, _P, _P,
+                                    _P, _I64, _P, _P],
     "lce_profile_begin": [],
     "lce_profile_end": [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64)],
 }
@@ -371,6 +395,94 @@ def lce_beam_reorder(items, beams, out_beams, parents, states, n_states, status,
     """states: a ctypes array of BeamState."""
     _check(lib().lce_beam_reorder(items, beams, out_beams, _ptr(parents), states, n_states, _ptr(status),
                                   _stream(stream)), "lce_beam_reorder")
+
+
+FP8_GROUP = 128         # LCE_FP8_GROUP
+NO_PADDING = -(1 << 63)  # LCE_NO_PADDING
+
+
+def lce_rms_norm_forward(rows, H, dtype, wtype, x, ldx, residual, ldr, weight, eps, sum, lds, y, ldy, rstd,
+                         stream) -> None:
+    _check(lib().lce_rms_norm_forward(rows, H, dtype, wtype, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), eps,
+                                      _ptr(sum), lds, _ptr(y), ldy, _ptr(rstd), _stream(stream)), "lce_rms_norm_forward")
+
+
+def lce_rms_norm_fp8(rows, H, dtype, wtype, x, ldx, residual, ldr, weight, eps, sum, lds, q, ldq, scales, group,
+                     stream) -> None:
+    _check(lib().lce_rms_norm_fp8(rows, H, dtype, wtype, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), eps, _ptr(sum),
+                                  lds, _ptr(q), ldq, _ptr(scales), group, _stream(stream)), "lce_rms_norm_fp8")
+
+
+def lce_rms_norm_workspace_size(rows: int, H: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().lce_rms_norm_workspace_size(rows, H, ctypes.byref(out)), "lce_rms_norm_workspace_size")
+    return out.value
+
+
+def lce_rms_norm_backward(rows, H, dtype, wtype, grad_y, ldg, x, ldx, weight, rstd, grad_sum, ldgs, grad_x, ldgx,
+                          grad_weight, ws, ws_bytes, stream) -> None:
+    _check(lib().lce_rms_norm_backward(rows, H, dtype, wtype, _ptr(grad_y), ldg, _ptr(x), ldx, _ptr(weight), _ptr(rstd),
+                                       _ptr(grad_sum), ldgs, _ptr(grad_x), ldgx, _ptr(grad_weight), _ptr(ws), ws_bytes,
+                                       _stream(stream)), "lce_rms_norm_backward")
+
+
+def lce_embedding_forward(N, V, H, dtype, tokens, index_bytes, weight, ldw, scale, padding_token, y, ldy, status,
+                          stream) -> None:
+    _check(lib().lce_embedding_forward(N, V, H, dtype, _ptr(tokens), index_bytes, _ptr(weight), ldw, scale, padding_token,
+                                       _ptr(y), ldy, _ptr(status), _stream(stream)), "lce_embedding_forward")
+
+
+def lce_embedding_workspace_size(N: int, V: int, H: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().lce_embedding_workspace_size(N, V, H, ctypes.byref(out)), "lce_embedding_workspace_size")
+    return out.value
+
+
+def lce_embedding_backward(N, V, H, dtype, gtype, tokens, index_bytes, grad_y, ldg, scale, padding_token, grad_weight,
+                           ldgw, ws, ws_bytes, stream, flags) -> None:
+    _check(lib().lce_embedding_backward(N, V, H, dtype, gtype, _ptr(tokens), index_bytes, _ptr(grad_y), ldg, scale,
+                                        padding_token, _ptr(grad_weight), ldgw, _ptr(ws), ws_bytes, _stream(stream),
+                                        int(flags)), "lce_embedding_backward")
+
+
+def lce_expert_rows(T: int, k: int, E: int, align: int) -> int:
+    out = _I64(0)
+    _check(lib().lce_expert_rows(T, k, E, align, ctypes.byref(out)), "lce_expert_rows")
+    return out.value
+
+
+def lce_expert_plan_workspace_size(T: int, k: int, E: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().lce_expert_plan_workspace_size(T, k, E, ctypes.byref(out)), "lce_expert_plan_workspace_size")
+    return out.value
+
+
+def lce_expert_plan(T, k, E, align, experts, index_bytes, mask, positions, slots, counts, offsets, ws, ws_bytes,
+                    stream) -> None:
+    _check(lib().lce_expert_plan(T, k, E, align, _ptr(experts), index_bytes, _ptr(mask), _ptr(positions), _ptr(slots),
+                                 _ptr(counts), _ptr(offsets), _ptr(ws), ws_bytes, _stream(stream)), "lce_expert_plan")
+
+
+def lce_expert_dispatch(T, k, H, R, dtype, x, ldx, positions, slots, rows, ldr, stream) -> None:
+    _check(lib().lce_expert_dispatch(T, k, H, R, dtype, _ptr(x), ldx, _ptr(positions), _ptr(slots), _ptr(rows), ldr,
+                                     _stream(stream)), "lce_expert_dispatch")
+
+
+def lce_expert_dispatch_backward(T, k, H, R, dtype, grad_rows, ldr, positions, grad_x, ldx, stream) -> None:
+    _check(lib().lce_expert_dispatch_backward(T, k, H, R, dtype, _ptr(grad_rows), ldr, _ptr(positions), _ptr(grad_x), ldx,
+                                              _stream(stream)), "lce_expert_dispatch_backward")
+
+
+def lce_expert_combine(T, k, H, R, dtype, wtype, rows, ldr, weights, positions, y, ldy, stream) -> None:
+    _check(lib().lce_expert_combine(T, k, H, R, dtype, wtype, _ptr(rows), ldr, _ptr(weights), _ptr(positions), _ptr(y),
+                                    ldy, _stream(stream)), "lce_expert_combine")
+
+
+def lce_expert_combine_backward(T, k, H, R, dtype, wtype, grad_y, ldg, rows, ldr, weights, positions, slots, grad_rows,
+                                ldgr, grad_weights, stream) -> None:
+    _check(lib().lce_expert_combine_backward(T, k, H, R, dtype, wtype, _ptr(grad_y), ldg, _ptr(rows), ldr, _ptr(weights),
+                                             _ptr(positions), _ptr(slots), _ptr(grad_rows), ldgr, _ptr(grad_weights),
+                                             _stream(stream)), "lce_expert_combine_backward")
 
 
 def lce_profile_begin() -> None:

@@ -1,4 +1,4 @@
-"""The compiled torch side of the operators beside the head (lce_torch.cpp):
+"""The compiled torch side of the operators around the head (lce_torch*.cpp):
 checks of tensors, their outputs and workspaces, and one call of the C ABI.
 It calls the library that the ctypes binding has loaded, on torch's current
 stream."""
@@ -22,7 +22,10 @@ class Traced(RuntimeError):
 
 _NAMES = ("lce_layer_norm_forward", "lce_layer_norm_backward", "lce_layer_norm_workspace_size", "lce_balance_forward",
           "lce_balance_fused", "lce_balance_backward", "lce_balance_workspace_size", "lce_beam_select",
-          "lce_beam_workspace_size", "lce_beam_reorder")
+          "lce_beam_workspace_size", "lce_beam_reorder", "lce_rms_norm_forward", "lce_rms_norm_fp8", "lce_rms_norm_backward",
+          "lce_rms_norm_workspace_size", "lce_embedding_forward", "lce_embedding_backward", "lce_embedding_workspace_size",
+          "lce_expert_rows", "lce_expert_plan", "lce_expert_plan_workspace_size", "lce_expert_dispatch",
+          "lce_expert_dispatch_backward", "lce_expert_combine", "lce_expert_combine_backward")
 
 
 def native():

@@ -8,7 +8,7 @@ into one shared library with the CUDA runtime linked statically, so that
 loading it needs no GPU and no driver (the driver is only touched when a
 function enqueues work).
 
-The torch side of the operators beside the head (lce_torch.cpp) is compiled
+The torch side of the operators around the head (lce_torch*.cpp) is compiled
 with the host compiler into _lce_torch.so, against the installed torch.
 """
 from __future__ import annotations
@@ -26,7 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblce.so")
 LIB_DEBUG = os.path.join(PKG, "liblce_debug.so")
-TORCH_SRC = os.path.join(CSRC, "lce_torch.cpp")
+TORCH_SRC = [os.path.join(CSRC, f) for f in ("lce_torch.cpp", "lce_torch_rows.cpp")]
 TORCH_LIB = os.path.join(PKG, "_lce_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -46,7 +46,7 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.startswith("lce_torch")]
     return files + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [__file__]
 
 
@@ -95,7 +95,7 @@ def build_torch(force: bool = False, verbose: bool = False) -> str:
 
     tag = TORCH_LIB + ".for"
     made_for = f"torch {torch.__version__} python {sys.version}"
-    deps = [TORCH_SRC, os.path.join(INCLUDE, "lce.h"), __file__]
+    deps = [*TORCH_SRC, os.path.join(CSRC, "lce_torch.h"), os.path.join(INCLUDE, "lce.h"), __file__]
     if not force and os.path.exists(TORCH_LIB) and os.path.exists(tag) and open(tag).read() == made_for \
             and all(os.path.getmtime(f) <= os.path.getmtime(TORCH_LIB) for f in deps):
         return TORCH_LIB
@@ -103,16 +103,28 @@ def build_torch(force: bool = False, verbose: bool = False) -> str:
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     include = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
                os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"), INCLUDE]
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    cxx = os.environ.get("CXX", "g++")
+    flags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in include)]
+
+    def run(what: str, cmd: list[str]) -> None:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if verbose or r.returncode:
+            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        if r.returncode:
+            raise RuntimeError(f"g++ failed on {what}")
+
+    def compiled(src: str) -> str:
+        obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-4] + ".o")
+        run(os.path.basename(src), [cxx, *flags, "-c", src, "-o", obj])
+        return obj
+
+    with ThreadPoolExecutor(max_workers=len(TORCH_SRC)) as ex:
+        objs = list(ex.map(compiled, TORCH_SRC))
     tmp = TORCH_LIB + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", TORCH_SRC, "-o", tmp,
-           *(f"-I{i}" for i in include), f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
-           "-ltorch_python"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if verbose or r.returncode:
-        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-    if r.returncode:
-        raise RuntimeError("g++ failed on lce_torch.cpp")
+    run("_lce_torch.so", [cxx, "-shared", *objs, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                          "-ltorch", "-ltorch_python"])
     os.replace(tmp, TORCH_LIB)
     with open(tag, "w") as f:
         f.write(made_for)

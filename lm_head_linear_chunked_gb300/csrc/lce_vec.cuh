@@ -26,6 +26,12 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// Element i of values that are fp32 with w32, else T.
+template <typename T>
+__device__ __forceinline__ float load_w(const void* w, bool w32, int64_t i) {
+    return w32 ? static_cast<const float*>(w)[i] : to_f32(static_cast<const T*>(w)[i]);
+}
+
 // VEC elements read or written at once; the address is a multiple of the size,
 // or of 16 bytes for larger ones.
 template <typename T, int VEC>
