@@ -32,23 +32,34 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, bool idx64, int6
     return idx64 ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
 }
 
-// A block per token.
-template <typename T, int VEC>
+// A warp per U vectors of each lane of a token's row.
+template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) emb_fwd(EmbFwd<T> a) {
     using V = Vec<T, VEC>;
-    const int64_t i = blockIdx.x;
+    const int n = a.H / VEC, parts = (n + 32 * U - 1) / (32 * U), lane = threadIdx.x & 31;
+    const int64_t item = blockIdx.x * 8ll + (threadIdx.x >> 5), i = item / parts;
+    if (i >= a.N) return;
     const int64_t v = token_at(a.tokens, a.idx64, i);
     const bool in = v >= 0 && v < a.V;
     const float fill = v == a.padding ? 0.f : __int_as_float(0x7fffffff);
-    if (!in && v != a.padding && a.status && threadIdx.x == 0) atomicOr(a.status, STATUS_INDEX);
+    const int k0 = static_cast<int>(item % parts) * 32 * U + lane;
+    if (!in && v != a.padding && a.status && k0 == 0) atomicOr(a.status, STATUS_INDEX);
     const V* w = reinterpret_cast<const V*>(a.w + (in ? v : 0) * a.ldw);
     V* y = reinterpret_cast<V*>(a.y + i * a.ldy);
-    for (int k = threadIdx.x; k < a.H / VEC; k += blockDim.x) {
-        V x{};
-        if (in) x = w[k];
+    V x[U];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x.set(e, in ? x.f(e) * a.scale : fill);
-        y[k] = x;
+    for (int u = 0; u < U; ++u)
+        if (in && k0 + 32 * u < n) x[u] = w[k0 + 32 * u];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (k0 + 32 * u >= n) break;
+        if (!in)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[u].set(e, fill);
+        else if (a.scale != 1.f)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[u].set(e, x[u].f(e) * a.scale);
+        y[k0 + 32 * u] = x[u];
     }
 }
 
@@ -57,7 +68,10 @@ __global__ void __launch_bounds__(256) emb_fwd(EmbFwd<T> a) {
 // The workspace.
 struct EmbSpace {
     WsHeader* hdr;
+    int32_t* spans;          // how many runs reach past the chunk they start in; from [1] on, those chunks
+    uint8_t* named;          // [V]: 1 for rows that a token names
     int32_t *bad, *hist, *keys[2], *rows[2];
+    float* parts;            // [chunks, 2, H]
 };
 
 // The first digit: tokens as they come.  V stands for the ones to leave out.
@@ -69,6 +83,15 @@ struct FirstDigit {
     int64_t padding;
     int32_t *keys, *rows;
     unsigned* stat;
+    int32_t* spans;
+    uint8_t* named;  // nullable
+    __device__ __forceinline__ void begin() const {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *spans = 0;
+        if (named)
+            for (int64_t v = static_cast<int64_t>(blockIdx.x) * SORT_THREADS + threadIdx.x; v * 16 < V;
+                 v += static_cast<int64_t>(gridDim.x) * SORT_THREADS)
+                reinterpret_cast<uint4*>(named)[v] = make_uint4(0, 0, 0, 0);
+    }
     __device__ __forceinline__ int32_t key(int64_t i, bool* bad) const {
         const int64_t v = token_at(tokens, idx64, i);
         if (v == padding) return V;
@@ -79,8 +102,10 @@ struct FirstDigit {
     __device__ __forceinline__ int32_t digit(int64_t i, bool* bad) const { return key(i, bad) & mask; }
     __device__ __forceinline__ void put(int64_t i, int32_t, int32_t at) const {
         bool bad;
-        keys[at] = key(i, &bad);
+        const int32_t v = key(i, &bad);
+        keys[at] = v;
         rows[at] = static_cast<int32_t>(i);
+        if (named && v < V) named[v] = 1;
     }
     __device__ __forceinline__ void status(int any) const { *stat = any ? STATUS_INDEX : 0u; }
 };
@@ -91,6 +116,7 @@ struct NextDigit {
     const int32_t *from_keys, *from_rows;
     int32_t shift, mask;
     int32_t *keys, *rows;
+    __device__ __forceinline__ void begin() const {}
     __device__ __forceinline__ int32_t digit(int64_t i, bool*) const { return from_keys[i] >> shift & mask; }
     __device__ __forceinline__ void put(int64_t i, int32_t, int32_t at) const {
         keys[at] = from_keys[i];
@@ -99,39 +125,150 @@ struct NextDigit {
     __device__ __forceinline__ void status(int) const {}
 };
 
+constexpr int EMB_CHUNK = 32;       // sorted tokens of a warp
+constexpr int EMB_ZERO_ROWS = 8;    // vocabulary rows of a warp that looks for rows to clear
+
 template <typename T>
 struct EmbBwd {
     const T* dy;
     int64_t ldd, N, V;
     float scale;
     const int32_t *keys, *rows;  // sorted
+    const uint8_t* named;
+    int32_t* spans;
+    float* parts;
     void* dw;
-    int64_t lddw;
+    int64_t lddw, chunks;
     bool add;
-    int32_t H;
+    int32_t H, slabs;
 };
 
-// A block per vocabulary row: its place among the sorted tokens, then its rows.
-template <typename T, typename W>
-__global__ void __launch_bounds__(256) emb_bwd_row(EmbBwd<T> a) {
-    const int64_t v = blockIdx.x;
-    wait_for_primary();
-    int64_t lo = 0, hi = a.N;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (a.keys[mid] < v)
-            lo = mid + 1;
-        else
-            hi = mid;
+// A lane's share of a row's slab: ITEMS vectors, 32 vectors apart, summed in FP32.
+template <typename W, int VEC, int ITEMS>
+__device__ __forceinline__ void emb_store(const float (&s)[VEC * ITEMS], W* row, int k0, int n, float scale, bool add) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        if (k0 + 32 * i >= n) break;
+        Vec<W, VEC>* out = reinterpret_cast<Vec<W, VEC>*>(row) + k0 + 32 * i;
+        Vec<W, VEC> o{};
+        if (add) o = *out;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o.set(e, add ? fmaf(s[i * VEC + e], scale, o.f(e)) : s[i * VEC + e] * scale);
+        *out = o;
     }
-    W* dw = static_cast<W*>(a.dw) + v * a.lddw;
-    if (a.add && (lo == a.N || a.keys[lo] != v)) return;
-    for (int h = threadIdx.x; h < a.H; h += blockDim.x) {
-        float s = 0.f;
-        for (int64_t i = lo; i < a.N && a.keys[i] == v; ++i) s += to_f32(a.dy[a.rows[i] * a.ldd + h]);
-        s *= a.scale;
-        if (a.add) s += to_f32(dw[h]);
-        dw[h] = from_f32<W>(s);
+}
+
+// The sums.  A warp takes 32 sorted tokens and a slab of columns, loads BATCH
+// rows at a time and adds them up until the token changes.  A run of equal
+// tokens that lies inside the chunk is finished here; the pieces of one that
+// does not go to `parts`: [chunk][0] of a run that comes from the chunk before,
+// [chunk][1] of one that starts here.  So a token that fills half of the batch
+// is spread over as many warps as its rows need.
+// The warps behind those clear the vocabulary rows that no token names.
+template <typename T, typename W, int VEC, int ITEMS, int BATCH>
+__global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
+    using V = Vec<T, VEC>;
+    const int lane = threadIdx.x & 31;
+    const int n = a.H / VEC;
+    int64_t item = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    launch_dependents();
+    wait_for_primary();
+    if (item >= a.chunks * a.slabs) {
+        if (a.add) return;
+        const int64_t v0 = (item - a.chunks * a.slabs) * EMB_ZERO_ROWS;
+        for (int64_t v = v0; v < v0 + EMB_ZERO_ROWS && v < a.V; ++v) {
+            if (a.named[v]) continue;
+            Vec<W, VEC>* out = reinterpret_cast<Vec<W, VEC>*>(static_cast<W*>(a.dw) + v * a.lddw);
+            for (int k = lane; k < n; k += 32) out[k] = Vec<W, VEC>{};
+        }
+        return;
+    }
+    const int64_t c = item / a.slabs;
+    const int k0 = static_cast<int>(item % a.slabs) * 32 * ITEMS + lane;
+    const int64_t at = c * EMB_CHUNK + lane;
+    const int32_t none = static_cast<int32_t>(a.V);  // the key of what is left out, behind all others
+    const int32_t key = at < a.N ? a.keys[at] : none;
+    const int32_t row = at < a.N ? a.rows[at] : 0;
+    int32_t next = __shfl_down_sync(0xFFFFFFFFu, key, 1), before = -1;
+    if (lane == 31) next = at + 1 < a.N ? a.keys[at + 1] : none;
+    if (lane == 0 && c > 0) before = a.keys[at - 1];
+    const int items = __popc(__ballot_sync(0xFFFFFFFFu, key < none));
+    const unsigned last = __ballot_sync(0xFFFFFFFFu, key != next || lane == 31);  // of a run or the chunk
+    const bool from_before = __shfl_sync(0xFFFFFFFFu, before == key, 0), goes_on = __shfl_sync(0xFFFFFFFFu, key == next, 31);
+    bool first = true;
+    float s[VEC * ITEMS];
+#pragma unroll
+    for (int e = 0; e < VEC * ITEMS; ++e) s[e] = 0.f;
+    for (int i0 = 0; i0 < items; i0 += BATCH) {
+        V x[BATCH][ITEMS];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int64_t r = __shfl_sync(0xFFFFFFFFu, row, i0 + b);
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                x[b][i] = V{};
+                if (i0 + b < items && k0 + 32 * i < n) x[b][i] = reinterpret_cast<const V*>(a.dy + r * a.ldd)[k0 + 32 * i];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            if (i0 + b >= items) break;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s[i * VEC + e] += x[b][i].f(e);
+            if (!(last >> (i0 + b) & 1)) continue;
+            const int64_t v = __shfl_sync(0xFFFFFFFFu, key, i0 + b);
+            const bool came = first && from_before, goes = i0 + b == 31 && goes_on;
+            if (!came && !goes) {
+                emb_store<W, VEC, ITEMS>(s, static_cast<W*>(a.dw) + v * a.lddw, k0, n, a.scale, a.add);
+            } else {
+                emb_store<float, VEC, ITEMS>(s, a.parts + (c * 2 + (came ? 0 : 1)) * a.H, k0, n, 1.f, false);
+                if (!came && k0 == 0) a.spans[1 + atomicAdd(a.spans, 1)] = static_cast<int32_t>(c);
+            }
+            first = false;
+#pragma unroll
+            for (int e = 0; e < VEC * ITEMS; ++e) s[e] = 0.f;
+        }
+    }
+}
+
+// The runs that reach past a chunk: 32 columns of one per block, its pieces
+// shared out over 32 rows of threads and added in a fixed order.
+template <typename W>
+__global__ void __launch_bounds__(1024) emb_join(EmbBwd<float> a) {
+    __shared__ float s[32][33];
+    const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+    wait_for_primary();
+    const int slabs = (a.H + 31) / 32;
+    const int64_t items = static_cast<int64_t>(*a.spans) * slabs;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t c0 = a.spans[1 + item / slabs];
+        const int col = static_cast<int>(item % slabs) * 32 + c;
+        const int32_t v = a.keys[c0 * EMB_CHUNK + EMB_CHUNK - 1];
+        int64_t lo = c0 + 1, hi = a.chunks;  // the first chunk that does not start with v
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (a.keys[mid * EMB_CHUNK] == v)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        float sum = 0.f;
+        if (col < a.H) {
+            if (k == 0) sum = a.parts[(c0 * 2 + 1) * a.H + col];
+#pragma unroll 8
+            for (int64_t p = c0 + 1 + k; p < lo; p += 32) sum += a.parts[p * 2 * a.H + col];
+        }
+        s[k][c] = sum;
+        __syncthreads();
+        sum = warp_sum(s[c][k]);  // column k of the slab
+        const int64_t out = (item % slabs) * 32 + k;
+        if (c == 0 && out < a.H) {
+            W* dw = static_cast<W*>(a.dw) + v * a.lddw + out;
+            *dw = from_f32<W>(a.add ? fmaf(sum, a.scale, to_f32(*dw)) : sum * a.scale);
+        }
+        __syncthreads();
     }
 }
 
@@ -156,27 +293,34 @@ Digits digits_of(int64_t V) {
     return {passes, (bits + passes - 1) / passes};
 }
 
-size_t emb_space(int64_t N, int64_t V, EmbSpace* e, void* ws) {
+size_t emb_space(int64_t N, int64_t V, int64_t H, EmbSpace* e, void* ws) {
     const Digits d = digits_of(V);
+    const int64_t chunks = (N + EMB_CHUNK - 1) / EMB_CHUNK;
     const size_t blocks = static_cast<size_t>(sort_blocks(N)), items = align256(static_cast<size_t>(N) * 4);
-    const size_t hist = 1024 + align256(blocks * 4);
-    const size_t keys = hist + align256(blocks * 4 << d.bits);
-    if (e) {
-        uint8_t* w = static_cast<uint8_t*>(ws);
-        e->hdr = reinterpret_cast<WsHeader*>(w);
-        e->bad = reinterpret_cast<int32_t*>(w + 1024);
-        e->hist = reinterpret_cast<int32_t*>(w + hist);
-        for (int k = 0; k < 2; ++k) {
-            e->keys[k] = reinterpret_cast<int32_t*>(w + keys + 2 * k * items);
-            e->rows[k] = reinterpret_cast<int32_t*>(w + keys + (2 * k + 1) * items);
-        }
+    size_t at = 1024;
+    auto take = [&](size_t bytes) {
+        uint8_t* p = static_cast<uint8_t*>(ws) + at;
+        at += align256(bytes);
+        return p;
+    };
+    EmbSpace here{};
+    EmbSpace& f = e ? *e : here;
+    f.hdr = static_cast<WsHeader*>(ws);
+    f.bad = reinterpret_cast<int32_t*>(take(blocks * 4));
+    f.hist = reinterpret_cast<int32_t*>(take(blocks * 4 << d.bits));
+    f.spans = reinterpret_cast<int32_t*>(take(static_cast<size_t>(chunks + 1) * 4));
+    f.named = take(static_cast<size_t>(V));
+    for (int k = 0; k < 2; ++k) {
+        f.keys[k] = reinterpret_cast<int32_t*>(take(items));
+        f.rows[k] = reinterpret_cast<int32_t*>(take(items));
     }
-    return keys + 4 * items;
+    f.parts = reinterpret_cast<float*>(take(chunks > 1 ? static_cast<size_t>(chunks) * 2 * H * 4 : 0));
+    return at;
 }
 
 // The sorted tokens: their place in e->keys and e->rows.
-lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int64_t padding, const EmbSpace& e, int* where,
-                      cudaStream_t s) {
+lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int64_t padding, bool clear, const EmbSpace& e,
+                      int* where, cudaStream_t s) {
     const Digits d = digits_of(V);
     SortShape shape{};
     shape.n = N;
@@ -185,7 +329,8 @@ lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int6
     shape.per = (N + shape.blocks - 1) / shape.blocks;
     shape.hist = e.hist;
     shape.bad = e.bad;
-    const FirstDigit first{tokens, idx64, static_cast<int32_t>(V), shape.bins - 1, padding, e.keys[0], e.rows[0], &e.hdr->status};
+    const FirstDigit first{tokens, idx64, static_cast<int32_t>(V), shape.bins - 1, padding, e.keys[0], e.rows[0], &e.hdr->status,
+                           e.spans, clear ? e.named : nullptr};
     lce_status_t st = sort_by(first, shape, true, s);
     shape.bad = nullptr;
     for (int p = 1; p < d.passes && st == LCE_OK; ++p) {
@@ -194,6 +339,63 @@ lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int6
     }
     *where = (d.passes - 1) & 1;
     return st;
+}
+
+// The widest vectors in which rows `ld` elements apart from p can be read.
+template <typename T>
+int vector_of(const void* p, int64_t ld, int64_t H) {
+    constexpr int V = vec16<T>(), V4 = 4 / static_cast<int>(sizeof(T));
+    if (H % V == 0 && ld % V == 0 && aligned_to(p, 16)) return V;
+    return H % V4 == 0 && ld % V4 == 0 && aligned_to(p, 4) ? V4 : 1;
+}
+
+template <typename T, int VEC>
+lce_status_t emb_lookup(const EmbFwd<T>& a, cudaStream_t s) {
+    // four vectors a lane where that still gives every SM its warps, one for a decode step
+    const int64_t n = a.H / VEC, four = a.N * ((n + 127) / 128);
+    const bool wide = n > 32 && four >= 152 * 32;
+    const int64_t blocks = ((wide ? four : a.N * ((n + 31) / 32)) + 7) / 8;
+    if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
+    if (wide)
+        LCE_PROFILED(emb_fwd<T, VEC, 4><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+    else
+        LCE_PROFILED(emb_fwd<T, VEC, 1><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+    return LCE_OK;
+}
+
+template <typename T, typename W, int VEC>
+lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
+    constexpr int ITEMS = VEC >= 8 ? 1 : 8 / VEC, BATCH = VEC * sizeof(T) == 16 ? (ITEMS == 1 ? 8 : 4) : 4;
+    const int64_t n = a.H / VEC;
+    a.slabs = static_cast<int32_t>((n + 32 * ITEMS - 1) / (32 * ITEMS));
+    const int64_t warps = a.chunks * a.slabs + (a.add ? 0 : (a.V + EMB_ZERO_ROWS - 1) / EMB_ZERO_ROWS), blocks = (warps + 7) / 8;
+    if (blocks == 0) return LCE_OK;
+    if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
+    LCE_PROFILED(launch_after(emb_sum<T, W, VEC, ITEMS, BATCH>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a));
+    if (a.chunks < 2) return LCE_OK;
+    EmbBwd<float> j{};
+    j.V = a.V;
+    j.scale = a.scale;
+    j.keys = a.keys;
+    j.spans = a.spans;
+    j.parts = a.parts;
+    j.dw = a.dw;
+    j.lddw = a.lddw;
+    j.chunks = a.chunks;
+    j.add = a.add;
+    j.H = a.H;
+    const int64_t most = (a.chunks - 1) * ((a.H + 31) / 32);
+    LCE_PROFILED(launch_after(emb_join<W>, dim3(static_cast<unsigned>(most < 304 ? most : 304)), 1024, 0, s, j));
+    return LCE_OK;
+}
+
+template <typename T, typename W>
+lce_status_t emb_gradient(const EmbBwd<T>& a, cudaStream_t s) {
+    const int in = vector_of<T>(a.dy, a.ldd, a.H), out = vector_of<W>(a.dw, a.lddw, a.H);
+    constexpr int V = vec16<T>(), V4 = 4 / static_cast<int>(sizeof(T));
+    if (in == V && out == vec16<W>()) return emb_sums<T, W, V>(a, s);
+    if (V4 > 1 && in >= V4 && a.lddw % V4 == 0 && aligned_to(a.dw, V4 * sizeof(W))) return emb_sums<T, W, V4>(a, s);
+    return emb_sums<T, W, 1>(a, s);
 }
 
 bool index_ok(const void* p, int bytes) { return (bytes == 4 || bytes == 8) && p && aligned_to(p, bytes); }
@@ -218,22 +420,19 @@ lce_status_t lce_embedding_forward(int64_t N, int64_t V, int64_t H, int dtype, c
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);
-        constexpr int VEC = vec16<T>();
         const EmbFwd<T> a{tokens, index_bytes == 8, static_cast<const T*>(weight), ldw, N, V, padding_token, scale,
                           static_cast<T*>(y), ldy, static_cast<unsigned*>(status), static_cast<int32_t>(H)};
-        const unsigned blocks = static_cast<unsigned>(N);
-        if (H % VEC == 0 && ldw % VEC == 0 && ldy % VEC == 0 && aligned_to(weight, 16) && aligned_to(y, 16))
-            LCE_PROFILED(emb_fwd<T, VEC><<<blocks, 256, 0, s>>>(a));
-        else
-            LCE_PROFILED(emb_fwd<T, 1><<<blocks, 256, 0, s>>>(a));
-        return LCE_OK;
+        constexpr int V16 = vec16<T>(), V4 = 4 / static_cast<int>(sizeof(T));
+        const int from = vector_of<T>(weight, ldw, H), to = vector_of<T>(y, ldy, H), vec = from < to ? from : to;
+        if (vec == V16) return emb_lookup<T, V16>(a, s);
+        return V4 > 1 && vec == V4 ? emb_lookup<T, V4>(a, s) : emb_lookup<T, 1>(a, s);
     });
 }
 
 lce_status_t lce_embedding_workspace_size(int64_t N, int64_t V, int64_t H, size_t* bytes) {
     if (!bytes) return LCE_ERR_INVALID_ARG;
     const lce_status_t st = emb_sizes(N, V, H);
-    if (st == LCE_OK) *bytes = emb_space(N, V, nullptr, nullptr);
+    if (st == LCE_OK) *bytes = emb_space(N, V, H, nullptr, nullptr);
     return st;
 }
 
@@ -249,21 +448,16 @@ lce_status_t lce_embedding_backward(int64_t N, int64_t V, int64_t H, int dtype, 
     if (!grad_weight || !aligned_to(grad_weight, dtype_bytes(gtype)) || !ws || !aligned_to(ws, 256)) return LCE_ERR_INVALID_ARG;
     if (N && (!index_ok(tokens, index_bytes) || !grad_y || !aligned_to(grad_y, dtype_bytes(dtype)))) return LCE_ERR_INVALID_ARG;
     EmbSpace e;
-    if (ws_bytes < emb_space(N, V, &e, ws)) return LCE_ERR_WORKSPACE;
+    if (ws_bytes < emb_space(N, V, H, &e, ws)) return LCE_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int where = 0;
-    const lce_status_t sorted = emb_sort(N, V, tokens, index_bytes == 8, padding_token, e, &where, s);
+    const lce_status_t sorted = emb_sort(N, V, tokens, index_bytes == 8, padding_token, !add, e, &where, s);
     if (sorted != LCE_OK) return sorted;
     return with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);
-        const EmbBwd<T> a{static_cast<const T*>(grad_y), ldg, N, V, scale, e.keys[where], e.rows[where], grad_weight, ldgw,
-                          add, static_cast<int32_t>(H)};
-        const dim3 blocks(static_cast<unsigned>(V));
-        if (gtype == LCE_F32)
-            LCE_PROFILED(launch_after(emb_bwd_row<T, float>, blocks, 256, 0, s, a));
-        else
-            LCE_PROFILED(launch_after(emb_bwd_row<T, T>, blocks, 256, 0, s, a));
-        return LCE_OK;
+        const EmbBwd<T> a{static_cast<const T*>(grad_y), ldg, N, V, scale, e.keys[where], e.rows[where], e.named, e.spans,
+                          e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, static_cast<int32_t>(H), 0};
+        return gtype == LCE_F32 ? emb_gradient<T, float>(a, s) : emb_gradient<T, T>(a, s);
     });
 }
 

@@ -26,6 +26,7 @@ struct PlanArgs {
     int64_t *counts, *offsets;
     int32_t R;
     unsigned* stat;
+    __device__ __forceinline__ void begin() const {}
     __device__ __forceinline__ int32_t digit(int64_t i, bool* bad) const {
         if (mask && !mask[i / k]) return E;
         const int64_t e = idx64 ? static_cast<const int64_t*>(experts)[i] : static_cast<const int32_t*>(experts)[i];

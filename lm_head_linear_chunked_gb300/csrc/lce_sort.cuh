@@ -10,6 +10,7 @@
 //     multiples of f.align, the last digit (items to leave out) in none;
 //     then also segment(d, count, start), called by one thread per digit, and
 //     ends(end), one past the last segment, called by all threads of all blocks
+//   void begin()   called by all threads of all blocks of the counting
 //   void status(int any)   with shape.bad: whether an item was bad, once
 #pragma once
 
@@ -55,6 +56,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count(SortJob<F> job) {
     wait_for_primary();
     const int64_t i0 = blockIdx.x * s.per, i1 = i0 + s.per < s.n ? i0 + s.per : s.n;
     bool bad = false;
+    f.begin();
     __syncthreads();
     for (int64_t i = i0 + threadIdx.x; i < i1; i += SORT_THREADS) atomicAdd(counts + f.digit(i, &bad), 1);
     const int any = __syncthreads_or(bad);
