@@ -143,9 +143,9 @@ struct EmbBwd {
     int32_t H, slabs;
 };
 
-// A lane's share of a row's slab: ITEMS vectors, 32 vectors apart, summed in FP32.
+// A lane's share of a row's slab: ITEMS vectors, 32 vectors apart, as pairs of FP32 sums.
 template <typename W, int VEC, int ITEMS>
-__device__ __forceinline__ void emb_store(const float (&s)[VEC * ITEMS], W* row, int k0, int n, float scale, bool add) {
+__device__ __forceinline__ void emb_store(const F2 (&s)[VEC * ITEMS / 2], W* row, int k0, int n, float scale, bool add) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         if (k0 + 32 * i >= n) break;
@@ -153,21 +153,26 @@ __device__ __forceinline__ void emb_store(const float (&s)[VEC * ITEMS], W* row,
         Vec<W, VEC> o{};
         if (add) o = *out;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) o.set(e, add ? fmaf(s[i * VEC + e], scale, o.f(e)) : s[i * VEC + e] * scale);
+        for (int e = 0; e < VEC; ++e) {
+            const float v = (i * VEC + e) & 1 ? hi(s[(i * VEC + e) / 2]) : lo(s[(i * VEC + e) / 2]);
+            o.set(e, add ? fmaf(v, scale, o.f(e)) : v * scale);
+        }
         *out = o;
     }
 }
 
 // The sums.  A warp takes 32 sorted tokens and a slab of columns, loads BATCH
 // rows at a time and adds them up until the token changes.  A run of equal
-// tokens that lies inside the chunk is finished here; the pieces of one that
-// does not go to `parts`: [chunk][0] of a run that comes from the chunk before,
-// [chunk][1] of one that starts here.  So a token that fills half of the batch
-// is spread over as many warps as its rows need.
+// tokens that reaches into the next chunk belongs to the warp it starts in, as
+// long as it has at most 32 rows.  Longer ones are cut at the chunks' borders
+// and their pieces go to `parts`: [chunk][0] of a run that comes from the chunk
+// before, [chunk][1] of one that starts here; so a token that fills half of the
+// batch is spread over as many warps as its rows need.
 // The warps behind those clear the vocabulary rows that no token names.
 template <typename T, typename W, int VEC, int ITEMS, int BATCH>
-__global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
+__global__ void __launch_bounds__(256, 3) emb_sum(EmbBwd<T> a) {
     using V = Vec<T, VEC>;
+    constexpr unsigned ALL = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31;
     const int n = a.H / VEC;
     int64_t item = blockIdx.x * 8ll + (threadIdx.x >> 5);
@@ -176,9 +181,11 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
     if (item >= a.chunks * a.slabs) {
         if (a.add) return;
         const int64_t v0 = (item - a.chunks * a.slabs) * EMB_ZERO_ROWS;
-        for (int64_t v = v0; v < v0 + EMB_ZERO_ROWS && v < a.V; ++v) {
-            if (a.named[v]) continue;
-            Vec<W, VEC>* out = reinterpret_cast<Vec<W, VEC>*>(static_cast<W*>(a.dw) + v * a.lddw);
+        const unsigned named = __ballot_sync(ALL, lane >= EMB_ZERO_ROWS || v0 + lane >= a.V || a.named[v0 + lane]);
+        for (int j = 0; j < EMB_ZERO_ROWS; ++j) {
+            if (named >> j & 1) continue;
+            Vec<W, VEC>* out = reinterpret_cast<Vec<W, VEC>*>(static_cast<W*>(a.dw) + (v0 + j) * a.lddw);
+#pragma unroll 4
             for (int k = lane; k < n; k += 32) out[k] = Vec<W, VEC>{};
         }
         return;
@@ -187,86 +194,101 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
     const int k0 = static_cast<int>(item % a.slabs) * 32 * ITEMS + lane;
     const int64_t at = c * EMB_CHUNK + lane;
     const int32_t none = static_cast<int32_t>(a.V);  // the key of what is left out, behind all others
-    const int32_t key = at < a.N ? a.keys[at] : none;
-    const int32_t row = at < a.N ? a.rows[at] : 0;
-    int32_t next = __shfl_down_sync(0xFFFFFFFFu, key, 1), before = -1;
-    if (lane == 31) next = at + 1 < a.N ? a.keys[at + 1] : none;
-    if (lane == 0 && c > 0) before = a.keys[at - 1];
-    const int items = __popc(__ballot_sync(0xFFFFFFFFu, key < none));
-    const unsigned last = __ballot_sync(0xFFFFFFFFu, key != next || lane == 31);  // of a run or the chunk
-    const bool from_before = __shfl_sync(0xFFFFFFFFu, before == key, 0), goes_on = __shfl_sync(0xFFFFFFFFu, key == next, 31);
-    bool first = true;
-    float s[VEC * ITEMS];
+    const int32_t key = at < a.N ? a.keys[at] : none, key2 = at + EMB_CHUNK < a.N ? a.keys[at + EMB_CHUNK] : none;
+    const int32_t key0 = c > 0 ? a.keys[at - EMB_CHUNK] : -1;  // of the chunk before
+    const int32_t row = at < a.N ? a.rows[at] : 0, row2 = at + EMB_CHUNK < a.N ? a.rows[at + EMB_CHUNK] : 0;
+    const int items = __popc(__ballot_sync(ALL, key < none));
+    if (items == 0) return;
+    const int32_t head = __shfl_sync(ALL, key, 0), tail = __shfl_sync(ALL, key, 31);
+    // rows of the first run before and in this chunk, and of the last one in this chunk and behind it
+    const int head_before = __clz(~__ballot_sync(ALL, key0 == head)), head_here = __ffs(~__ballot_sync(ALL, key == head)) - 1;
+    const int tail_here = __clz(~__ballot_sync(ALL, key == tail)), tail_behind = __ffs(~__ballot_sync(ALL, key2 == tail)) - 1;
+    auto whole = [](int rows) { return rows < 0 ? 32 : rows; };  // __ffs finds nothing where all 32 are equal
+    const bool came = head_before > 0, goes = items == 32 && tail_behind != 0;
+    const bool head_long = came && head_before + whole(head_here) > 32, tail_long = goes && tail_here + whole(tail_behind) > 32;
+    const int begin = came && !head_long ? head_here : 0;                   // the warp before has those
+    const int end = goes && !tail_long ? 32 + tail_behind : items;
+    int32_t next = __shfl_down_sync(ALL, key, 1);
+    if (lane == 31) next = -1;                                              // a border, unless the last run goes on
+    unsigned last = __ballot_sync(ALL, key != next);
+    if (end > 32) last &= 0x7FFFFFFFu;
+    constexpr int PAIRS = VEC * ITEMS / 2;
+    F2 s[PAIRS];
 #pragma unroll
-    for (int e = 0; e < VEC * ITEMS; ++e) s[e] = 0.f;
-    for (int i0 = 0; i0 < items; i0 += BATCH) {
-        V x[BATCH][ITEMS];
+    for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
+    for (int i0 = begin; i0 < end; i0 += BATCH) {
+        RowVectors<T, VEC, ITEMS> x[BATCH];
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
-            const int64_t r = __shfl_sync(0xFFFFFFFFu, row, i0 + b);
+            const int64_t r = __shfl_sync(ALL, i0 + b < 32 ? row : row2, (i0 + b) & 31);
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
-                x[b][i] = V{};
-                if (i0 + b < items && k0 + 32 * i < n) x[b][i] = reinterpret_cast<const V*>(a.dy + r * a.ldd)[k0 + 32 * i];
+                x[b].v[i] = V{};
+                if (i0 + b < end && k0 + 32 * i < n) x[b].v[i] = reinterpret_cast<const V*>(a.dy + r * a.ldd)[k0 + 32 * i];
             }
         }
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
-            if (i0 + b >= items) break;
+            if (i0 + b >= end) break;
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) s[i * VEC + e] += x[b][i].f(e);
-            if (!(last >> (i0 + b) & 1)) continue;
-            const int64_t v = __shfl_sync(0xFFFFFFFFu, key, i0 + b);
-            const bool came = first && from_before, goes = i0 + b == 31 && goes_on;
-            if (!came && !goes) {
+            for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], x[b].pair(p));
+            const int at_end = i0 + b;
+            if (at_end < 32 ? !(last >> at_end & 1) : at_end + 1 < end) continue;
+            const int64_t v = at_end < 32 ? __shfl_sync(ALL, key, at_end) : tail;
+            const bool is_head = v == head && head_long, is_tail = v == tail && tail_long;
+            if (!is_head && !is_tail) {
                 emb_store<W, VEC, ITEMS>(s, static_cast<W*>(a.dw) + v * a.lddw, k0, n, a.scale, a.add);
             } else {
-                emb_store<float, VEC, ITEMS>(s, a.parts + (c * 2 + (came ? 0 : 1)) * a.H, k0, n, 1.f, false);
-                if (!came && k0 == 0) a.spans[1 + atomicAdd(a.spans, 1)] = static_cast<int32_t>(c);
+                emb_store<float, VEC, ITEMS>(s, a.parts + (c * 2 + (is_head ? 0 : 1)) * a.H, k0, n, 1.f, false);
+                if (!is_head && k0 == 0) a.spans[1 + atomicAdd(a.spans, 1)] = static_cast<int32_t>(c);
             }
-            first = false;
 #pragma unroll
-            for (int e = 0; e < VEC * ITEMS; ++e) s[e] = 0.f;
+            for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
         }
     }
 }
 
-// The runs that reach past a chunk: 32 columns of one per block, its pieces
-// shared out over 32 rows of threads and added in a fixed order.
-template <typename W>
-__global__ void __launch_bounds__(1024) emb_join(EmbBwd<float> a) {
-    __shared__ float s[32][33];
-    const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+// The runs that reach past a chunk: a slab of columns of one per block, its
+// pieces shared out over eight warps and added in a fixed order.
+template <typename W, int VEC, int ITEMS>
+__global__ void __launch_bounds__(256) emb_join(EmbBwd<float> a) {
+    constexpr int PAIRS = VEC * ITEMS / 2;
+    __shared__ F2 s[8][PAIRS][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = a.H / VEC;
     wait_for_primary();
-    const int slabs = (a.H + 31) / 32;
-    const int64_t items = static_cast<int64_t>(*a.spans) * slabs;
+    const int64_t items = static_cast<int64_t>(*a.spans) * a.slabs;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t c0 = a.spans[1 + item / slabs];
-        const int col = static_cast<int>(item % slabs) * 32 + c;
+        const int64_t c0 = a.spans[1 + item / a.slabs];
+        const int k0 = static_cast<int>(item % a.slabs) * 32 * ITEMS + lane;
         const int32_t v = a.keys[c0 * EMB_CHUNK + EMB_CHUNK - 1];
-        int64_t lo = c0 + 1, hi = a.chunks;  // the first chunk that does not start with v
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (a.keys[mid * EMB_CHUNK] == v)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        float sum = 0.f;
-        if (col < a.H) {
-            if (k == 0) sum = a.parts[(c0 * 2 + 1) * a.H + col];
+        int64_t end = c0 + 1;  // the first chunk that does not start with v
+        for (unsigned same = 0xFFFFFFFFu; same == 0xFFFFFFFFu; end += same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1)
+            same = __ballot_sync(0xFFFFFFFFu, end + lane < a.chunks && a.keys[(end + lane) * EMB_CHUNK] == v);
+        F2 sum[PAIRS];
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) sum[p] = f2(0.f);
+        auto add = [&](int64_t part) {
+            RowVectors<float, VEC, ITEMS> x;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                x.v[i] = Vec<float, VEC>{};
+                if (k0 + 32 * i < n) x.v[i] = reinterpret_cast<const Vec<float, VEC>*>(a.parts + part * a.H)[k0 + 32 * i];
+            }
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p) sum[p] = add2(sum[p], x.pair(p));
+        };
+        if (warp == 0) add(c0 * 2 + 1);
 #pragma unroll 8
-            for (int64_t p = c0 + 1 + k; p < lo; p += 32) sum += a.parts[p * 2 * a.H + col];
-        }
-        s[k][c] = sum;
+        for (int64_t c = c0 + 1 + warp; c < end; c += 8) add(c * 2);
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) s[warp][p][lane] = sum[p];
         __syncthreads();
-        sum = warp_sum(s[c][k]);  // column k of the slab
-        const int64_t out = (item % slabs) * 32 + k;
-        if (c == 0 && out < a.H) {
-            W* dw = static_cast<W*>(a.dw) + v * a.lddw + out;
-            *dw = from_f32<W>(a.add ? fmaf(sum, a.scale, to_f32(*dw)) : sum * a.scale);
+        if (warp == 0) {
+            for (int w = 1; w < 8; ++w)
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p) sum[p] = add2(sum[p], s[w][p][lane]);
+            emb_store<W, VEC, ITEMS>(sum, static_cast<W*>(a.dw) + v * a.lddw, k0, n, a.scale, a.add);
         }
         __syncthreads();
     }
@@ -351,13 +373,14 @@ int vector_of(const void* p, int64_t ld, int64_t H) {
 
 template <typename T, int VEC>
 lce_status_t emb_lookup(const EmbFwd<T>& a, cudaStream_t s) {
-    // four vectors a lane where that still gives every SM its warps, one for a decode step
-    const int64_t n = a.H / VEC, four = a.N * ((n + 127) / 128);
-    const bool wide = n > 32 && four >= 152 * 32;
-    const int64_t blocks = ((wide ? four : a.N * ((n + 31) / 32)) + 7) / 8;
+    // several vectors a lane where that still gives every SM its warps, one for a decode step
+    constexpr int U = VEC * sizeof(T) == 16 ? 4 : 8;
+    const int64_t n = a.H / VEC, wide = a.N * ((n + 32 * U - 1) / (32 * U));
+    const bool enough = n > 32 && wide >= 152 * 32;
+    const int64_t blocks = ((enough ? wide : a.N * ((n + 31) / 32)) + 7) / 8;
     if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
-    if (wide)
-        LCE_PROFILED(emb_fwd<T, VEC, 4><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+    if (enough)
+        LCE_PROFILED(emb_fwd<T, VEC, U><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
     else
         LCE_PROFILED(emb_fwd<T, VEC, 1><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
     return LCE_OK;
@@ -384,8 +407,11 @@ lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
     j.chunks = a.chunks;
     j.add = a.add;
     j.H = a.H;
-    const int64_t most = (a.chunks - 1) * ((a.H + 31) / 32);
-    LCE_PROFILED(launch_after(emb_join<W>, dim3(static_cast<unsigned>(most < 304 ? most : 304)), 1024, 0, s, j));
+    // 16-byte vectors of FP32 where dw's rows have vectors at all, and few columns to a block: there are few long runs
+    constexpr int JVEC = VEC % 4 == 0 ? 4 : VEC, JITEMS = JVEC == 4 ? 1 : 4 / JVEC;
+    j.slabs = static_cast<int32_t>((a.H / JVEC + 32 * JITEMS - 1) / (32 * JITEMS));
+    const int64_t most = (a.chunks - 1) * j.slabs;
+    LCE_PROFILED(launch_after(emb_join<W, JVEC, JITEMS>, dim3(static_cast<unsigned>(most < 1216 ? most : 1216)), 256, 0, s, j));
     return LCE_OK;
 }
 

@@ -1,6 +1,7 @@
 // A stable counting sort by one digit, in two kernels: every block counts the
 // digits of its share of the items, then every block adds up what the others
-// have counted and puts its items in their places.  The places depend on the
+// have counted and puts its items in their places (one block needs the second
+// kernel alone).  The places depend on the
 // items alone, so what is summed in the sorted order has equal bits every time.
 //
 // What the items are is up to a functor F:
@@ -10,19 +11,23 @@
 //     multiples of f.align, the last digit (items to leave out) in none;
 //     then also segment(d, count, start), called by one thread per digit, and
 //     ends(end), one past the last segment, called by all threads of all blocks
-//   void begin()   called by all threads of all blocks of the counting
+//   void begin()   called by all threads of all blocks before anything is put
 //   void status(int any)   with shape.bad: whether an item was bad, once
 #pragma once
+
+#include <atomic>
 
 #include "lce_internal.cuh"
 #include "lce_vec.cuh"
 
 namespace lce {
 
-constexpr int SORT_WARPS = 8;
+// A block is as large as it can be, as every block adds up what all the others
+// have counted: 131072 items in 64 blocks of 1024 threads, not 128 of 256.
+constexpr int SORT_WARPS = 32;
 constexpr int SORT_THREADS = 32 * SORT_WARPS;
-constexpr int SORT_BINS_MAX = 1025;  // (SORT_WARPS + 1) counters each fit the 48 KB of a block without asking
-constexpr int64_t SORT_ITEMS = 1024; // a block's fewest
+constexpr int SORT_BINS_MAX = 1025;
+constexpr int64_t SORT_ITEMS = 2048;  // a block's fewest
 constexpr int64_t SORT_BLOCKS = 152;
 
 struct SortShape {
@@ -36,7 +41,7 @@ inline int64_t sort_blocks(int64_t n) {
     const int64_t b = (n + SORT_ITEMS - 1) / SORT_ITEMS;
     return b < 1 ? 1 : (b < SORT_BLOCKS ? b : SORT_BLOCKS);
 }
-inline size_t sort_smem(int bins) { return static_cast<size_t>(SORT_WARPS + 1) * bins * 4; }
+inline size_t sort_smem(int bins) { return static_cast<size_t>(SORT_WARPS) * bins * 4; }
 
 namespace {
 
@@ -68,27 +73,42 @@ template <typename F>
 __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     const F& f = job.f;
     const SortShape& s = job.shape;
-    extern __shared__ int32_t counts[];  // [SORT_WARPS, bins], then [bins]
+    extern __shared__ int32_t counts[];  // [SORT_WARPS, bins]: of each warp's items, then their places
     __shared__ int32_t sums[SORT_WARPS];
     launch_dependents();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    int32_t* first = counts + SORT_WARPS * s.bins;
     for (int d = t; d < SORT_WARPS * s.bins; d += SORT_THREADS) counts[d] = 0;
     wait_for_primary();
+    const bool alone = s.blocks == 1;  // nothing has been counted before
+    bool bad = false;
+    if (alone) f.begin();
+    __syncthreads();
+    // each warp a stretch of the block's items
+    const int64_t i0 = blockIdx.x * s.per, i1 = i0 + s.per < s.n ? i0 + s.per : s.n;
+    const int64_t share = (s.per + SORT_THREADS - 1) / SORT_THREADS * 32;
+    const int64_t w0 = i0 + warp * share, w1 = w0 + share < i1 ? w0 + share : i1;
+    int32_t* own = counts + warp * s.bins;
+    for (int64_t i = w0 + lane; i < w1; i += 32) atomicAdd(own + f.digit(i, &bad), 1);
     // each thread a stretch of the digits: their items in all blocks, and in those before this one
     constexpr int MOST = (SORT_BINS_MAX + SORT_THREADS - 1) / SORT_THREADS;
     const int each = (s.bins + SORT_THREADS - 1) / SORT_THREADS;
     int32_t total[MOST], before[MOST], mine = 0;
+    if (alone) bad = __syncthreads_or(bad);
 #pragma unroll
     for (int j = 0; j < MOST; ++j) {
         const int d = t * each + j;
         total[j] = before[j] = 0;
         if (j < each && d < s.bins) {
+            if (alone) {
+#pragma unroll
+                for (int w = 0; w < SORT_WARPS; ++w) total[j] += counts[w * s.bins + d];
+            } else {
 #pragma unroll 16
-            for (int b = 0; b < s.blocks; ++b) {
-                const int32_t c = s.hist[static_cast<int64_t>(b) * s.bins + d];
-                total[j] += c;
-                before[j] += b < static_cast<int>(blockIdx.x) ? c : 0;
+                for (int b = 0; b < s.blocks; ++b) {
+                    const int32_t c = s.hist[static_cast<int64_t>(b) * s.bins + d];
+                    total[j] += c;
+                    before[j] += b < static_cast<int>(blockIdx.x) ? c : 0;
+                }
             }
         }
         if constexpr (F::SEGMENTS) {
@@ -106,35 +126,23 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     }
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    int32_t start = upto - mine;
-    for (int w = 0; w < warp; ++w) start += sums[w];
+    int32_t start = upto - mine + warp_sum(lane < warp ? sums[lane] : 0);
 #pragma unroll
     for (int j = 0; j < MOST; ++j) {
         const int d = t * each + j;
         if (j >= each || d >= s.bins) break;
-        first[d] = start + before[j];
-        if constexpr (F::SEGMENTS) {
-            if (d % s.blocks == static_cast<int>(blockIdx.x)) f.segment(d, total[j], start);
-            start += (total[j] + f.align - 1) / f.align * f.align;
-        } else {
-            start += total[j];
-        }
-    }
-    // each warp a stretch of the block's items, counted, then put one after the other
-    const int64_t i0 = blockIdx.x * s.per, i1 = i0 + s.per < s.n ? i0 + s.per : s.n;
-    const int64_t share = (s.per + 32 * SORT_WARPS - 1) / (32 * SORT_WARPS) * 32;
-    const int64_t w0 = i0 + warp * share, w1 = w0 + share < i1 ? w0 + share : i1;
-    int32_t* own = counts + warp * s.bins;
-    bool bad = false;
-    for (int64_t i = w0 + lane; i < w1; i += 32) atomicAdd(own + f.digit(i, &bad), 1);
-    __syncthreads();
-    for (int d = t; d < s.bins; d += SORT_THREADS) {
-        int32_t at = first[d];
+        int32_t at = start + before[j];
 #pragma unroll
         for (int w = 0; w < SORT_WARPS; ++w) {
             const int32_t c = counts[w * s.bins + d];
             counts[w * s.bins + d] = at;
             at += c;
+        }
+        if constexpr (F::SEGMENTS) {
+            if (d % s.blocks == static_cast<int>(blockIdx.x)) f.segment(d, total[j], start);
+            start += (total[j] + f.align - 1) / f.align * f.align;
+        } else {
+            start += total[j];
         }
     }
     __syncthreads();
@@ -152,29 +160,43 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
         }
         __syncwarp();
     }
-    if constexpr (F::SEGMENTS) {
-        int32_t end = 0;
-        for (int w = 0; w < SORT_WARPS; ++w) end += sums[w];
-        f.ends(end);
+    if constexpr (F::SEGMENTS) f.ends(warp_sum(sums[lane]));
+    if (s.bad && blockIdx.x == 0) {
+        const int any = alone ? bad : __syncthreads_or(t < s.blocks && s.bad[t]);
+        if (t == 0) f.status(any);
     }
-    if (s.bad && blockIdx.x == 0 && t == 0) {
-        int any = 0;
-        for (int b = 0; b < s.blocks; ++b) any |= s.bad[b];
-        f.status(any);
-    }
+}
+
+// Lets a kernel take `bytes` of dynamic shared memory; asked once per device.
+template <typename K>
+bool allow_smem(std::atomic<uint64_t>* known, K kernel, int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (known->load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    known->fetch_or(bit, std::memory_order_relaxed);
+    return true;
 }
 
 // Sorts by one digit; `first`: after all that came before it in the stream,
 // else under the kernel before it, whose results it waits for.
 template <typename F>
 lce_status_t sort_by(const F& f, const SortShape& shape, bool first, cudaStream_t s) {
+    static std::atomic<uint64_t> known{0};
+    if (!allow_smem(&known, sort_place<F>, static_cast<int>(sort_smem(SORT_BINS_MAX)))) return LCE_ERR_CUDA;
     const SortJob<F> job{f, shape};
     const unsigned blocks = static_cast<unsigned>(shape.blocks);
-    if (first)
-        LCE_PROFILED(sort_count<F><<<blocks, SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s>>>(job));
+    if (blocks > 1) {
+        if (first)
+            LCE_PROFILED(sort_count<F><<<blocks, SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s>>>(job));
+        else
+            LCE_PROFILED(launch_after(sort_count<F>, dim3(blocks), SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s, job));
+    }
+    if (blocks == 1 && first)
+        LCE_PROFILED(sort_place<F><<<1, SORT_THREADS, sort_smem(shape.bins), s>>>(job));
     else
-        LCE_PROFILED(launch_after(sort_count<F>, dim3(blocks), SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s, job));
-    LCE_PROFILED(launch_after(sort_place<F>, dim3(blocks), SORT_THREADS, sort_smem(shape.bins), s, job));
+        LCE_PROFILED(launch_after(sort_place<F>, dim3(blocks), SORT_THREADS, sort_smem(shape.bins), s, job));
     return LCE_OK;
 }
 

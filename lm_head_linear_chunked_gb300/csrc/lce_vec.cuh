@@ -208,7 +208,8 @@ cudaError_t launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStre
     return cudaLaunchKernelEx(&config, kernel, args);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+template <typename T>
+__device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
