@@ -74,9 +74,14 @@ struct EmbSpace {
     float* parts;            // [chunks, 2, H]
 };
 
+struct SortItem {
+    int32_t digit, key, row;
+};
+
 // The first digit: tokens as they come.  V stands for the ones to leave out.
 struct FirstDigit {
     static constexpr bool SEGMENTS = false;
+    using Item = SortItem;
     const void* tokens;
     bool idx64;
     int32_t V, mask;
@@ -92,20 +97,17 @@ struct FirstDigit {
                  v += static_cast<int64_t>(gridDim.x) * SORT_THREADS)
                 reinterpret_cast<uint4*>(named)[v] = make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ int32_t key(int64_t i, bool* bad) const {
+    __device__ __forceinline__ Item load(int64_t i, bool* bad) const {
         const int64_t v = token_at(tokens, idx64, i);
-        if (v == padding) return V;
-        if (v >= 0 && v < V) return static_cast<int32_t>(v);
-        *bad = true;
-        return V;
+        const bool in = v >= 0 && v < V && v != padding;
+        *bad |= !in && v != padding;
+        const int32_t key = in ? static_cast<int32_t>(v) : V;
+        return {key & mask, key, static_cast<int32_t>(i)};
     }
-    __device__ __forceinline__ int32_t digit(int64_t i, bool* bad) const { return key(i, bad) & mask; }
-    __device__ __forceinline__ void put(int64_t i, int32_t, int32_t at) const {
-        bool bad;
-        const int32_t v = key(i, &bad);
-        keys[at] = v;
-        rows[at] = static_cast<int32_t>(i);
-        if (named && v < V) named[v] = 1;
+    __device__ __forceinline__ void put(const Item& x, int32_t at) const {
+        keys[at] = x.key;
+        rows[at] = x.row;
+        if (named && x.key < V) named[x.key] = 1;
     }
     __device__ __forceinline__ void status(int any) const { *stat = any ? STATUS_INDEX : 0u; }
 };
@@ -113,14 +115,18 @@ struct FirstDigit {
 // A later digit.
 struct NextDigit {
     static constexpr bool SEGMENTS = false;
+    using Item = SortItem;
     const int32_t *from_keys, *from_rows;
     int32_t shift, mask;
     int32_t *keys, *rows;
     __device__ __forceinline__ void begin() const {}
-    __device__ __forceinline__ int32_t digit(int64_t i, bool*) const { return from_keys[i] >> shift & mask; }
-    __device__ __forceinline__ void put(int64_t i, int32_t, int32_t at) const {
-        keys[at] = from_keys[i];
-        rows[at] = from_rows[i];
+    __device__ __forceinline__ Item load(int64_t i, bool*) const {
+        const int32_t key = from_keys[i];
+        return {key >> shift & mask, key, from_rows[i]};
+    }
+    __device__ __forceinline__ void put(const Item& x, int32_t at) const {
+        keys[at] = x.key;
+        rows[at] = x.row;
     }
     __device__ __forceinline__ void status(int) const {}
 };

@@ -18,6 +18,9 @@ namespace {
 
 struct PlanArgs {
     static constexpr bool SEGMENTS = true;
+    struct Item {
+        int32_t digit, slot;
+    };
     const void* experts;
     bool idx64;
     const uint8_t* mask;   // nullable; one byte per token
@@ -27,16 +30,17 @@ struct PlanArgs {
     int32_t R;
     unsigned* stat;
     __device__ __forceinline__ void begin() const {}
-    __device__ __forceinline__ int32_t digit(int64_t i, bool* bad) const {
-        if (mask && !mask[i / k]) return E;
+    __device__ __forceinline__ Item load(int64_t i, bool* bad) const {
+        const int32_t slot = static_cast<int32_t>(i);
         const int64_t e = idx64 ? static_cast<const int64_t*>(experts)[i] : static_cast<const int32_t*>(experts)[i];
-        if (e >= 0 && e < E) return static_cast<int32_t>(e);
+        if (mask && !mask[slot / k]) return {E, slot};
+        if (e >= 0 && e < E) return {static_cast<int32_t>(e), slot};
         if (e != -1) *bad = true;
-        return E;
+        return {E, slot};
     }
-    __device__ __forceinline__ void put(int64_t i, int32_t e, int32_t at) const {
-        positions[i] = e < E ? at : -1;
-        if (e < E) slots[at] = static_cast<int32_t>(i);
+    __device__ __forceinline__ void put(const Item& x, int32_t at) const {
+        positions[x.slot] = x.digit < E ? at : -1;
+        if (x.digit < E) slots[at] = x.slot;
     }
     __device__ __forceinline__ void segment(int32_t e, int32_t count, int32_t start) const {
         offsets[e] = start;

@@ -5,13 +5,13 @@
 // items alone, so what is summed in the sorted order has equal bits every time.
 //
 // What the items are is up to a functor F:
-//   int32_t digit(int64_t i, bool* bad)   item i's digit in [0, bins)
-//   void put(int64_t i, int32_t d, int32_t at)   item i belongs at place `at`
+//   Item load(int64_t i, bool* bad)   item i, whose `digit` lies in [0, bins)
+//   void put(const Item& x, int32_t at)   x belongs at place `at`
+//   void begin()   called by all threads of all blocks before anything is put
 //   static constexpr bool SEGMENTS: whether digits have segments that start on
 //     multiples of f.align, the last digit (items to leave out) in none;
 //     then also segment(d, count, start), called by one thread per digit, and
 //     ends(end), one past the last segment, called by all threads of all blocks
-//   void begin()   called by all threads of all blocks before anything is put
 //   void status(int any)   with shape.bad: whether an item was bad, once
 #pragma once
 
@@ -51,11 +51,30 @@ struct SortJob {
     SortShape shape;
 };
 
+// Calls g(item, whether there is one) for the items i, i + step, ... before end,
+// loading several at a time: a block has few, and waits for each load.
+template <typename F, typename G>
+__device__ __forceinline__ void sort_items(const F& f, int64_t i, int64_t end, int64_t step, bool* bad, G g) {
+    constexpr int AHEAD = 4;
+    const int64_t lane = threadIdx.x & 31;
+    for (; i - lane < end; i += AHEAD * step) {  // the lanes of a warp stay together
+        typename F::Item x[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (i + k * step < end) x[k] = f.load(i + k * step, bad);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (i - lane + k * step >= end) break;
+            g(x[k], i + k * step < end);
+        }
+    }
+}
+
 template <typename F>
 __global__ void __launch_bounds__(SORT_THREADS) sort_count(SortJob<F> job) {
     const F& f = job.f;
     const SortShape& s = job.shape;
-    extern __shared__ int32_t counts[];
+    extern __shared__ __align__(16) int32_t counts[];
     launch_dependents();
     for (int d = threadIdx.x; d < s.bins; d += SORT_THREADS) counts[d] = 0;
     wait_for_primary();
@@ -63,7 +82,9 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count(SortJob<F> job) {
     bool bad = false;
     f.begin();
     __syncthreads();
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += SORT_THREADS) atomicAdd(counts + f.digit(i, &bad), 1);
+    sort_items(f, i0 + threadIdx.x, i1, SORT_THREADS, &bad, [&](const typename F::Item& x, bool in) {
+        if (in) atomicAdd(counts + x.digit, 1);
+    });
     const int any = __syncthreads_or(bad);
     for (int d = threadIdx.x; d < s.bins; d += SORT_THREADS) s.hist[static_cast<int64_t>(blockIdx.x) * s.bins + d] = counts[d];
     if (threadIdx.x == 0 && s.bad) s.bad[blockIdx.x] = any;
@@ -73,11 +94,11 @@ template <typename F>
 __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     const F& f = job.f;
     const SortShape& s = job.shape;
-    extern __shared__ int32_t counts[];  // [SORT_WARPS, bins]: of each warp's items, then their places
+    extern __shared__ __align__(16) int32_t counts[];  // [SORT_WARPS, bins]: of each warp's items, then their places
     __shared__ int32_t sums[SORT_WARPS];
     launch_dependents();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    for (int d = t; d < SORT_WARPS * s.bins; d += SORT_THREADS) counts[d] = 0;
+    for (int d = t; d < SORT_WARPS * s.bins / 4; d += SORT_THREADS) reinterpret_cast<int4*>(counts)[d] = make_int4(0, 0, 0, 0);
     wait_for_primary();
     const bool alone = s.blocks == 1;  // nothing has been counted before
     bool bad = false;
@@ -88,7 +109,9 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     const int64_t share = (s.per + SORT_THREADS - 1) / SORT_THREADS * 32;
     const int64_t w0 = i0 + warp * share, w1 = w0 + share < i1 ? w0 + share : i1;
     int32_t* own = counts + warp * s.bins;
-    for (int64_t i = w0 + lane; i < w1; i += 32) atomicAdd(own + f.digit(i, &bad), 1);
+    sort_items(f, w0 + lane, w1, 32, &bad, [&](const typename F::Item& x, bool in) {
+        if (in) atomicAdd(own + x.digit, 1);
+    });
     // each thread a stretch of the digits: their items in all blocks, and in those before this one
     constexpr int MOST = (SORT_BINS_MAX + SORT_THREADS - 1) / SORT_THREADS;
     const int each = (s.bins + SORT_THREADS - 1) / SORT_THREADS;
@@ -103,11 +126,15 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
 #pragma unroll
                 for (int w = 0; w < SORT_WARPS; ++w) total[j] += counts[w * s.bins + d];
             } else {
-#pragma unroll 16
-                for (int b = 0; b < s.blocks; ++b) {
-                    const int32_t c = s.hist[static_cast<int64_t>(b) * s.bins + d];
-                    total[j] += c;
-                    before[j] += b < static_cast<int>(blockIdx.x) ? c : 0;
+                for (int b0 = 0; b0 < s.blocks; b0 += 16) {  // sixteen loads on their way
+                    int32_t c[16];
+#pragma unroll
+                    for (int b = 0; b < 16; ++b) c[b] = b0 + b < s.blocks ? s.hist[static_cast<int64_t>(b0 + b) * s.bins + d] : 0;
+#pragma unroll
+                    for (int b = 0; b < 16; ++b) {
+                        total[j] += c[b];
+                        before[j] += b0 + b < static_cast<int>(blockIdx.x) ? c[b] : 0;
+                    }
                 }
             }
         }
@@ -146,20 +173,17 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
         }
     }
     __syncthreads();
-    for (int64_t base = w0; base < w1; base += 32) {
-        const int64_t i = base + lane;
-        const bool in = i < w1;
+    sort_items(f, w0 + lane, w1, 32, &bad, [&](const typename F::Item& x, bool in) {
         const unsigned active = __ballot_sync(0xFFFFFFFFu, in);
         if (in) {
-            const int32_t d = f.digit(i, &bad);
-            const unsigned same = __match_any_sync(active, d);
-            const int32_t at = own[d] + __popc(same & ((1u << lane) - 1));
+            const unsigned same = __match_any_sync(active, x.digit);
+            const int32_t at = own[x.digit] + __popc(same & ((1u << lane) - 1));
             __syncwarp(active);
-            if ((same >> lane) == 1u) own[d] = at + 1;  // the last of them
-            f.put(i, d, at);
+            if ((same >> lane) == 1u) own[x.digit] = at + 1;  // the last of them
+            f.put(x, at);
         }
         __syncwarp();
-    }
+    });
     if constexpr (F::SEGMENTS) f.ends(warp_sum(sums[lane]));
     if (s.bad && blockIdx.x == 0) {
         const int any = alone ? bad : __syncthreads_or(t < s.blocks && s.bad[t]);
