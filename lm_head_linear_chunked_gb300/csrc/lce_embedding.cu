@@ -68,11 +68,37 @@ __global__ void __launch_bounds__(256) emb_fwd(EmbFwd<T> a) {
 // The workspace.
 struct EmbSpace {
     WsHeader* hdr;
-    int32_t* spans;          // how many runs reach past the chunk they start in; from [1] on, those chunks
+    int32_t* n_spans;        // how many runs were cut at chunks' borders
+    int4* spans;             // [chunks]: the first and one past the last chunk of one, and its token
     uint8_t* named;          // [V]: 1 for rows that a token names
     int32_t *bad, *hist, *keys[2], *rows[2];
     float* parts;            // [chunks, 2, H]
 };
+
+// A share of the gradient's rows to be cleared.
+struct Clear {
+    uint8_t* at;
+    int64_t rows, bytes;  // of a row
+    int64_t stride;       // bytes from row to row
+    int part, of;         // the shares of all rows that its first kernel takes, the next one the next
+};
+
+__device__ __forceinline__ void clear_bytes(uint8_t* p, int64_t n) {  // by a block; p and n even
+    const int64_t head = -reinterpret_cast<intptr_t>(p) & 15, lead = head < n ? head : n;
+    const int64_t mid = (n - lead) / 16;
+    for (int64_t i = threadIdx.x; i < lead / 2; i += SORT_THREADS) reinterpret_cast<uint16_t*>(p)[i] = 0;
+    uint4* q = reinterpret_cast<uint4*>(p + lead);
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < mid; i += SORT_THREADS) q[i] = make_uint4(0, 0, 0, 0);
+    for (int64_t i = lead + mid * 16 + 2 * threadIdx.x; i < n; i += 2 * SORT_THREADS) *reinterpret_cast<uint16_t*>(p + i) = 0;
+}
+
+__device__ __forceinline__ void clear_share(const Clear& c, int kernel, int64_t block, int64_t of) {
+    const int64_t first = c.rows * (c.part + kernel) / c.of, rows = c.rows * (c.part + kernel + 1) / c.of - first;
+    const int64_t r0 = first + rows * block / of, r1 = first + rows * (block + 1) / of;
+    if (c.stride == c.bytes) return clear_bytes(c.at + r0 * c.bytes, (r1 - r0) * c.bytes);
+    for (int64_t r = r0; r < r1; ++r) clear_bytes(c.at + r * c.stride, c.bytes);
+}
 
 struct SortItem {
     int32_t digit, key, row;
@@ -88,13 +114,16 @@ struct FirstDigit {
     int64_t padding;
     int32_t *keys, *rows;
     unsigned* stat;
-    int32_t* spans;
+    int32_t* n_spans;
     uint8_t* named;  // nullable
+    int32_t sorting;  // blocks that sort
+    Clear clear;
+    __device__ __forceinline__ void beside(int kernel, int64_t block, int64_t of) const { clear_share(clear, kernel, block, of); }
     __device__ __forceinline__ void begin() const {
-        if (blockIdx.x == 0 && threadIdx.x == 0) *spans = 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0) *n_spans = 0;
         if (named)
             for (int64_t v = static_cast<int64_t>(blockIdx.x) * SORT_THREADS + threadIdx.x; v * 16 < V;
-                 v += static_cast<int64_t>(gridDim.x) * SORT_THREADS)
+                 v += static_cast<int64_t>(sorting) * SORT_THREADS)
                 reinterpret_cast<uint4*>(named)[v] = make_uint4(0, 0, 0, 0);
     }
     __device__ __forceinline__ Item load(int64_t i, bool* bad) const {
@@ -107,7 +136,6 @@ struct FirstDigit {
     __device__ __forceinline__ void put(const Item& x, int32_t at) const {
         keys[at] = x.key;
         rows[at] = x.row;
-        if (named && x.key < V) named[x.key] = 1;
     }
     __device__ __forceinline__ void status(int any) const { *stat = any ? STATUS_INDEX : 0u; }
 };
@@ -119,6 +147,8 @@ struct NextDigit {
     const int32_t *from_keys, *from_rows;
     int32_t shift, mask;
     int32_t *keys, *rows;
+    Clear clear;
+    __device__ __forceinline__ void beside(int kernel, int64_t block, int64_t of) const { clear_share(clear, kernel, block, of); }
     __device__ __forceinline__ void begin() const {}
     __device__ __forceinline__ Item load(int64_t i, bool*) const {
         const int32_t key = from_keys[i];
@@ -132,6 +162,7 @@ struct NextDigit {
 };
 
 constexpr int EMB_CHUNK = 32;       // sorted tokens of a warp
+constexpr int EMB_AHEAD = 8;         // rows of it on their way
 constexpr int EMB_ZERO_ROWS = 8;    // vocabulary rows of a warp that looks for rows to clear
 
 template <typename T>
@@ -140,13 +171,15 @@ struct EmbBwd {
     int64_t ldd, N, V;
     float scale;
     const int32_t *keys, *rows;  // sorted
-    const uint8_t* named;
-    int32_t* spans;
+    uint8_t* named;        // nullable: the others need not be cleared
+    int32_t* n_spans;
+    int4* spans;
     float* parts;
     void* dw;
     int64_t lddw, chunks;
     bool add;
     int32_t H, slabs;
+    int32_t joining;  // blocks of the last kernel that add pieces up
 };
 
 // A lane's share of a row's slab: ITEMS vectors, 32 vectors apart, as pairs of FP32 sums.
@@ -167,16 +200,16 @@ __device__ __forceinline__ void emb_store(const F2 (&s)[VEC * ITEMS / 2], W* row
     }
 }
 
-// The sums.  A warp takes 32 sorted tokens and a slab of columns, loads BATCH
-// rows at a time and adds them up until the token changes.  A run of equal
-// tokens that reaches into the next chunk belongs to the warp it starts in, as
+// The sums.  A warp takes 32 sorted tokens and a slab of columns, copies their
+// rows ahead to shared memory and adds them up until the token changes.  A run
+// of equal tokens that reaches into the next chunk belongs to the warp it starts in, as
 // long as it has at most 32 rows.  Longer ones are cut at the chunks' borders
 // and their pieces go to `parts`: [chunk][0] of a run that comes from the chunk
 // before, [chunk][1] of one that starts here; so a token that fills half of the
 // batch is spread over as many warps as its rows need.
-// The warps behind those clear the vocabulary rows that no token names.
-template <typename T, typename W, int VEC, int ITEMS, int BATCH>
-__global__ void __launch_bounds__(256, 3) emb_sum(EmbBwd<T> a) {
+template <typename T, typename W, int VEC, int ITEMS>
+__global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
+    extern __shared__ __align__(16) uint8_t dyn[];
     using V = Vec<T, VEC>;
     constexpr unsigned ALL = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31;
@@ -184,18 +217,7 @@ __global__ void __launch_bounds__(256, 3) emb_sum(EmbBwd<T> a) {
     int64_t item = blockIdx.x * 8ll + (threadIdx.x >> 5);
     launch_dependents();
     wait_for_primary();
-    if (item >= a.chunks * a.slabs) {
-        if (a.add) return;
-        const int64_t v0 = (item - a.chunks * a.slabs) * EMB_ZERO_ROWS;
-        const unsigned named = __ballot_sync(ALL, lane >= EMB_ZERO_ROWS || v0 + lane >= a.V || a.named[v0 + lane]);
-        for (int j = 0; j < EMB_ZERO_ROWS; ++j) {
-            if (named >> j & 1) continue;
-            Vec<W, VEC>* out = reinterpret_cast<Vec<W, VEC>*>(static_cast<W*>(a.dw) + (v0 + j) * a.lddw);
-#pragma unroll 4
-            for (int k = lane; k < n; k += 32) out[k] = Vec<W, VEC>{};
-        }
-        return;
-    }
+    if (item >= a.chunks * a.slabs) return;
     const int64_t c = item / a.slabs;
     const int k0 = static_cast<int>(item % a.slabs) * 32 * ITEMS + lane;
     const int64_t at = c * EMB_CHUNK + lane;
@@ -218,59 +240,102 @@ __global__ void __launch_bounds__(256, 3) emb_sum(EmbBwd<T> a) {
     if (lane == 31) next = -1;                                              // a border, unless the last run goes on
     unsigned last = __ballot_sync(ALL, key != next);
     if (end > 32) last &= 0x7FFFFFFFu;
+    if (tail_long && !(head_long && head == tail) && k0 == lane) {          // a long run starts here: where does it end?
+        int64_t to = c + 1;
+        for (unsigned same = ALL; same == ALL; to += same == ALL ? 32 : __ffs(~same) - 1)
+            same = __ballot_sync(ALL, to + lane < a.chunks && a.keys[(to + lane) * EMB_CHUNK] == tail);
+        if (lane == 0) a.spans[atomicAdd(a.n_spans, 1)] = make_int4(static_cast<int>(c), static_cast<int>(to), tail, 0);
+    }
     constexpr int PAIRS = VEC * ITEMS / 2;
     F2 s[PAIRS];
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
-    for (int i0 = begin; i0 < end; i0 += BATCH) {
-        RowVectors<T, VEC, ITEMS> x[BATCH];
+    auto row_at = [&](int i) {
+        const int64_t r = __shfl_sync(ALL, i < 32 ? row : row2, i & 31);
+        return reinterpret_cast<const V*>(a.dy + r * a.ldd) + k0;
+    };
+    auto add = [&](const RowVectors<T, VEC, ITEMS>& x, int i) {
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            const int64_t r = __shfl_sync(ALL, i0 + b < 32 ? row : row2, (i0 + b) & 31);
+        for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], x.pair(p));
+        if (i < 32 ? !(last >> i & 1) : i + 1 < end) return;
+        const int32_t v = i < 32 ? __shfl_sync(ALL, key, i) : tail;
+        const bool is_head = v == head && head_long, is_tail = v == tail && tail_long;
+        if (a.named && k0 == 0) a.named[v] = 1;
+        if (!is_head && !is_tail)
+            emb_store<W, VEC, ITEMS>(s, static_cast<W*>(a.dw) + v * a.lddw, k0, n, a.scale, a.add);
+        else
+            emb_store<float, VEC, ITEMS>(s, a.parts + (c * 2 + (is_head ? 0 : 1)) * a.H, k0, n, 1.f, false);
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                x[b].v[i] = V{};
-                if (i0 + b < end && k0 + 32 * i < n) x[b].v[i] = reinterpret_cast<const V*>(a.dy + r * a.ldd)[k0 + 32 * i];
+        for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
+    };
+    if constexpr (sizeof(V) >= 4) {
+        V* ring = reinterpret_cast<V*>(dyn) + threadIdx.x;  // [EMB_AHEAD][ITEMS][threads], each thread its own vectors
+        auto copy = [&](int i) {
+            if (i < end) {
+                const V* from = row_at(i);
+#pragma unroll
+                for (int k = 0; k < ITEMS; ++k)
+                    if (k0 + 32 * k < n) copy_async<sizeof(V)>(ring + ((i & (EMB_AHEAD - 1)) * ITEMS + k) * 256, from + 32 * k);
             }
+            copy_async_commit();
+        };
+        for (int i = begin; i < begin + EMB_AHEAD - 1; ++i) copy(i);
+        for (int i = begin; i < end; ++i) {
+            copy(i + EMB_AHEAD - 1);
+            copy_async_wait<EMB_AHEAD - 1>();
+            RowVectors<T, VEC, ITEMS> x;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) x.v[k] = k0 + 32 * k < n ? ring[((i & (EMB_AHEAD - 1)) * ITEMS + k) * 256] : V{};
+            add(x, i);
         }
+    } else {  // single 16-bit elements: a few rows in registers
+        constexpr int BATCH = 4;
+        for (int i0 = begin; i0 < end; i0 += BATCH) {
+            RowVectors<T, VEC, ITEMS> x[BATCH];
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            if (i0 + b >= end) break;
+            for (int b = 0; b < BATCH; ++b) {
+                const V* from = row_at(i0 + b);
 #pragma unroll
-            for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], x[b].pair(p));
-            const int at_end = i0 + b;
-            if (at_end < 32 ? !(last >> at_end & 1) : at_end + 1 < end) continue;
-            const int64_t v = at_end < 32 ? __shfl_sync(ALL, key, at_end) : tail;
-            const bool is_head = v == head && head_long, is_tail = v == tail && tail_long;
-            if (!is_head && !is_tail) {
-                emb_store<W, VEC, ITEMS>(s, static_cast<W*>(a.dw) + v * a.lddw, k0, n, a.scale, a.add);
-            } else {
-                emb_store<float, VEC, ITEMS>(s, a.parts + (c * 2 + (is_head ? 0 : 1)) * a.H, k0, n, 1.f, false);
-                if (!is_head && k0 == 0) a.spans[1 + atomicAdd(a.spans, 1)] = static_cast<int32_t>(c);
+                for (int k = 0; k < ITEMS; ++k) {
+                    x[b].v[k] = V{};
+                    if (i0 + b < end && k0 + 32 * k < n) x[b].v[k] = from[32 * k];
+                }
             }
 #pragma unroll
-            for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
+            for (int b = 0; b < BATCH; ++b)
+                if (i0 + b < end) add(x[b], i0 + b);
         }
     }
 }
 
-// The runs that reach past a chunk: a slab of columns of one per block, its
-// pieces shared out over eight warps and added in a fixed order.
-template <typename W, int VEC, int ITEMS>
-__global__ void __launch_bounds__(256) emb_join(EmbBwd<float> a) {
+// What is left after the sums.  The first `joining` blocks: the runs that reach
+// past a chunk, a slab of columns of one per block, its pieces shared out over
+// eight warps and added in a fixed order.  The others: the vocabulary rows that
+// no token names are cleared, while those wait for their pieces.
+template <typename W, int VEC, int ITEMS, int CLEAR_VEC>
+__global__ void __launch_bounds__(256) emb_finish(EmbBwd<float> a) {
     constexpr int PAIRS = VEC * ITEMS / 2;
     __shared__ F2 s[8][PAIRS][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = a.H / VEC;
     wait_for_primary();
-    const int64_t items = static_cast<int64_t>(*a.spans) * a.slabs;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t c0 = a.spans[1 + item / a.slabs];
+    if (static_cast<int>(blockIdx.x) >= a.joining) {
+        const int64_t v0 = ((static_cast<int64_t>(blockIdx.x) - a.joining) * 8 + warp) * EMB_ZERO_ROWS;
+        const unsigned named = __ballot_sync(0xFFFFFFFFu, lane >= EMB_ZERO_ROWS || v0 + lane >= a.V || a.named[v0 + lane]);
+        for (int j = 0; j < EMB_ZERO_ROWS; ++j) {
+            if (named >> j & 1) continue;
+            using Z = Vec<W, CLEAR_VEC>;
+            Z* out = reinterpret_cast<Z*>(static_cast<W*>(a.dw) + (v0 + j) * a.lddw);
+#pragma unroll 4
+            for (int k = lane; k < a.H / CLEAR_VEC; k += 32) out[k] = Z{};
+        }
+        return;
+    }
+    const int n = a.H / VEC;
+    const int64_t items = static_cast<int64_t>(*a.n_spans) * a.slabs;
+    for (int64_t item = blockIdx.x; item < items; item += a.joining) {
+        const int4 span = a.spans[item / a.slabs];
         const int k0 = static_cast<int>(item % a.slabs) * 32 * ITEMS + lane;
-        const int32_t v = a.keys[c0 * EMB_CHUNK + EMB_CHUNK - 1];
-        int64_t end = c0 + 1;  // the first chunk that does not start with v
-        for (unsigned same = 0xFFFFFFFFu; same == 0xFFFFFFFFu; end += same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1)
-            same = __ballot_sync(0xFFFFFFFFu, end + lane < a.chunks && a.keys[(end + lane) * EMB_CHUNK] == v);
+        const int64_t c0 = span.x, end = span.y, v = span.z;
         F2 sum[PAIRS];
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) sum[p] = f2(0.f);
@@ -336,7 +401,8 @@ size_t emb_space(int64_t N, int64_t V, int64_t H, EmbSpace* e, void* ws) {
     f.hdr = static_cast<WsHeader*>(ws);
     f.bad = reinterpret_cast<int32_t*>(take(blocks * 4));
     f.hist = reinterpret_cast<int32_t*>(take(blocks * 4 << d.bits));
-    f.spans = reinterpret_cast<int32_t*>(take(static_cast<size_t>(chunks + 1) * 4));
+    f.n_spans = reinterpret_cast<int32_t*>(take(4));
+    f.spans = reinterpret_cast<int4*>(take(static_cast<size_t>(chunks) * 16));
     f.named = take(static_cast<size_t>(V));
     for (int k = 0; k < 2; ++k) {
         f.keys[k] = reinterpret_cast<int32_t*>(take(items));
@@ -346,9 +412,14 @@ size_t emb_space(int64_t N, int64_t V, int64_t H, EmbSpace* e, void* ws) {
     return at;
 }
 
-// The sorted tokens: their place in e->keys and e->rows.
-lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int64_t padding, bool clear, const EmbSpace& e,
-                      int* where, cudaStream_t s) {
+// Rows that no token names are cleared while the tokens are sorted, all rows at
+// once (clear.at), where the tokens are so few that they name few of them; else
+// by the sums, which look at what is named.
+constexpr int64_t EMB_CLEAR_RATIO = 4;  // vocabulary rows to a token
+
+// The sorted tokens: their place in e.keys and e.rows.
+lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int64_t padding, bool name, Clear clear,
+                      const EmbSpace& e, int* where, cudaStream_t s) {
     const Digits d = digits_of(V);
     SortShape shape{};
     shape.n = N;
@@ -357,13 +428,17 @@ lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int6
     shape.per = (N + shape.blocks - 1) / shape.blocks;
     shape.hist = e.hist;
     shape.bad = e.bad;
+    if (clear.at) shape.extra = shape.blocks < SORT_BLOCKS / 2 ? static_cast<int32_t>(SORT_BLOCKS) - shape.blocks : SORT_BLOCKS / 2;
+    const int kernels = shape.blocks > 1 ? 2 : 1;  // of a pass
+    clear.of = kernels * d.passes;
     const FirstDigit first{tokens, idx64, static_cast<int32_t>(V), shape.bins - 1, padding, e.keys[0], e.rows[0], &e.hdr->status,
-                           e.spans, clear ? e.named : nullptr};
+                           e.n_spans, name ? e.named : nullptr, shape.blocks, clear};
     lce_status_t st = sort_by(first, shape, true, s);
     shape.bad = nullptr;
     for (int p = 1; p < d.passes && st == LCE_OK; ++p) {
         const int from = (p - 1) & 1, to = p & 1;
-        st = sort_by(NextDigit{e.keys[from], e.rows[from], p * d.bits, shape.bins - 1, e.keys[to], e.rows[to]}, shape, false, s);
+        clear.part = p * kernels;
+        st = sort_by(NextDigit{e.keys[from], e.rows[from], p * d.bits, shape.bins - 1, e.keys[to], e.rows[to], clear}, shape, false, s);
     }
     *where = (d.passes - 1) & 1;
     return st;
@@ -394,18 +469,24 @@ lce_status_t emb_lookup(const EmbFwd<T>& a, cudaStream_t s) {
 
 template <typename T, typename W, int VEC>
 lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
-    constexpr int ITEMS = VEC >= 8 ? 1 : 8 / VEC, BATCH = VEC * sizeof(T) == 16 ? (ITEMS == 1 ? 8 : 4) : 4;
+    constexpr int ITEMS = VEC >= 8 ? 1 : 8 / VEC;
     const int64_t n = a.H / VEC;
     a.slabs = static_cast<int32_t>((n + 32 * ITEMS - 1) / (32 * ITEMS));
-    const int64_t warps = a.chunks * a.slabs + (a.add ? 0 : (a.V + EMB_ZERO_ROWS - 1) / EMB_ZERO_ROWS), blocks = (warps + 7) / 8;
-    if (blocks == 0) return LCE_OK;
+    const int64_t blocks = (a.chunks * a.slabs + 7) / 8;
+    if (blocks == 0) return LCE_OK;  // no tokens: all rows have been cleared
     if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
-    LCE_PROFILED(launch_after(emb_sum<T, W, VEC, ITEMS, BATCH>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a));
-    if (a.chunks < 2) return LCE_OK;
+    constexpr size_t smem = VEC * sizeof(T) >= 4 ? EMB_AHEAD * ITEMS * 256 * VEC * sizeof(T) : 0;
+    static std::atomic<uint64_t> sums{0}, finishes{0};
+    // 16-byte vectors of FP32 pieces where dw's rows have vectors at all, and few columns to a block: there are few long runs
+    constexpr int JVEC = VEC % 4 == 0 ? 4 : VEC, JITEMS = JVEC == 4 ? 1 : 4 / JVEC;
+    auto finish = emb_finish<W, JVEC, JITEMS, VEC>;
+    if (!allow_smem(&sums, emb_sum<T, W, VEC, ITEMS>, static_cast<int>(smem)) || !allow_smem(&finishes, finish, 0)) return LCE_ERR_CUDA;
+    LCE_PROFILED(launch_after(emb_sum<T, W, VEC, ITEMS>, dim3(static_cast<unsigned>(blocks)), 256, smem, s, a));
     EmbBwd<float> j{};
     j.V = a.V;
     j.scale = a.scale;
-    j.keys = a.keys;
+    j.named = a.named;
+    j.n_spans = a.n_spans;
     j.spans = a.spans;
     j.parts = a.parts;
     j.dw = a.dw;
@@ -413,11 +494,11 @@ lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
     j.chunks = a.chunks;
     j.add = a.add;
     j.H = a.H;
-    // 16-byte vectors of FP32 where dw's rows have vectors at all, and few columns to a block: there are few long runs
-    constexpr int JVEC = VEC % 4 == 0 ? 4 : VEC, JITEMS = JVEC == 4 ? 1 : 4 / JVEC;
     j.slabs = static_cast<int32_t>((a.H / JVEC + 32 * JITEMS - 1) / (32 * JITEMS));
-    const int64_t most = (a.chunks - 1) * j.slabs;
-    LCE_PROFILED(launch_after(emb_join<W, JVEC, JITEMS>, dim3(static_cast<unsigned>(most < 1216 ? most : 1216)), 256, 0, s, j));
+    const int64_t most = (a.chunks - 1) * j.slabs, clearing = a.named ? (a.V + 8 * EMB_ZERO_ROWS - 1) / (8 * EMB_ZERO_ROWS) : 0;
+    j.joining = static_cast<int32_t>(most < 1216 ? most : 1216);
+    if (j.joining + clearing == 0) return LCE_OK;
+    LCE_PROFILED(launch_after(finish, dim3(static_cast<unsigned>(j.joining + clearing)), 256, 0, s, j));
     return LCE_OK;
 }
 
@@ -483,12 +564,16 @@ lce_status_t lce_embedding_backward(int64_t N, int64_t V, int64_t H, int dtype, 
     if (ws_bytes < emb_space(N, V, H, &e, ws)) return LCE_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int where = 0;
-    const lce_status_t sorted = emb_sort(N, V, tokens, index_bytes == 8, padding_token, !add, e, &where, s);
+    const int64_t size = static_cast<int64_t>(dtype_bytes(gtype));
+    const bool early = !add && N <= V / EMB_CLEAR_RATIO;
+    const Clear clear{early ? static_cast<uint8_t*>(grad_weight) : nullptr, V, H * size, ldgw * size, 0, 1};
+    const lce_status_t sorted = emb_sort(N, V, tokens, index_bytes == 8, padding_token, !add && !early, clear, e, &where, s);
     if (sorted != LCE_OK) return sorted;
     return with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);
-        const EmbBwd<T> a{static_cast<const T*>(grad_y), ldg, N, V, scale, e.keys[where], e.rows[where], e.named, e.spans,
-                          e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, static_cast<int32_t>(H), 0};
+        const EmbBwd<T> a{static_cast<const T*>(grad_y), ldg, N, V, scale, e.keys[where], e.rows[where],
+                          add || early ? nullptr : e.named, e.n_spans, e.spans,
+                          e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, static_cast<int32_t>(H), 0, 0};
         return gtype == LCE_F32 ? emb_gradient<T, float>(a, s) : emb_gradient<T, T>(a, s);
     });
 }

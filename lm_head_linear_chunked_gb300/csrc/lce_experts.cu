@@ -19,7 +19,7 @@ namespace {
 struct PlanArgs {
     static constexpr bool SEGMENTS = true;
     struct Item {
-        int32_t digit, slot;
+        int32_t digit, slot;  // the expert, and the slot's number
     };
     const void* experts;
     bool idx64;
@@ -30,6 +30,7 @@ struct PlanArgs {
     int32_t R;
     unsigned* stat;
     __device__ __forceinline__ void begin() const {}
+    __device__ __forceinline__ void beside(int, int64_t, int64_t) const {}
     __device__ __forceinline__ Item load(int64_t i, bool* bad) const {
         const int32_t slot = static_cast<int32_t>(i);
         const int64_t e = idx64 ? static_cast<const int64_t*>(experts)[i] : static_cast<const int32_t*>(experts)[i];

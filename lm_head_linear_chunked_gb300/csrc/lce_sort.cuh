@@ -13,6 +13,11 @@
 //     then also segment(d, count, start), called by one thread per digit, and
 //     ends(end), one past the last segment, called by all threads of all blocks
 //   void status(int any)   with shape.bad: whether an item was bad, once
+//   void beside(int kernel, int64_t block, int64_t of)   called by all threads
+//     of the shape's `extra` blocks of each kernel (the first is 0): work that
+//     needs nothing sorted, for the SMs that so few items leave idle.  The next
+//     kernel is launched when they have ended: earlier, its blocks would crowd
+//     onto the first SMs that are free
 #pragma once
 
 #include <atomic>
@@ -32,7 +37,7 @@ constexpr int64_t SORT_BLOCKS = 152;
 
 struct SortShape {
     int64_t n, per;  // items, and items of a block
-    int32_t bins, blocks;
+    int32_t bins, blocks, extra;
     int32_t* hist;   // [blocks, bins]
     int32_t* bad;    // [blocks]: a block has seen an item out of range
 };
@@ -75,6 +80,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count(SortJob<F> job) {
     const F& f = job.f;
     const SortShape& s = job.shape;
     extern __shared__ __align__(16) int32_t counts[];
+    if (static_cast<int>(blockIdx.x) >= s.blocks) return f.beside(0, blockIdx.x - s.blocks, s.extra);
     launch_dependents();
     for (int d = threadIdx.x; d < s.bins; d += SORT_THREADS) counts[d] = 0;
     wait_for_primary();
@@ -96,6 +102,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     const SortShape& s = job.shape;
     extern __shared__ __align__(16) int32_t counts[];  // [SORT_WARPS, bins]: of each warp's items, then their places
     __shared__ int32_t sums[SORT_WARPS];
+    if (static_cast<int>(blockIdx.x) >= s.blocks) return f.beside(s.blocks > 1, blockIdx.x - s.blocks, s.extra);
     launch_dependents();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     for (int d = t; d < SORT_WARPS * s.bins / 4; d += SORT_THREADS) reinterpret_cast<int4*>(counts)[d] = make_int4(0, 0, 0, 0);
@@ -158,12 +165,13 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     for (int j = 0; j < MOST; ++j) {
         const int d = t * each + j;
         if (j >= each || d >= s.bins) break;
-        int32_t at = start + before[j];
+        int32_t at = start + before[j], c[SORT_WARPS];
+#pragma unroll
+        for (int w = 0; w < SORT_WARPS; ++w) c[w] = counts[w * s.bins + d];
 #pragma unroll
         for (int w = 0; w < SORT_WARPS; ++w) {
-            const int32_t c = counts[w * s.bins + d];
             counts[w * s.bins + d] = at;
-            at += c;
+            at += c[w];
         }
         if constexpr (F::SEGMENTS) {
             if (d % s.blocks == static_cast<int>(blockIdx.x)) f.segment(d, total[j], start);
@@ -176,7 +184,13 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     sort_items(f, w0 + lane, w1, 32, &bad, [&](const typename F::Item& x, bool in) {
         const unsigned active = __ballot_sync(0xFFFFFFFFu, in);
         if (in) {
-            const unsigned same = __match_any_sync(active, x.digit);
+            unsigned same = active;  // the lanes with this digit, bit by bit: a match instruction took longer
+#pragma unroll
+            for (int b = 0; b < 11; ++b) {
+                if (s.bins - 1 >> b == 0) break;
+                const unsigned ones = __ballot_sync(active, x.digit >> b & 1);
+                same &= x.digit >> b & 1 ? ones : ~ones;
+            }
             const int32_t at = own[x.digit] + __popc(same & ((1u << lane) - 1));
             __syncwarp(active);
             if ((same >> lane) == 1u) own[x.digit] = at + 1;  // the last of them
@@ -191,14 +205,18 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     }
 }
 
-// Lets a kernel take `bytes` of dynamic shared memory; asked once per device.
+// Lets a kernel take `bytes` of dynamic shared memory, out of the largest share
+// of an SM's: kernels that overlap with the one before them need the same
+// division into L1 and shared memory.  Asked once per device.
 template <typename K>
 bool allow_smem(std::atomic<uint64_t>* known, K kernel, int bytes) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (bit && (known->load(std::memory_order_relaxed) & bit)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+        return false;
     known->fetch_or(bit, std::memory_order_relaxed);
     return true;
 }
@@ -207,18 +225,20 @@ bool allow_smem(std::atomic<uint64_t>* known, K kernel, int bytes) {
 // else under the kernel before it, whose results it waits for.
 template <typename F>
 lce_status_t sort_by(const F& f, const SortShape& shape, bool first, cudaStream_t s) {
-    static std::atomic<uint64_t> known{0};
-    if (!allow_smem(&known, sort_place<F>, static_cast<int>(sort_smem(SORT_BINS_MAX)))) return LCE_ERR_CUDA;
+    static std::atomic<uint64_t> counts{0}, places{0};
+    if (!allow_smem(&counts, sort_count<F>, SORT_BINS_MAX * 4) ||
+        !allow_smem(&places, sort_place<F>, static_cast<int>(sort_smem(SORT_BINS_MAX))))
+        return LCE_ERR_CUDA;
     const SortJob<F> job{f, shape};
-    const unsigned blocks = static_cast<unsigned>(shape.blocks);
-    if (blocks > 1) {
+    const unsigned blocks = static_cast<unsigned>(shape.blocks + shape.extra);
+    if (shape.blocks > 1) {
         if (first)
             LCE_PROFILED(sort_count<F><<<blocks, SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s>>>(job));
         else
             LCE_PROFILED(launch_after(sort_count<F>, dim3(blocks), SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s, job));
     }
-    if (blocks == 1 && first)
-        LCE_PROFILED(sort_place<F><<<1, SORT_THREADS, sort_smem(shape.bins), s>>>(job));
+    if (shape.blocks == 1 && first)
+        LCE_PROFILED(sort_place<F><<<blocks, SORT_THREADS, sort_smem(shape.bins), s>>>(job));
     else
         LCE_PROFILED(launch_after(sort_place<F>, dim3(blocks), SORT_THREADS, sort_smem(shape.bins), s, job));
     return LCE_OK;
