@@ -162,7 +162,6 @@ struct NextDigit {
 };
 
 constexpr int EMB_CHUNK = 32;       // sorted tokens of a warp
-constexpr int EMB_AHEAD = 8;         // rows of it on their way
 constexpr int EMB_ZERO_ROWS = 8;    // vocabulary rows of a warp that looks for rows to clear
 
 template <typename T>
@@ -207,7 +206,7 @@ __device__ __forceinline__ void emb_store(const F2 (&s)[VEC * ITEMS / 2], W* row
 // and their pieces go to `parts`: [chunk][0] of a run that comes from the chunk
 // before, [chunk][1] of one that starts here; so a token that fills half of the
 // batch is spread over as many warps as its rows need.
-template <typename T, typename W, int VEC, int ITEMS>
+template <typename T, typename W, int VEC, int ITEMS, int AHEAD>
 __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
     extern __shared__ __align__(16) uint8_t dyn[];
     using V = Vec<T, VEC>;
@@ -250,14 +249,13 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
     F2 s[PAIRS];
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
+    const V* from = reinterpret_cast<const V*>(a.dy + row * a.ldd) + k0;  // shifted back by the lane that holds the row
+    const V* from2 = reinterpret_cast<const V*>(a.dy + row2 * a.ldd) + k0;
     auto row_at = [&](int i) {
-        const int64_t r = __shfl_sync(ALL, i < 32 ? row : row2, i & 31);
-        return reinterpret_cast<const V*>(a.dy + r * a.ldd) + k0;
+        const auto p = reinterpret_cast<unsigned long long>(i < 32 ? from : from2);
+        return reinterpret_cast<const V*>(__shfl_sync(ALL, p, i & 31)) + (lane - (i & 31));
     };
-    auto add = [&](const RowVectors<T, VEC, ITEMS>& x, int i) {
-#pragma unroll
-        for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], x.pair(p));
-        if (i < 32 ? !(last >> i & 1) : i + 1 < end) return;
+    auto finish = [&](int i) {  // of a run, or of its part in this chunk: i is its last row
         const int32_t v = i < 32 ? __shfl_sync(ALL, key, i) : tail;
         const bool is_head = v == head && head_long, is_tail = v == tail && tail_long;
         if (a.named && k0 == 0) a.named[v] = 1;
@@ -268,42 +266,58 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
     };
-    if constexpr (sizeof(V) >= 4) {
-        V* ring = reinterpret_cast<V*>(dyn) + threadIdx.x;  // [EMB_AHEAD][ITEMS][threads], each thread its own vectors
-        auto copy = [&](int i) {
+    if constexpr (AHEAD > 0) {
+        // rows on their way: [AHEAD][ITEMS][threads], each thread its own vectors
+        constexpr int SLOT = ITEMS * 256;
+        V* ring = reinterpret_cast<V*>(dyn) + threadIdx.x;
+        auto copy = [&](int i, int slot) {
             if (i < end) {
-                const V* from = row_at(i);
+                const V* p = row_at(i);
 #pragma unroll
                 for (int k = 0; k < ITEMS; ++k)
-                    if (k0 + 32 * k < n) copy_async<sizeof(V)>(ring + ((i & (EMB_AHEAD - 1)) * ITEMS + k) * 256, from + 32 * k);
+                    if (k0 + 32 * k < n) copy_async<sizeof(V)>(ring + slot + k * 256, p + 32 * k);
             }
             copy_async_commit();
         };
-        for (int i = begin; i < begin + EMB_AHEAD - 1; ++i) copy(i);
-        for (int i = begin; i < end; ++i) {
-            copy(i + EMB_AHEAD - 1);
-            copy_async_wait<EMB_AHEAD - 1>();
-            RowVectors<T, VEC, ITEMS> x;
 #pragma unroll
-            for (int k = 0; k < ITEMS; ++k) x.v[k] = k0 + 32 * k < n ? ring[((i & (EMB_AHEAD - 1)) * ITEMS + k) * 256] : V{};
-            add(x, i);
+        for (int k = 0; k < AHEAD - 1; ++k) copy(begin + k, k * SLOT);
+        int slot = 0;
+        for (int i = begin; i < end;) {
+            const unsigned ends = i < 32 ? last >> i : 0u;
+            const int stop = ends ? i + __ffs(ends) : end;
+            for (; i < stop; ++i) {
+                copy(i + AHEAD - 1, (slot + (AHEAD - 1) * SLOT) & (AHEAD * SLOT - 1));
+                copy_async_wait<AHEAD - 1>();
+                RowVectors<T, VEC, ITEMS> x;
+#pragma unroll
+                for (int k = 0; k < ITEMS; ++k) x.v[k] = ring[slot + k * 256];
+                slot = (slot + SLOT) & (AHEAD * SLOT - 1);
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], x.pair(p));
+            }
+            finish(i - 1);
         }
-    } else {  // single 16-bit elements: a few rows in registers
+    } else {  // a few rows in registers
         constexpr int BATCH = 4;
         for (int i0 = begin; i0 < end; i0 += BATCH) {
             RowVectors<T, VEC, ITEMS> x[BATCH];
 #pragma unroll
             for (int b = 0; b < BATCH; ++b) {
-                const V* from = row_at(i0 + b);
+                const V* p = row_at(i0 + b);
 #pragma unroll
                 for (int k = 0; k < ITEMS; ++k) {
                     x[b].v[k] = V{};
-                    if (i0 + b < end && k0 + 32 * k < n) x[b].v[k] = from[32 * k];
+                    if (i0 + b < end && k0 + 32 * k < n) x[b].v[k] = p[32 * k];
                 }
             }
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b)
-                if (i0 + b < end) add(x[b], i0 + b);
+            for (int b = 0; b < BATCH; ++b) {
+                const int i = i0 + b;
+                if (i >= end) break;
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], x[b].pair(p));
+                if (i < 32 ? last >> i & 1 : i + 1 == end) finish(i);
+            }
         }
     }
 }
@@ -412,10 +426,13 @@ size_t emb_space(int64_t N, int64_t V, int64_t H, EmbSpace* e, void* ws) {
     return at;
 }
 
-// Rows that no token names are cleared while the tokens are sorted, all rows at
-// once (clear.at), where the tokens are so few that they name few of them; else
-// by the sums, which look at what is named.
+// Whether all of the gradient's rows are cleared while the tokens are sorted, on
+// the SMs that the sort leaves idle: where the tokens are so few that they name
+// few rows (16384 tokens, 151936 rows of 1024: 86 us against 92).  Else the
+// rows that no token names are cleared at the end.  (131072 tokens, rows of
+// 4096: clearing a part of them early, 64 MB, gained 1%, 256 MB lost 2%.)
 constexpr int64_t EMB_CLEAR_RATIO = 4;  // vocabulary rows to a token
+bool emb_early(int64_t N, int64_t V) { return sort_blocks(N) <= SORT_BLOCKS / 2 && N <= V / EMB_CLEAR_RATIO; }
 
 // The sorted tokens: their place in e.keys and e.rows.
 lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int64_t padding, bool name, Clear clear,
@@ -428,7 +445,7 @@ lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int6
     shape.per = (N + shape.blocks - 1) / shape.blocks;
     shape.hist = e.hist;
     shape.bad = e.bad;
-    if (clear.at) shape.extra = shape.blocks < SORT_BLOCKS / 2 ? static_cast<int32_t>(SORT_BLOCKS) - shape.blocks : SORT_BLOCKS / 2;
+    if (clear.rows) shape.extra = static_cast<int32_t>(SORT_BLOCKS) - shape.blocks;
     const int kernels = shape.blocks > 1 ? 2 : 1;  // of a pass
     clear.of = kernels * d.passes;
     const FirstDigit first{tokens, idx64, static_cast<int32_t>(V), shape.bins - 1, padding, e.keys[0], e.rows[0], &e.hdr->status,
@@ -467,21 +484,22 @@ lce_status_t emb_lookup(const EmbFwd<T>& a, cudaStream_t s) {
     return LCE_OK;
 }
 
+int32_t emb_slabs(int64_t vectors, int items) { return static_cast<int32_t>((vectors + 32 * items - 1) / (32 * items)); }
+
 template <typename T, typename W, int VEC>
 lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
-    constexpr int ITEMS = VEC >= 8 ? 1 : 8 / VEC;
-    const int64_t n = a.H / VEC;
-    a.slabs = static_cast<int32_t>((n + 32 * ITEMS - 1) / (32 * ITEMS));
+    constexpr int ITEMS = 8 / VEC, AHEAD = VEC * sizeof(T) >= 4 ? 8 : 0;
+    a.slabs = emb_slabs(a.H / VEC, ITEMS);
     const int64_t blocks = (a.chunks * a.slabs + 7) / 8;
     if (blocks == 0) return LCE_OK;  // no tokens: all rows have been cleared
     if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
-    constexpr size_t smem = VEC * sizeof(T) >= 4 ? EMB_AHEAD * ITEMS * 256 * VEC * sizeof(T) : 0;
+    constexpr size_t smem = static_cast<size_t>(AHEAD) * ITEMS * 256 * VEC * sizeof(T);
     static std::atomic<uint64_t> sums{0}, finishes{0};
     // 16-byte vectors of FP32 pieces where dw's rows have vectors at all, and few columns to a block: there are few long runs
     constexpr int JVEC = VEC % 4 == 0 ? 4 : VEC, JITEMS = JVEC == 4 ? 1 : 4 / JVEC;
     auto finish = emb_finish<W, JVEC, JITEMS, VEC>;
-    if (!allow_smem(&sums, emb_sum<T, W, VEC, ITEMS>, static_cast<int>(smem)) || !allow_smem(&finishes, finish, 0)) return LCE_ERR_CUDA;
-    LCE_PROFILED(launch_after(emb_sum<T, W, VEC, ITEMS>, dim3(static_cast<unsigned>(blocks)), 256, smem, s, a));
+    if (!allow_smem(&sums, emb_sum<T, W, VEC, ITEMS, AHEAD>, static_cast<int>(smem)) || !allow_smem(&finishes, finish, 0)) return LCE_ERR_CUDA;
+    LCE_PROFILED(launch_after(emb_sum<T, W, VEC, ITEMS, AHEAD>, dim3(static_cast<unsigned>(blocks)), 256, smem, s, a));
     EmbBwd<float> j{};
     j.V = a.V;
     j.scale = a.scale;
@@ -494,7 +512,7 @@ lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
     j.chunks = a.chunks;
     j.add = a.add;
     j.H = a.H;
-    j.slabs = static_cast<int32_t>((a.H / JVEC + 32 * JITEMS - 1) / (32 * JITEMS));
+    j.slabs = emb_slabs(a.H / JVEC, JITEMS);
     const int64_t most = (a.chunks - 1) * j.slabs, clearing = a.named ? (a.V + 8 * EMB_ZERO_ROWS - 1) / (8 * EMB_ZERO_ROWS) : 0;
     j.joining = static_cast<int32_t>(most < 1216 ? most : 1216);
     if (j.joining + clearing == 0) return LCE_OK;
@@ -565,14 +583,14 @@ lce_status_t lce_embedding_backward(int64_t N, int64_t V, int64_t H, int dtype, 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int where = 0;
     const int64_t size = static_cast<int64_t>(dtype_bytes(gtype));
-    const bool early = !add && N <= V / EMB_CLEAR_RATIO;
-    const Clear clear{early ? static_cast<uint8_t*>(grad_weight) : nullptr, V, H * size, ldgw * size, 0, 1};
-    const lce_status_t sorted = emb_sort(N, V, tokens, index_bytes == 8, padding_token, !add && !early, clear, e, &where, s);
+    const bool early = !add && emb_early(N, V), late = !add && !early;
+    const Clear clear{static_cast<uint8_t*>(grad_weight), early ? V : 0, H * size, ldgw * size, 0, 1};
+    const lce_status_t sorted = emb_sort(N, V, tokens, index_bytes == 8, padding_token, late, clear, e, &where, s);
     if (sorted != LCE_OK) return sorted;
     return with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);
         const EmbBwd<T> a{static_cast<const T*>(grad_y), ldg, N, V, scale, e.keys[where], e.rows[where],
-                          add || early ? nullptr : e.named, e.n_spans, e.spans,
+                          late ? e.named : nullptr, e.n_spans, e.spans,
                           e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, static_cast<int32_t>(H), 0, 0};
         return gtype == LCE_F32 ? emb_gradient<T, float>(a, s) : emb_gradient<T, T>(a, s);
     });

@@ -68,107 +68,191 @@ struct MoveArgs {
     int64_t ldt, lds, ldto, ldso;
     int64_t T, R;
     int32_t k, H;
+    int32_t share;           // warps to a token (combine's gradients): 1, 2, 4 or 8
 };
 
-__device__ __forceinline__ int64_t row_of(const MoveArgs& a, int64_t slot) {
-    const int64_t p = a.positions[slot];
-    return p < a.R ? p : -1;  // a plan of other rows
+// The rows of up to 32 slots of a token, one to a lane; -1 for none (a position
+// outside the rows, as of a plan made for others, counts as none).
+__device__ __forceinline__ int64_t lane_row(const MoveArgs& a, int64_t t, int j0) {
+    const int j = j0 + (threadIdx.x & 31);
+    const int64_t p = j < a.k ? a.positions[t * a.k + j] : -1;
+    return p < a.R ? p : -1;
 }
-
 template <typename T>
-__device__ __forceinline__ float weight_of(const MoveArgs& a, int64_t slot) {
-    return a.weights ? load_w<T>(a.weights, a.w32, slot) : 1.f;
+__device__ __forceinline__ float lane_weight(const MoveArgs& a, int64_t t, int j0) {
+    const int j = j0 + (threadIdx.x & 31);
+    return a.weights && j < a.k ? load_w<T>(a.weights, a.w32, t * a.k + j) : 1.f;
 }
 
-// Block T + r: row r of the sorted ones is zero where no slot takes it.
+// 32 sorted rows of a warp: those that no slot takes are zero.
 template <typename T, int VEC>
-__device__ __forceinline__ void zero_row(const MoveArgs& a, int64_t r) {
-    if (a.slots[r] >= 0) return;
-    Vec<T, VEC>* out = reinterpret_cast<Vec<T, VEC>*>(static_cast<T*>(a.slot_out) + r * a.ldso);
-    for (int i = threadIdx.x; i < a.H / VEC; i += blockDim.x) out[i] = Vec<T, VEC>{};
+__device__ __forceinline__ void clear_rows(const MoveArgs& a, int64_t r0) {
+    using V = Vec<T, VEC>;
+    const int lane = threadIdx.x & 31;
+    unsigned todo = __ballot_sync(0xFFFFFFFFu, r0 + lane < a.R && a.slots[r0 + lane] < 0);
+    for (; todo; todo &= todo - 1) {
+        V* out = reinterpret_cast<V*>(static_cast<T*>(a.slot_out) + (r0 + __ffs(todo) - 1) * a.ldso);
+#pragma unroll 4
+        for (int i = lane; i < a.H / VEC; i += 32) out[i] = V{};
+    }
 }
 
-// dispatch: a block per token.
-template <typename T, int VEC>
+// dispatch: a warp per token and U vectors of each lane, read once and written
+// to all the token's rows.  The warps behind those clear rows.
+template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) expert_spread(MoveArgs a) {
-    const int64_t t = blockIdx.x;
-    if (t >= a.T) return zero_row<T, VEC>(a, t - a.T);
     using V = Vec<T, VEC>;
+    const int lane = threadIdx.x & 31, n = a.H / VEC, parts = (n + 32 * U - 1) / (32 * U);
+    const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5), tokens = static_cast<uint32_t>(a.T) * parts;
+    if (item >= tokens) return clear_rows<T, VEC>(a, static_cast<int64_t>(item - tokens) * 32);
+    const int64_t t = item / parts;
+    const int k0 = static_cast<int>(item % parts) * 32 * U + lane;
     const V* x = reinterpret_cast<const V*>(static_cast<const T*>(a.token_rows) + t * a.ldt);
-    for (int i = threadIdx.x; i < a.H / VEC; i += blockDim.x) {
-        const V v = x[i];
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t p = row_of(a, t * a.k + j);
-            if (p >= 0) reinterpret_cast<V*>(static_cast<T*>(a.slot_out) + p * a.ldso)[i] = v;
+    V v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (k0 + 32 * u < n) v[u] = x[k0 + 32 * u];
+    for (int j0 = 0; j0 < a.k; j0 += 32) {
+        const int64_t p = lane_row(a, t, j0);
+        for (unsigned todo = __ballot_sync(0xFFFFFFFFu, p >= 0); todo; todo &= todo - 1) {
+            V* out = reinterpret_cast<V*>(static_cast<T*>(a.slot_out) + __shfl_sync(0xFFFFFFFFu, p, __ffs(todo) - 1) * a.ldso);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (k0 + 32 * u < n) out[k0 + 32 * u] = v[u];
         }
     }
 }
 
-// combine, and dispatch's gradient (without weights): a block per token.
-template <typename T, int VEC>
+// combine, and dispatch's gradient (without weights): a warp per token and U
+// vectors of each lane, with the vectors of EXPERT_BATCH slots on their way.
+constexpr int EXPERT_BATCH = 8;
+template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) expert_join(MoveArgs a) {
-    const int64_t t = blockIdx.x;
+    using Row = RowVectors<T, VEC, U>;
     using V = Vec<T, VEC>;
-    V* y = reinterpret_cast<V*>(static_cast<T*>(a.token_out) + t * a.ldto);
-    for (int i = threadIdx.x; i < a.H / VEC; i += blockDim.x) {
-        float s[VEC];
+    const int lane = threadIdx.x & 31, n = a.H / VEC, parts = (n + 32 * U - 1) / (32 * U);
+    const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5);
+    if (item >= static_cast<uint32_t>(a.T) * parts) return;
+    const int64_t t = item / parts;
+    const int k0 = static_cast<int>(item % parts) * 32 * U + lane;
+    F2 s[Row::PAIRS];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s[e] = 0.f;
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t p = row_of(a, t * a.k + j);
-            if (p < 0) continue;
-            const float w = weight_of<T>(a, t * a.k + j);
-            const V v = reinterpret_cast<const V*>(static_cast<const T*>(a.slot_rows) + p * a.lds)[i];
+    for (int p = 0; p < Row::PAIRS; ++p) s[p] = f2(0.f);
+    for (int j0 = 0; j0 < a.k; j0 += 32) {
+        const int64_t row = lane_row(a, t, j0);
+        const float weight = lane_weight<T>(a, t, j0);
+        unsigned todo = __ballot_sync(0xFFFFFFFFu, row >= 0);
+        while (todo) {
+            Row x[EXPERT_BATCH];
+            float w[EXPERT_BATCH];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s[e] = fmaf(w, v.f(e), s[e]);
+            for (int b = 0; b < EXPERT_BATCH; ++b) {
+                const int j = todo ? __ffs(todo) - 1 : 0;
+                const V* from = reinterpret_cast<const V*>(static_cast<const T*>(a.slot_rows) + __shfl_sync(0xFFFFFFFFu, row, j) * a.lds);
+                w[b] = __shfl_sync(0xFFFFFFFFu, weight, j);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    x[b].v[u] = V{};
+                    if (todo && k0 + 32 * u < n) load_now(x[b].v[u], from + k0 + 32 * u);
+                }
+                if (!todo) w[b] = 0.f;
+                todo &= todo - 1;
+            }
+#pragma unroll
+            for (int b = 0; b < EXPERT_BATCH; ++b)
+#pragma unroll
+                for (int p = 0; p < Row::PAIRS; ++p) s[p] = fma2(f2(w[b]), x[b].pair(p), s[p]);
         }
-        V o;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o.set(e, s[e]);
-        y[i] = o;
     }
+    Row o;
+    V* y = reinterpret_cast<V*>(static_cast<T*>(a.token_out) + t * a.ldto);
+#pragma unroll
+    for (int p = 0; p < Row::PAIRS; ++p) o.set(p, s[p]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (k0 + 32 * u < n) y[k0 + 32 * u] = o.v[u];
 }
 
-// combine's gradients: a block per token, a slot after the other.
-template <typename T, int VEC>
+// combine's gradients: `share` warps of a block per token, each every share-th
+// stretch of U vectors of each lane, EXPERT_BATCH slots at a time.  The sums
+// over a row are put together warp by warp.  The warps behind those clear rows.
+template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
-    __shared__ float part[8];
-    const int64_t t = blockIdx.x;
-    if (t >= a.T) return zero_row<T, VEC>(a, t - a.T);
+    using Row = RowVectors<T, VEC, U>;
     using V = Vec<T, VEC>;
+    __shared__ float part[8][EXPERT_BATCH];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.H / VEC, per = 8 / a.share;
+    const int64_t tokens = (a.T + per - 1) / per;
+    if (blockIdx.x >= tokens) return clear_rows<T, VEC>(a, ((blockIdx.x - tokens) * 8 + warp) * 32);
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * per + warp / a.share;
+    const bool here = t < a.T;
+    const int first = warp % a.share * 32 * U + lane, step = a.share * 32 * U;
     const V* dy = reinterpret_cast<const V*>(static_cast<const T*>(a.token_rows) + t * a.ldt);
-    for (int j = 0; j < a.k; ++j) {
-        const int64_t slot = t * a.k + j, p = row_of(a, slot);
-        float s = 0.f;
-        if (p >= 0) {
-            const float w = weight_of<T>(a, slot);
-            const V* y = reinterpret_cast<const V*>(static_cast<const T*>(a.slot_rows) + p * a.lds);
-            V* out = a.slot_out ? reinterpret_cast<V*>(static_cast<T*>(a.slot_out) + p * a.ldso) : nullptr;
-            for (int i = threadIdx.x; i < a.H / VEC; i += blockDim.x) {
-                const V d = dy[i];
-                V o;
-                if (a.weights_out) {
-                    const V v = y[i];
+    for (int j0 = 0; j0 < a.k; j0 += EXPERT_BATCH) {
+        const int64_t row = here ? lane_row(a, t, j0) : -1;
+        const float weight = here ? lane_weight<T>(a, t, j0) : 0.f;
+        const V* from[EXPERT_BATCH];
+        V* to[EXPERT_BATCH];
+        F2 w[EXPERT_BATCH], dot[EXPERT_BATCH];
+        bool any = false;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) s = fmaf(d.f(e), v.f(e), s);
+        for (int b = 0; b < EXPERT_BATCH; ++b) {
+            const int64_t r = __shfl_sync(0xFFFFFFFFu, row, b);
+            from[b] = r >= 0 && a.weights_out ? reinterpret_cast<const V*>(static_cast<const T*>(a.slot_rows) + r * a.lds) : nullptr;
+            to[b] = r >= 0 && a.slot_out ? reinterpret_cast<V*>(static_cast<T*>(a.slot_out) + r * a.ldso) : nullptr;
+            w[b] = f2(__shfl_sync(0xFFFFFFFFu, weight, b));
+            dot[b] = f2(0.f);
+            any |= r >= 0 && j0 + b < a.k;
+            if (j0 + b >= a.k) from[b] = to[b] = nullptr;
+        }
+        if (any)
+            for (int k0 = first; k0 < n; k0 += step) {
+                Row d, y[EXPERT_BATCH];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    d.v[u] = V{};
+                    if (k0 + 32 * u < n) d.v[u] = dy[k0 + 32 * u];
                 }
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) o.set(e, w * d.f(e));
-                if (out) out[i] = o;
+                for (int b = 0; b < EXPERT_BATCH; ++b)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        y[b].v[u] = V{};
+                        if (from[b] && k0 + 32 * u < n) load_now(y[b].v[u], from[b] + k0 + 32 * u);
+                    }
+#pragma unroll
+                for (int b = 0; b < EXPERT_BATCH; ++b) {
+#pragma unroll
+                    for (int p = 0; p < Row::PAIRS; ++p) dot[b] = fma2(d.pair(p), y[b].pair(p), dot[b]);
+                    if (!to[b]) continue;
+                    Row o;
+#pragma unroll
+                    for (int p = 0; p < Row::PAIRS; ++p) o.set(p, mul2(w[b], d.pair(p)));
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (k0 + 32 * u < n) to[b][k0 + 32 * u] = o.v[u];
+                }
             }
-        }
         if (!a.weights_out) continue;
-        s = warp_sum(s);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            s = 0.f;
-            for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += part[w];
+        float mine = 0.f;  // lane b: the batch's slot b
+#pragma unroll
+        for (int b = 0; b < EXPERT_BATCH; ++b) {
+            const float v = warp_sum(lo(dot[b]) + hi(dot[b]));
+            if (lane == b) mine = v;
+        }
+        if (a.share > 1) {
+            __syncthreads();
+            if (lane < EXPERT_BATCH) part[warp][lane] = mine;
+            __syncthreads();
+            if (warp % a.share == 0 && lane < EXPERT_BATCH)
+                for (int s = 1; s < a.share; ++s) mine += part[warp + s][lane];
+        }
+        if (here && warp % a.share == 0 && lane < EXPERT_BATCH && j0 + lane < a.k) {
+            const int64_t slot = t * a.k + j0 + lane;
             if (a.w32)
-                static_cast<float*>(a.weights_out)[slot] = s;
+                static_cast<float*>(a.weights_out)[slot] = mine;
             else
-                static_cast<T*>(a.weights_out)[slot] = from_f32<T>(s);
+                static_cast<T*>(a.weights_out)[slot] = from_f32<T>(mine);
         }
     }
 }
@@ -227,28 +311,40 @@ bool rows_ok(const void* p, int64_t n, int64_t ld, int64_t H, int dtype) {
     return ld >= H && (n == 0 || (p && aligned_to(p, dtype_bytes(dtype))));
 }
 
-// Whether rows can be read and written in vectors of 16 bytes.
-template <typename T>
-bool wide(const MoveArgs& a) {
-    constexpr int V = vec16<T>();
-    return a.H % V == 0 && a.ldt % V == 0 && a.lds % V == 0 && a.ldto % V == 0 && a.ldso % V == 0 && aligned_to(a.token_rows, 16) &&
-           aligned_to(a.slot_rows, 16) && aligned_to(a.token_out, 16) && aligned_to(a.slot_out, 16);
+// Whether rows can be read and written in vectors of `vec` elements, `bytes` bytes.
+bool in_vectors(const MoveArgs& a, int vec, int bytes) {
+    return a.H % vec == 0 && a.ldt % vec == 0 && a.lds % vec == 0 && a.ldto % vec == 0 && a.ldso % vec == 0 &&
+           aligned_to(a.token_rows, bytes) && aligned_to(a.slot_rows, bytes) && aligned_to(a.token_out, bytes) &&
+           aligned_to(a.slot_out, bytes);
 }
 
 enum class Move { SPREAD, JOIN, JOIN_BWD };
 
+// Vectors of a lane: as many as 16 bytes hold of single elements, and with
+// 16-byte vectors `wide` of them where that still gives every SM its warps.
 template <typename T, int VEC>
-lce_status_t move_as(const MoveArgs& a, Move what, cudaStream_t s) {
-    const int64_t blocks = a.T + (what != Move::JOIN && a.slot_out ? a.R : 0);
-    if (blocks == 0) return LCE_OK;
-    if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
-    const unsigned grid = static_cast<unsigned>(blocks);
-    if (what == Move::SPREAD)
-        LCE_PROFILED(expert_spread<T, VEC><<<grid, 256, 0, s>>>(a));
-    else if (what == Move::JOIN)
-        LCE_PROFILED(expert_join<T, VEC><<<grid, 256, 0, s>>>(a));
+lce_status_t move_as(MoveArgs a, Move what, cudaStream_t s) {
+    constexpr int NARROW = VEC == 1 ? 8 : VEC * sizeof(T) < 16 ? 4 : 1, WIDE = VEC * sizeof(T) < 16 ? NARROW : 4;
+    const int64_t n = a.H / VEC, clear = what != Move::JOIN && a.slot_out ? (a.R + 31) / 32 : 0;  // warps
+    auto parts = [&](int u) { return (n + 32 * u - 1) / (32 * u); };
+    const bool wide = what == Move::SPREAD && a.T * parts(WIDE) >= 152 * 32;
+    int64_t warps = a.T * parts(wide ? WIDE : NARROW);
+    if (what == Move::JOIN_BWD) {
+        a.share = 1;
+        while (a.share < 8 && a.share < parts(NARROW) && a.T * a.share < 152 * 32) a.share *= 2;
+        warps = (a.T + 8 / a.share - 1) / (8 / a.share) * 8;
+    }
+    if (warps + clear == 0) return LCE_OK;
+    if (warps + clear > INT32_MAX) return LCE_ERR_UNSUPPORTED;
+    const unsigned grid = static_cast<unsigned>((warps + clear + 7) / 8);
+    if (what == Move::JOIN)
+        LCE_PROFILED(expert_join<T, VEC, NARROW><<<grid, 256, 0, s>>>(a));
+    else if (what == Move::JOIN_BWD)
+        LCE_PROFILED(expert_join_bwd<T, VEC, NARROW><<<grid, 256, 0, s>>>(a));
+    else if (wide)
+        LCE_PROFILED(expert_spread<T, VEC, WIDE><<<grid, 256, 0, s>>>(a));
     else
-        LCE_PROFILED(expert_join_bwd<T, VEC><<<grid, 256, 0, s>>>(a));
+        LCE_PROFILED(expert_spread<T, VEC, NARROW><<<grid, 256, 0, s>>>(a));
     return LCE_OK;
 }
 
@@ -256,7 +352,9 @@ lce_status_t move(const MoveArgs& a, int dtype, Move what, lce_stream_t stream) 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);
-        return wide<T>(a) ? move_as<T, vec16<T>()>(a, what, s) : move_as<T, 1>(a, what, s);
+        constexpr int V = vec16<T>(), V4 = 4 / static_cast<int>(sizeof(T));
+        if (in_vectors(a, V, 16)) return move_as<T, V>(a, what, s);
+        return V4 > 1 && in_vectors(a, V4, 4) ? move_as<T, V4>(a, what, s) : move_as<T, 1>(a, what, s);
     });
 }
 

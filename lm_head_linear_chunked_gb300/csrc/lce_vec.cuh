@@ -150,6 +150,27 @@ struct RowVectors {
     }
 };
 
+// A vector's load that stays where it is written: several of them in a row are
+// all on their way before the first is used, which the compiler otherwise gives
+// up for fewer registers.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_now(Vec<T, VEC>& v, const Vec<T, VEC>* p) {
+    if constexpr (sizeof(v) == 16) {
+        uint32_t u[4];
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "l"(p) : "memory");
+        __builtin_memcpy(&v, u, 16);
+    } else if constexpr (sizeof(v) == 4) {
+        uint32_t u;
+        asm volatile("ld.global.u32 %0, [%1];" : "=r"(u) : "l"(p) : "memory");
+        __builtin_memcpy(&v, &u, 4);
+    } else {
+        static_assert(sizeof(v) == 2);
+        uint16_t u;
+        asm volatile("ld.global.u16 %0, [%1];" : "=h"(u) : "l"(p) : "memory");
+        __builtin_memcpy(&v, &u, 2);
+    }
+}
+
 // Elements of T in a 16-byte vector.
 template <typename T>
 constexpr int vec16() { return 16 / static_cast<int>(sizeof(T)); }
