@@ -124,7 +124,7 @@ def build_torch(force: bool = False, verbose: bool = False) -> str:
         objs = list(ex.map(compiled, TORCH_SRC))
     tmp = TORCH_LIB + f".tmp{os.getpid()}"
     run("_lce_torch.so", [cxx, "-shared", *objs, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
-                          "-ltorch", "-ltorch_python"])
+                          "-ltorch_cuda", "-ltorch", "-ltorch_python"])
     os.replace(tmp, TORCH_LIB)
     with open(tag, "w") as f:
         f.write(made_for)

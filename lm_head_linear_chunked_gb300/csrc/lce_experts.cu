@@ -69,6 +69,7 @@ struct MoveArgs {
     int64_t T, R;
     int32_t k, H;
     int32_t share;           // warps to a token (combine's gradients): 1, 2, 4 or 8
+    int32_t clearing;        // blocks that clear rows
 };
 
 // The rows of up to 32 slots of a token, one to a lane; -1 for none (a position
@@ -84,12 +85,13 @@ __device__ __forceinline__ float lane_weight(const MoveArgs& a, int64_t t, int j
     return a.weights && j < a.k ? load_w<T>(a.weights, a.w32, t * a.k + j) : 1.f;
 }
 
-// 32 sorted rows of a warp: those that no slot takes are zero.
+// EXPERT_CLEAR sorted rows of a warp: those that no slot takes are zero.
+constexpr int EXPERT_CLEAR = 8;
 template <typename T, int VEC>
 __device__ __forceinline__ void clear_rows(const MoveArgs& a, int64_t r0) {
     using V = Vec<T, VEC>;
     const int lane = threadIdx.x & 31;
-    unsigned todo = __ballot_sync(0xFFFFFFFFu, r0 + lane < a.R && a.slots[r0 + lane] < 0);
+    unsigned todo = __ballot_sync(0xFFFFFFFFu, lane < EXPERT_CLEAR && r0 + lane < a.R && a.slots[r0 + lane] < 0);
     for (; todo; todo &= todo - 1) {
         V* out = reinterpret_cast<V*>(static_cast<T*>(a.slot_out) + (r0 + __ffs(todo) - 1) * a.ldso);
 #pragma unroll 4
@@ -98,13 +100,14 @@ __device__ __forceinline__ void clear_rows(const MoveArgs& a, int64_t r0) {
 }
 
 // dispatch: a warp per token and U vectors of each lane, read once and written
-// to all the token's rows.  The warps behind those clear rows.
+// to all the token's rows.  The first blocks clear rows.
 template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) expert_spread(MoveArgs a) {
     using V = Vec<T, VEC>;
     const int lane = threadIdx.x & 31, n = a.H / VEC, parts = (n + 32 * U - 1) / (32 * U);
-    const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5), tokens = static_cast<uint32_t>(a.T) * parts;
-    if (item >= tokens) return clear_rows<T, VEC>(a, static_cast<int64_t>(item - tokens) * 32);
+    if (static_cast<int>(blockIdx.x) < a.clearing) return clear_rows<T, VEC>(a, (blockIdx.x * 8ll + (threadIdx.x >> 5)) * EXPERT_CLEAR);
+    const uint32_t item = (blockIdx.x - a.clearing) * 8u + (threadIdx.x >> 5);
+    if (item >= static_cast<uint32_t>(a.T) * parts) return;
     const int64_t t = item / parts;
     const int k0 = static_cast<int>(item % parts) * 32 * U + lane;
     const V* x = reinterpret_cast<const V*>(static_cast<const T*>(a.token_rows) + t * a.ldt);
@@ -124,9 +127,8 @@ __global__ void __launch_bounds__(256) expert_spread(MoveArgs a) {
 }
 
 // combine, and dispatch's gradient (without weights): a warp per token and U
-// vectors of each lane, with the vectors of EXPERT_BATCH slots on their way.
-constexpr int EXPERT_BATCH = 8;
-template <typename T, int VEC, int U>
+// vectors of each lane, with the vectors of BATCH slots on their way.
+template <typename T, int VEC, int U, int BATCH>
 __global__ void __launch_bounds__(256) expert_join(MoveArgs a) {
     using Row = RowVectors<T, VEC, U>;
     using V = Vec<T, VEC>;
@@ -143,10 +145,10 @@ __global__ void __launch_bounds__(256) expert_join(MoveArgs a) {
         const float weight = lane_weight<T>(a, t, j0);
         unsigned todo = __ballot_sync(0xFFFFFFFFu, row >= 0);
         while (todo) {
-            Row x[EXPERT_BATCH];
-            float w[EXPERT_BATCH];
+            Row x[BATCH];
+            float w[BATCH];
 #pragma unroll
-            for (int b = 0; b < EXPERT_BATCH; ++b) {
+            for (int b = 0; b < BATCH; ++b) {
                 const int j = todo ? __ffs(todo) - 1 : 0;
                 const V* from = reinterpret_cast<const V*>(static_cast<const T*>(a.slot_rows) + __shfl_sync(0xFFFFFFFFu, row, j) * a.lds);
                 w[b] = __shfl_sync(0xFFFFFFFFu, weight, j);
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(256) expert_join(MoveArgs a) {
                 todo &= todo - 1;
             }
 #pragma unroll
-            for (int b = 0; b < EXPERT_BATCH; ++b)
+            for (int b = 0; b < BATCH; ++b)
 #pragma unroll
                 for (int p = 0; p < Row::PAIRS; ++p) s[p] = fma2(f2(w[b]), x[b].pair(p), s[p]);
         }
@@ -174,29 +176,28 @@ __global__ void __launch_bounds__(256) expert_join(MoveArgs a) {
 }
 
 // combine's gradients: `share` warps of a block per token, each every share-th
-// stretch of U vectors of each lane, EXPERT_BATCH slots at a time.  The sums
-// over a row are put together warp by warp.  The warps behind those clear rows.
-template <typename T, int VEC, int U>
+// stretch of U vectors of each lane, BATCH slots at a time.  The sums
+// over a row are put together warp by warp.  The first blocks clear rows.
+template <typename T, int VEC, int U, int BATCH>
 __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
     using Row = RowVectors<T, VEC, U>;
     using V = Vec<T, VEC>;
-    __shared__ float part[8][EXPERT_BATCH];
+    __shared__ float part[8][BATCH];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.H / VEC, per = 8 / a.share;
-    const int64_t tokens = (a.T + per - 1) / per;
-    if (blockIdx.x >= tokens) return clear_rows<T, VEC>(a, ((blockIdx.x - tokens) * 8 + warp) * 32);
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * per + warp / a.share;
+    if (static_cast<int>(blockIdx.x) < a.clearing) return clear_rows<T, VEC>(a, (blockIdx.x * 8ll + warp) * EXPERT_CLEAR);
+    const int64_t t = (static_cast<int64_t>(blockIdx.x) - a.clearing) * per + warp / a.share;
     const bool here = t < a.T;
     const int first = warp % a.share * 32 * U + lane, step = a.share * 32 * U;
     const V* dy = reinterpret_cast<const V*>(static_cast<const T*>(a.token_rows) + t * a.ldt);
-    for (int j0 = 0; j0 < a.k; j0 += EXPERT_BATCH) {
+    for (int j0 = 0; j0 < a.k; j0 += BATCH) {
         const int64_t row = here ? lane_row(a, t, j0) : -1;
         const float weight = here ? lane_weight<T>(a, t, j0) : 0.f;
-        const V* from[EXPERT_BATCH];
-        V* to[EXPERT_BATCH];
-        F2 w[EXPERT_BATCH], dot[EXPERT_BATCH];
+        const V* from[BATCH];
+        V* to[BATCH];
+        F2 w[BATCH], dot[BATCH];
         bool any = false;
 #pragma unroll
-        for (int b = 0; b < EXPERT_BATCH; ++b) {
+        for (int b = 0; b < BATCH; ++b) {
             const int64_t r = __shfl_sync(0xFFFFFFFFu, row, b);
             from[b] = r >= 0 && a.weights_out ? reinterpret_cast<const V*>(static_cast<const T*>(a.slot_rows) + r * a.lds) : nullptr;
             to[b] = r >= 0 && a.slot_out ? reinterpret_cast<V*>(static_cast<T*>(a.slot_out) + r * a.ldso) : nullptr;
@@ -207,21 +208,21 @@ __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
         }
         if (any)
             for (int k0 = first; k0 < n; k0 += step) {
-                Row d, y[EXPERT_BATCH];
+                Row d, y[BATCH];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     d.v[u] = V{};
                     if (k0 + 32 * u < n) d.v[u] = dy[k0 + 32 * u];
                 }
 #pragma unroll
-                for (int b = 0; b < EXPERT_BATCH; ++b)
+                for (int b = 0; b < BATCH; ++b)
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         y[b].v[u] = V{};
                         if (from[b] && k0 + 32 * u < n) load_now(y[b].v[u], from[b] + k0 + 32 * u);
                     }
 #pragma unroll
-                for (int b = 0; b < EXPERT_BATCH; ++b) {
+                for (int b = 0; b < BATCH; ++b) {
 #pragma unroll
                     for (int p = 0; p < Row::PAIRS; ++p) dot[b] = fma2(d.pair(p), y[b].pair(p), dot[b]);
                     if (!to[b]) continue;
@@ -236,18 +237,18 @@ __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
         if (!a.weights_out) continue;
         float mine = 0.f;  // lane b: the batch's slot b
 #pragma unroll
-        for (int b = 0; b < EXPERT_BATCH; ++b) {
+        for (int b = 0; b < BATCH; ++b) {
             const float v = warp_sum(lo(dot[b]) + hi(dot[b]));
             if (lane == b) mine = v;
         }
         if (a.share > 1) {
             __syncthreads();
-            if (lane < EXPERT_BATCH) part[warp][lane] = mine;
+            if (lane < BATCH) part[warp][lane] = mine;
             __syncthreads();
-            if (warp % a.share == 0 && lane < EXPERT_BATCH)
+            if (warp % a.share == 0 && lane < BATCH)
                 for (int s = 1; s < a.share; ++s) mine += part[warp + s][lane];
         }
-        if (here && warp % a.share == 0 && lane < EXPERT_BATCH && j0 + lane < a.k) {
+        if (here && warp % a.share == 0 && lane < BATCH && j0 + lane < a.k) {
             const int64_t slot = t * a.k + j0 + lane;
             if (a.w32)
                 static_cast<float*>(a.weights_out)[slot] = mine;
@@ -324,23 +325,30 @@ enum class Move { SPREAD, JOIN, JOIN_BWD };
 // 16-byte vectors `wide` of them where that still gives every SM its warps.
 template <typename T, int VEC>
 lce_status_t move_as(MoveArgs a, Move what, cudaStream_t s) {
-    constexpr int NARROW = VEC == 1 ? 8 : VEC * sizeof(T) < 16 ? 4 : 1, WIDE = VEC * sizeof(T) < 16 ? NARROW : 4;
-    const int64_t n = a.H / VEC, clear = what != Move::JOIN && a.slot_out ? (a.R + 31) / 32 : 0;  // warps
+    // (16384 tokens of 8 slots, 2048 bf16: combine with two vectors and eight slots at a time 4% faster than with one and
+    // eight or four and four; single elements with four slots, not eight: 4099 x 1601 fp16 in training 95 us, not 138)
+    constexpr bool V16 = VEC * sizeof(T) == 16;
+    constexpr int NARROW = VEC == 1 ? 8 : V16 ? 1 : 4, WIDE = V16 ? 4 : NARROW, BWD = VEC == 1 ? 2 : 1, JOIN = V16 ? 2 : NARROW;
+    constexpr int BATCH = V16 ? 8 : 4;
+    const int64_t n = a.H / VEC;
     auto parts = [&](int u) { return (n + 32 * u - 1) / (32 * u); };
     const bool wide = what == Move::SPREAD && a.T * parts(WIDE) >= 152 * 32;
-    int64_t warps = a.T * parts(wide ? WIDE : NARROW);
+    int64_t warps = a.T * parts(what == Move::JOIN ? JOIN : wide ? WIDE : NARROW);
     if (what == Move::JOIN_BWD) {
         a.share = 1;
-        while (a.share < 8 && a.share < parts(NARROW) && a.T * a.share < 152 * 32) a.share *= 2;
+        while (a.share < 8 && a.share < parts(BWD) && a.T * a.share < 152 * 32) a.share *= 2;
         warps = (a.T + 8 / a.share - 1) / (8 / a.share) * 8;
     }
-    if (warps + clear == 0) return LCE_OK;
-    if (warps + clear > INT32_MAX) return LCE_ERR_UNSUPPORTED;
-    const unsigned grid = static_cast<unsigned>((warps + clear + 7) / 8);
+    const int64_t clearing = what != Move::JOIN && a.slot_out ? (a.R + 8 * EXPERT_CLEAR - 1) / (8 * EXPERT_CLEAR) : 0;
+    const int64_t blocks = (warps + 7) / 8 + clearing;
+    if (blocks == 0) return LCE_OK;
+    if (warps > INT32_MAX || blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
+    a.clearing = static_cast<int32_t>(clearing);
+    const unsigned grid = static_cast<unsigned>(blocks);
     if (what == Move::JOIN)
-        LCE_PROFILED(expert_join<T, VEC, NARROW><<<grid, 256, 0, s>>>(a));
+        LCE_PROFILED(expert_join<T, VEC, JOIN, BATCH><<<grid, 256, 0, s>>>(a));
     else if (what == Move::JOIN_BWD)
-        LCE_PROFILED(expert_join_bwd<T, VEC, NARROW><<<grid, 256, 0, s>>>(a));
+        LCE_PROFILED(expert_join_bwd<T, VEC, BWD, BATCH><<<grid, 256, 0, s>>>(a));
     else if (wide)
         LCE_PROFILED(expert_spread<T, VEC, WIDE><<<grid, 256, 0, s>>>(a));
     else

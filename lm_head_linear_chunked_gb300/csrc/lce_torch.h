@@ -4,11 +4,12 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/TracerMode.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/SmallVector.h>
+#include <c10/util/accumulate.h>
 #include <torch/csrc/autograd/forward_grad.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -126,10 +127,26 @@ template <typename T>
 T* ptr(const Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 inline void* ptr(const OptTensor& t) { return t ? t->data_ptr() : nullptr; }
 
+// Outputs and workspaces, straight from the allocator: the dispatcher's way to
+// it takes as long as the rest of a small call.  A trace has to see them.
 inline Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device& device) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+    if (!device.is_cuda() || at::tracer::impl::is_dispatch_enabled()) return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+    return at::detail::empty_cuda(shape, type, device, std::nullopt);
 }
-inline Tensor like(const Tensor& t) { return at::empty_like(t, at::MemoryFormat::Contiguous); }
+// Two tensors of one type out of one allocation.
+inline std::pair<Tensor, Tensor> empty_pair(at::IntArrayRef a, at::IntArrayRef b, at::ScalarType type, const at::Device& device) {
+    const int64_t size = static_cast<int64_t>(c10::elementSize(type)), step = 256 / size;
+    const int64_t first = (c10::multiply_integers(a) + step - 1) / step * step;
+    const Tensor both = empty({first + c10::multiply_integers(b)}, type, device);
+    auto part = [&](at::IntArrayRef shape, int64_t offset) {
+        auto t = c10::make_intrusive<c10::TensorImpl>(c10::Storage(both.storage()), both.key_set(), both.dtype());
+        t->set_sizes_contiguous(shape);
+        t->set_storage_offset(offset);
+        return Tensor(std::move(t));
+    };
+    return {part(a, 0), part(b, first)};
+}
+inline Tensor like(const Tensor& t) { return empty(t.sizes(), t.scalar_type(), t.device()); }
 
 // t as rows of its last dimension: t itself where its rows are contiguous and
 // evenly spaced, else a contiguous copy.

@@ -243,8 +243,9 @@ std::vector<Tensor> expert_plan(const Tensor& experts_in, int64_t E, const OptTe
     const Tensor experts = experts_in.contiguous();
     OptTensor mask;
     if (mask_in) mask = mask_in->contiguous();
-    std::vector<Tensor> out{empty(experts.sizes(), at::kInt, dev), empty({R}, at::kInt, dev), empty({E}, at::kLong, dev),
-                            empty({E + 1}, at::kLong, dev), empty({static_cast<int64_t>(space)}, at::kByte, dev)};
+    const auto [positions, slots] = empty_pair(experts.sizes(), {R}, at::kInt, dev);
+    const auto [counts, offsets] = empty_pair({E}, {E + 1}, at::kLong, dev);
+    std::vector<Tensor> out{positions, slots, counts, offsets, empty({static_cast<int64_t>(space)}, at::kByte, dev)};
     check(lib.expert_plan(T, k, E, align, experts.data_ptr(), bytes, static_cast<const uint8_t*>(ptr(mask)), ptr<int32_t>(out[0]),
                           ptr<int32_t>(out[1]), ptr<int64_t>(out[2]), ptr<int64_t>(out[3]), out[4].data_ptr(), space, stream_of(dev)),
           "lce_expert_plan");
@@ -303,7 +304,7 @@ int check_weights(const Tensor& weights, const Tensor& rows, const Tensor& posit
     return type_code(weights, "weights");
 }
 
-Tensor plain(const Tensor& t) { return t.resolve_neg().contiguous(); }
+Tensor plain(const Tensor& t) { return t.is_neg() ? t.resolve_neg().contiguous() : t.contiguous(); }
 
 Tensor expert_combine(const Tensor& rows_in, const OptTensor& weights_in, const Tensor& positions, const Tensor& slots,
                       bool recorded) {
