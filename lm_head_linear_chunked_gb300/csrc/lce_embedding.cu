@@ -26,15 +26,17 @@ struct EmbFwd {
     int64_t ldy;
     unsigned* status;  // nullable
     int32_t H;
+    Deal deal;         // of the rows' vectors
 };
 
 __device__ __forceinline__ int64_t token_at(const void* tokens, bool idx64, int64_t i) {
     return idx64 ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
 }
 
-// A warp per U vectors of each lane of a token's row.
+// Wide rows: a warp per U vectors of each lane of a token's row, so that the
+// token is looked up once for them.
 template <typename T, int VEC, int U>
-__global__ void __launch_bounds__(256) emb_fwd(EmbFwd<T> a) {
+__global__ void __launch_bounds__(256) emb_fwd_wide(EmbFwd<T> a) {
     using V = Vec<T, VEC>;
     const int n = a.H / VEC, parts = (n + 32 * U - 1) / (32 * U), lane = threadIdx.x & 31;
     const int64_t item = blockIdx.x * 8ll + (threadIdx.x >> 5), i = item / parts;
@@ -60,6 +62,39 @@ __global__ void __launch_bounds__(256) emb_fwd(EmbFwd<T> a) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) x[u].set(e, x[u].f(e) * a.scale);
         y[k0 + 32 * u] = x[u];
+    }
+}
+
+// Narrow rows, dealt out by the vector.
+template <typename T, int VEC, int U>
+__global__ void __launch_bounds__(256) emb_fwd_narrow(EmbFwd<T> a) {
+    using V = Vec<T, VEC>;
+    const Dealt<U> mine(a.deal, blockIdx.x);
+    V x[U];
+    uint32_t at[U];
+    int64_t v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = mine.get(a.deal, u, at + u);
+        v[u] = i < a.N ? token_at(a.tokens, a.idx64, i) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (v[u] >= 0 && v[u] < a.V) x[u] = reinterpret_cast<const V*>(a.w + v[u] * a.ldw)[at[u]];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = mine.get(a.deal, u, at + u);
+        if (i >= a.N) break;
+        if (v[u] < 0 || v[u] >= a.V) {
+            const bool padding = v[u] == a.padding;
+            if (!padding && a.status && at[u] == 0) atomicOr(a.status, STATUS_INDEX);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[u].set(e, padding ? 0.f : __int_as_float(0x7fffffff));
+        } else if (a.scale != 1.f) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[u].set(e, x[u].f(e) * a.scale);
+        }
+        reinterpret_cast<V*>(a.y + i * a.ldy)[at[u]] = x[u];
     }
 }
 
@@ -469,18 +504,33 @@ int vector_of(const void* p, int64_t ld, int64_t H) {
     return H % V4 == 0 && ld % V4 == 0 && aligned_to(p, 4) ? V4 : 1;
 }
 
+// Rows of at least 64 vectors take a warp (16384 tokens of 1024 bf16: 8.9 us,
+// 10.4 dealt out; 131072 of 64 fp16: 20.7 and 6.5); several vectors a lane where
+// that still gives every SM its warps, one for a decode step.
 template <typename T, int VEC>
-lce_status_t emb_lookup(const EmbFwd<T>& a, cudaStream_t s) {
-    // several vectors a lane where that still gives every SM its warps, one for a decode step
+lce_status_t emb_lookup(EmbFwd<T> a, cudaStream_t s) {
     constexpr int U = VEC * sizeof(T) == 16 ? 4 : 8;
-    const int64_t n = a.H / VEC, wide = a.N * ((n + 32 * U - 1) / (32 * U));
-    const bool enough = n > 32 && wide >= 152 * 32;
-    const int64_t blocks = ((enough ? wide : a.N * ((n + 31) / 32)) + 7) / 8;
+    const int64_t n = a.H / VEC;
+    if (n >= 64) {
+        const int64_t wide = a.N * ((n + 32 * U - 1) / (32 * U));
+        const bool enough = wide >= 152 * 32;
+        const int64_t blocks = ((enough ? wide : a.N * ((n + 31) / 32)) + 7) / 8;
+        if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
+        if (enough)
+            LCE_PROFILED(emb_fwd_wide<T, VEC, U><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+        else
+            LCE_PROFILED(emb_fwd_wide<T, VEC, 1><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+        return LCE_OK;
+    }
+    const int64_t vectors = a.N * n;
+    const bool enough = vectors >= 152 * 4 * 256 * 4;
+    const int64_t share = 256 * (enough ? 4 : 1), blocks = (vectors + share - 1) / share;
     if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
+    a.deal = deal_of(n);
     if (enough)
-        LCE_PROFILED(emb_fwd<T, VEC, U><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+        LCE_PROFILED(emb_fwd_narrow<T, VEC, 4><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
     else
-        LCE_PROFILED(emb_fwd<T, VEC, 1><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+        LCE_PROFILED(emb_fwd_narrow<T, VEC, 1><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
     return LCE_OK;
 }
 
@@ -552,7 +602,7 @@ lce_status_t lce_embedding_forward(int64_t N, int64_t V, int64_t H, int dtype, c
     return with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);
         const EmbFwd<T> a{tokens, index_bytes == 8, static_cast<const T*>(weight), ldw, N, V, padding_token, scale,
-                          static_cast<T*>(y), ldy, static_cast<unsigned*>(status), static_cast<int32_t>(H)};
+                          static_cast<T*>(y), ldy, static_cast<unsigned*>(status), static_cast<int32_t>(H), {}};
         constexpr int V16 = vec16<T>(), V4 = 4 / static_cast<int>(sizeof(T));
         const int from = vector_of<T>(weight, ldw, H), to = vector_of<T>(y, ldy, H), vec = from < to ? from : to;
         if (vec == V16) return emb_lookup<T, V16>(a, s);

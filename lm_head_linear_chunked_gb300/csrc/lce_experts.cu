@@ -70,6 +70,7 @@ struct MoveArgs {
     int32_t k, H;
     int32_t share;           // warps to a token (combine's gradients): 1, 2, 4 or 8
     int32_t clearing;        // blocks that clear rows
+    Deal deal;               // of the tokens' vectors
 };
 
 // The rows of up to 32 slots of a token, one to a lane; -1 for none (a position
@@ -175,36 +176,115 @@ __global__ void __launch_bounds__(256) expert_join(MoveArgs a) {
         if (k0 + 32 * u < n) y[k0 + 32 * u] = o.v[u];
 }
 
-// combine's gradients: `share` warps of a block per token, each every share-th
-// stretch of U vectors of each lane, BATCH slots at a time.  The sums
-// over a row are put together warp by warp.  The first blocks clear rows.
+// The row of a slot; -1 for none.
+__device__ __forceinline__ int64_t slot_row(const MoveArgs& a, int64_t slot) {
+    const int64_t p = a.positions[slot];
+    return p < a.R ? p : -1;
+}
+
+// dispatch of narrow rows, dealt out by the vector: it is read once and written to all its rows.  The
+// first blocks clear rows.
+template <typename T, int VEC, int U>
+__global__ void __launch_bounds__(256) expert_spread_narrow(MoveArgs a) {
+    using V = Vec<T, VEC>;
+    if (static_cast<int>(blockIdx.x) < a.clearing) return clear_rows<T, VEC>(a, (blockIdx.x * 8ll + (threadIdx.x >> 5)) * EXPERT_CLEAR);
+    const Dealt<U> mine(a.deal, blockIdx.x - a.clearing);
+    V v[U];
+    uint32_t at[U];
+    int64_t t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        t[u] = mine.get(a.deal, u, at + u);
+        if (t[u] < a.T) v[u] = reinterpret_cast<const V*>(static_cast<const T*>(a.token_rows) + t[u] * a.ldt)[at[u]];
+    }
+    for (int j = 0; j < a.k; ++j)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t p = t[u] < a.T ? slot_row(a, t[u] * a.k + j) : -1;
+            if (p >= 0) reinterpret_cast<V*>(static_cast<T*>(a.slot_out) + p * a.ldso)[at[u]] = v[u];
+        }
+}
+
+// combine of narrow rows, dealt out by the vector.
 template <typename T, int VEC, int U, int BATCH>
+__global__ void __launch_bounds__(256) expert_join_narrow(MoveArgs a) {
+    using Row = RowVectors<T, VEC, U>;
+    using V = Vec<T, VEC>;
+    const Dealt<U> mine(a.deal, blockIdx.x);
+    uint32_t at[U];
+    int64_t t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) t[u] = mine.get(a.deal, u, at + u);
+    F2 s[Row::PAIRS];
+#pragma unroll
+    for (int p = 0; p < Row::PAIRS; ++p) s[p] = f2(0.f);
+    for (int j0 = 0; j0 < a.k; j0 += BATCH) {
+        Row x[BATCH];
+        float w[BATCH][U];
+        int64_t row[BATCH][U];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool in = j0 + b < a.k && t[u] < a.T;
+                row[b][u] = in ? slot_row(a, t[u] * a.k + j0 + b) : -1;
+                w[b][u] = in && a.weights && row[b][u] >= 0 ? load_w<T>(a.weights, a.w32, t[u] * a.k + j0 + b) : 1.f;
+            }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                x[b].v[u] = V{};
+                if (row[b][u] >= 0) load_now(x[b].v[u], reinterpret_cast<const V*>(static_cast<const T*>(a.slot_rows) + row[b][u] * a.lds) + at[u]);
+            }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+            for (int p = 0; p < Row::PAIRS; ++p)
+                s[p] = fma2(VEC == 1 ? f2(w[b][2 * p % U], w[b][(2 * p + 1) % U]) : f2(w[b][2 * p / VEC]), x[b].pair(p), s[p]);
+    }
+    Row o;
+#pragma unroll
+    for (int p = 0; p < Row::PAIRS; ++p) o.set(p, s[p]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (t[u] < a.T) reinterpret_cast<V*>(static_cast<T*>(a.token_out) + t[u] * a.ldto)[at[u]] = o.v[u];
+}
+
+// combine's gradients: LANES lanes of a warp per token for narrow rows, else
+// `share` warps of a block, each every share-th stretch of U vectors of each
+// lane; BATCH slots at a time.  The sums over a row are put together lane by
+// lane, then warp by warp.  The first blocks clear rows.
+template <typename T, int VEC, int U, int BATCH, int LANES>
 __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
     using Row = RowVectors<T, VEC, U>;
     using V = Vec<T, VEC>;
+    static_assert(BATCH <= LANES);
+    constexpr unsigned ALL = 0xFFFFFFFFu;
     __shared__ float part[8][BATCH];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.H / VEC, per = 8 / a.share;
+    const int lane = threadIdx.x & (LANES - 1), warp = threadIdx.x >> 5, n = a.H / VEC;
     if (static_cast<int>(blockIdx.x) < a.clearing) return clear_rows<T, VEC>(a, (blockIdx.x * 8ll + warp) * EXPERT_CLEAR);
-    const int64_t t = (static_cast<int64_t>(blockIdx.x) - a.clearing) * per + warp / a.share;
-    const bool here = t < a.T;
-    const int first = warp % a.share * 32 * U + lane, step = a.share * 32 * U;
+    const int64_t block = static_cast<int64_t>(blockIdx.x) - a.clearing;
+    const int64_t t = LANES < 32 ? block * (256 / LANES) + threadIdx.x / LANES : block * (8 / a.share) + warp / a.share;
+    const bool here = t < a.T, lead = LANES < 32 || warp % a.share == 0;
+    const int first = (LANES < 32 ? 0 : warp % a.share * 32 * U) + lane, step = LANES < 32 ? LANES * U : a.share * 32 * U;
     const V* dy = reinterpret_cast<const V*>(static_cast<const T*>(a.token_rows) + t * a.ldt);
     for (int j0 = 0; j0 < a.k; j0 += BATCH) {
-        const int64_t row = here ? lane_row(a, t, j0) : -1;
-        const float weight = here ? lane_weight<T>(a, t, j0) : 0.f;
+        const bool mine_in = here && lane < BATCH && j0 + lane < a.k;
+        const int64_t row = mine_in ? slot_row(a, t * a.k + j0 + lane) : -1;
+        const float weight = mine_in && a.weights ? load_w<T>(a.weights, a.w32, t * a.k + j0 + lane) : 1.f;
         const V* from[BATCH];
         V* to[BATCH];
         F2 w[BATCH], dot[BATCH];
         bool any = false;
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
-            const int64_t r = __shfl_sync(0xFFFFFFFFu, row, b);
+            const int64_t r = __shfl_sync(ALL, row, b, LANES);
             from[b] = r >= 0 && a.weights_out ? reinterpret_cast<const V*>(static_cast<const T*>(a.slot_rows) + r * a.lds) : nullptr;
             to[b] = r >= 0 && a.slot_out ? reinterpret_cast<V*>(static_cast<T*>(a.slot_out) + r * a.ldso) : nullptr;
-            w[b] = f2(__shfl_sync(0xFFFFFFFFu, weight, b));
+            w[b] = f2(__shfl_sync(ALL, weight, b, LANES));
             dot[b] = f2(0.f);
-            any |= r >= 0 && j0 + b < a.k;
-            if (j0 + b >= a.k) from[b] = to[b] = nullptr;
+            any |= r >= 0;
         }
         if (any)
             for (int k0 = first; k0 < n; k0 += step) {
@@ -212,14 +292,14 @@ __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     d.v[u] = V{};
-                    if (k0 + 32 * u < n) d.v[u] = dy[k0 + 32 * u];
+                    if (k0 + LANES * u < n) d.v[u] = dy[k0 + LANES * u];
                 }
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b)
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         y[b].v[u] = V{};
-                        if (from[b] && k0 + 32 * u < n) load_now(y[b].v[u], from[b] + k0 + 32 * u);
+                        if (from[b] && k0 + LANES * u < n) load_now(y[b].v[u], from[b] + k0 + LANES * u);
                     }
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b) {
@@ -231,24 +311,26 @@ __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
                     for (int p = 0; p < Row::PAIRS; ++p) o.set(p, mul2(w[b], d.pair(p)));
 #pragma unroll
                     for (int u = 0; u < U; ++u)
-                        if (k0 + 32 * u < n) to[b][k0 + 32 * u] = o.v[u];
+                        if (k0 + LANES * u < n) to[b][k0 + LANES * u] = o.v[u];
                 }
             }
         if (!a.weights_out) continue;
         float mine = 0.f;  // lane b: the batch's slot b
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
-            const float v = warp_sum(lo(dot[b]) + hi(dot[b]));
+            float v = lo(dot[b]) + hi(dot[b]);
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
             if (lane == b) mine = v;
         }
-        if (a.share > 1) {
+        if (LANES == 32 && a.share > 1) {
             __syncthreads();
             if (lane < BATCH) part[warp][lane] = mine;
             __syncthreads();
-            if (warp % a.share == 0 && lane < BATCH)
+            if (lead && lane < BATCH)
                 for (int s = 1; s < a.share; ++s) mine += part[warp + s][lane];
         }
-        if (here && warp % a.share == 0 && lane < BATCH && j0 + lane < a.k) {
+        if (mine_in && lead) {
             const int64_t slot = t * a.k + j0 + lane;
             if (a.w32)
                 static_cast<float*>(a.weights_out)[slot] = mine;
@@ -330,29 +412,66 @@ lce_status_t move_as(MoveArgs a, Move what, cudaStream_t s) {
     constexpr bool V16 = VEC * sizeof(T) == 16;
     constexpr int NARROW = VEC == 1 ? 8 : V16 ? 1 : 4, WIDE = V16 ? 4 : NARROW, BWD = VEC == 1 ? 2 : 1, JOIN = V16 ? 2 : NARROW;
     constexpr int BATCH = V16 ? 8 : 4;
-    const int64_t n = a.H / VEC;
+    const int64_t n = a.H / VEC, vectors = a.T * n;
     auto parts = [&](int u) { return (n + 32 * u - 1) / (32 * u); };
-    const bool wide = what == Move::SPREAD && a.T * parts(WIDE) >= 152 * 32;
-    int64_t warps = a.T * parts(what == Move::JOIN ? JOIN : wide ? WIDE : NARROW);
+    // rows of less than half a warp of 16-byte vectors are dealt out by the vector (65536 tokens of 4 slots, 64 bf16:
+    // dispatch 10.3 us, combine 14.5; a warp to a token 16.5 and 40.6), the gradients by parts of a warp
+    const bool narrow = V16 && n <= 16, wide = !narrow && what == Move::SPREAD && a.T * parts(WIDE) >= 152 * 32;
+    const int lanes = !V16 || n > 16 ? 32 : n > 8 ? 16 : 8;
+    int64_t work = 0;  // blocks
     if (what == Move::JOIN_BWD) {
         a.share = 1;
         while (a.share < 8 && a.share < parts(BWD) && a.T * a.share < 152 * 32) a.share *= 2;
-        warps = (a.T + 8 / a.share - 1) / (8 / a.share) * 8;
+        const int64_t tokens = lanes < 32 ? 256 / lanes : 8 / a.share;
+        work = (a.T + tokens - 1) / tokens;
+    } else if (narrow) {
+        work = (vectors + 256 * JOIN - 1) / (256 * JOIN);
+        a.deal = deal_of(n);
+    } else {
+        work = (a.T * parts(what == Move::JOIN ? JOIN : wide ? WIDE : NARROW) + 7) / 8;
+        if (work * 8 > INT32_MAX) return LCE_ERR_UNSUPPORTED;
     }
     const int64_t clearing = what != Move::JOIN && a.slot_out ? (a.R + 8 * EXPERT_CLEAR - 1) / (8 * EXPERT_CLEAR) : 0;
-    const int64_t blocks = (warps + 7) / 8 + clearing;
+    const int64_t blocks = work + clearing;
     if (blocks == 0) return LCE_OK;
-    if (warps > INT32_MAX || blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
+    if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
     a.clearing = static_cast<int32_t>(clearing);
     const unsigned grid = static_cast<unsigned>(blocks);
-    if (what == Move::JOIN)
+    if (what == Move::JOIN_BWD) {
+        if constexpr (V16) {
+            if (lanes < 32) {
+                if (lanes == 16)
+                    LCE_PROFILED(expert_join_bwd<T, VEC, BWD, 4, 16><<<grid, 256, 0, s>>>(a));
+                else
+                    LCE_PROFILED(expert_join_bwd<T, VEC, BWD, 4, 8><<<grid, 256, 0, s>>>(a));
+                return LCE_OK;
+            }
+            if (a.k > 4) {
+                LCE_PROFILED(expert_join_bwd<T, VEC, BWD, BATCH, 32><<<grid, 256, 0, s>>>(a));
+                return LCE_OK;
+            }
+        }
+        LCE_PROFILED(expert_join_bwd<T, VEC, BWD, 4, 32><<<grid, 256, 0, s>>>(a));
+    } else if (what == Move::JOIN) {
+        if constexpr (V16) {
+            if (narrow) {
+                LCE_PROFILED(expert_join_narrow<T, VEC, JOIN, BATCH><<<grid, 256, 0, s>>>(a));
+                return LCE_OK;
+            }
+        }
         LCE_PROFILED(expert_join<T, VEC, JOIN, BATCH><<<grid, 256, 0, s>>>(a));
-    else if (what == Move::JOIN_BWD)
-        LCE_PROFILED(expert_join_bwd<T, VEC, BWD, BATCH><<<grid, 256, 0, s>>>(a));
-    else if (wide)
-        LCE_PROFILED(expert_spread<T, VEC, WIDE><<<grid, 256, 0, s>>>(a));
-    else
-        LCE_PROFILED(expert_spread<T, VEC, NARROW><<<grid, 256, 0, s>>>(a));
+    } else {
+        if constexpr (V16) {
+            if (narrow) {
+                LCE_PROFILED(expert_spread_narrow<T, VEC, JOIN><<<grid, 256, 0, s>>>(a));
+                return LCE_OK;
+            }
+        }
+        if (wide)
+            LCE_PROFILED(expert_spread<T, VEC, WIDE><<<grid, 256, 0, s>>>(a));
+        else
+            LCE_PROFILED(expert_spread<T, VEC, NARROW><<<grid, 256, 0, s>>>(a));
+    }
     return LCE_OK;
 }
 
