@@ -213,6 +213,7 @@ struct EmbBwd {
     int64_t lddw, chunks;
     bool add;
     int32_t H, slabs;
+    int32_t split;    // warps to a chunk and slab
     int32_t joining;  // blocks of the last kernel that add pieces up
 };
 
@@ -251,7 +252,9 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
     int64_t item = blockIdx.x * 8ll + (threadIdx.x >> 5);
     launch_dependents();
     wait_for_primary();
-    if (item >= a.chunks * a.slabs) return;
+    if (item >= a.chunks * a.slabs * a.split) return;
+    const int sub = static_cast<int>(item % a.split);
+    item /= a.split;
     const int64_t c = item / a.slabs;
     const int k0 = static_cast<int>(item % a.slabs) * 32 * ITEMS + lane;
     const int64_t at = c * EMB_CHUNK + lane;
@@ -268,17 +271,25 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
     auto whole = [](int rows) { return rows < 0 ? 32 : rows; };  // __ffs finds nothing where all 32 are equal
     const bool came = head_before > 0, goes = items == 32 && tail_behind != 0;
     const bool head_long = came && head_before + whole(head_here) > 32, tail_long = goes && tail_here + whole(tail_behind) > 32;
-    const int begin = came && !head_long ? head_here : 0;                   // the warp before has those
-    const int end = goes && !tail_long ? 32 + tail_behind : items;
+    int begin = came && !head_long ? head_here : 0;                         // the warp before has those
+    int end = goes && !tail_long ? 32 + tail_behind : items;
     int32_t next = __shfl_down_sync(ALL, key, 1);
     if (lane == 31) next = -1;                                              // a border, unless the last run goes on
     unsigned last = __ballot_sync(ALL, key != next);
     if (end > 32) last &= 0x7FFFFFFFu;
-    if (tail_long && !(head_long && head == tail) && k0 == lane) {          // a long run starts here: where does it end?
+    if (tail_long && !(head_long && head == tail) && k0 == lane && sub == 0) {  // a long run starts here: where does it end?
         int64_t to = c + 1;
         for (unsigned same = ALL; same == ALL; to += same == ALL ? 32 : __ffs(~same) - 1)
             same = __ballot_sync(ALL, to + lane < a.chunks && a.keys[(to + lane) * EMB_CHUNK] == tail);
         if (lane == 0) a.spans[atomicAdd(a.n_spans, 1)] = make_int4(static_cast<int>(c), static_cast<int>(to), tail, 0);
+    }
+    if (a.split > 1) {  // the runs that start in this part of the chunk
+        const int width = 32 / a.split, lo = sub * width;
+        const unsigned starts = (last << 1 | 1u << (begin & 31)) & ALL << (begin & 31) & (items < 32 ? (1u << items) - 1 : ALL);
+        const unsigned here = starts >> lo & ((1u << width) - 1), behind = lo + width < 32 ? starts >> (lo + width) : 0u;
+        if (!here || begin >= items) return;
+        begin = lo + __ffs(here) - 1;
+        if (behind) end = lo + width + __ffs(behind) - 1;
     }
     constexpr int PAIRS = VEC * ITEMS / 2;
     F2 s[PAIRS];
@@ -333,7 +344,7 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
             finish(i - 1);
         }
     } else {  // a few rows in registers
-        constexpr int BATCH = 4;
+        constexpr int BATCH = 16;
         for (int i0 = begin; i0 < end; i0 += BATCH) {
             RowVectors<T, VEC, ITEMS> x[BATCH];
 #pragma unroll
@@ -342,7 +353,7 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
 #pragma unroll
                 for (int k = 0; k < ITEMS; ++k) {
                     x[b].v[k] = V{};
-                    if (i0 + b < end && k0 + 32 * k < n) x[b].v[k] = p[32 * k];
+                    if (i0 + b < end && k0 + 32 * k < n) load_now(x[b].v[k], p + 32 * k);
                 }
             }
 #pragma unroll
@@ -388,19 +399,28 @@ __global__ void __launch_bounds__(256) emb_finish(EmbBwd<float> a) {
         F2 sum[PAIRS];
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) sum[p] = f2(0.f);
-        auto add = [&](int64_t part) {
-            RowVectors<float, VEC, ITEMS> x;
+        auto load = [&](RowVectors<float, VEC, ITEMS>& x, int64_t part) {  // -1: none
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
                 x.v[i] = Vec<float, VEC>{};
-                if (k0 + 32 * i < n) x.v[i] = reinterpret_cast<const Vec<float, VEC>*>(a.parts + part * a.H)[k0 + 32 * i];
+                if (part >= 0 && k0 + 32 * i < n) load_now(x.v[i], reinterpret_cast<const Vec<float, VEC>*>(a.parts + part * a.H) + k0 + 32 * i);
             }
-#pragma unroll
-            for (int p = 0; p < PAIRS; ++p) sum[p] = add2(sum[p], x.pair(p));
         };
-        if (warp == 0) add(c0 * 2 + 1);
-#pragma unroll 8
-        for (int64_t c = c0 + 1 + warp; c < end; c += 8) add(c * 2);
+        if (warp == 0) {
+            RowVectors<float, VEC, ITEMS> x;
+            load(x, c0 * 2 + 1);
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p) sum[p] = x.pair(p);
+        }
+        for (int64_t c = c0 + 1 + warp; c < end; c += 64) {  // eight loads on their way
+            RowVectors<float, VEC, ITEMS> x[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) load(x[b], c + 8 * b < end ? (c + 8 * b) * 2 : -1);
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p) sum[p] = add2(sum[p], x[b].pair(p));
+        }
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) s[warp][p][lane] = sum[p];
         __syncthreads();
@@ -425,6 +445,7 @@ lce_status_t emb_sizes(int64_t N, int64_t V, int64_t H) {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Bits of the keys 0 .. V, in digits of at most EMB_DIGIT_BITS.
+static_assert(EMB_DIGIT_BITS * (SORT_PASSES_MAX + 1) >= 31);
 struct Digits {
     int passes, bits;
 };
@@ -481,18 +502,26 @@ lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int6
     shape.hist = e.hist;
     shape.bad = e.bad;
     if (clear.rows) shape.extra = static_cast<int32_t>(SORT_BLOCKS) - shape.blocks;
-    const int kernels = shape.blocks > 1 ? 2 : 1;  // of a pass
-    clear.of = kernels * d.passes;
-    const FirstDigit first{tokens, idx64, static_cast<int32_t>(V), shape.bins - 1, padding, e.keys[0], e.rows[0], &e.hdr->status,
+    *where = (d.passes - 1) & 1;
+    FirstDigit first{tokens, idx64, static_cast<int32_t>(V), shape.bins - 1, padding, e.keys[0], e.rows[0], &e.hdr->status,
                            e.n_spans, name ? e.named : nullptr, shape.blocks, clear};
+    auto next = [&](int p) {
+        const int from = (p - 1) & 1, to = p & 1;
+        return NextDigit{e.keys[from], e.rows[from], p * d.bits, shape.bins - 1, e.keys[to], e.rows[to], clear};
+    };
+    if (shape.blocks == 1) {
+        SortAlone<FirstDigit, NextDigit> job{first, {}, shape, d.passes - 1};
+        for (int p = 1; p < d.passes; ++p) job.next[p - 1] = next(p);
+        return sort_alone_by(job, s);
+    }
+    clear.of = 2 * d.passes;  // a share for each kernel
+    first.clear = clear;
     lce_status_t st = sort_by(first, shape, true, s);
     shape.bad = nullptr;
     for (int p = 1; p < d.passes && st == LCE_OK; ++p) {
-        const int from = (p - 1) & 1, to = p & 1;
-        clear.part = p * kernels;
-        st = sort_by(NextDigit{e.keys[from], e.rows[from], p * d.bits, shape.bins - 1, e.keys[to], e.rows[to], clear}, shape, false, s);
+        clear.part = 2 * p;
+        st = sort_by(next(p), shape, false, s);
     }
-    *where = (d.passes - 1) & 1;
     return st;
 }
 
@@ -538,9 +567,11 @@ int32_t emb_slabs(int64_t vectors, int items) { return static_cast<int32_t>((vec
 
 template <typename T, typename W, int VEC>
 lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
-    constexpr int ITEMS = 8 / VEC, AHEAD = VEC * sizeof(T) >= 4 ? 8 : 0;
+    constexpr int AHEAD = VEC * sizeof(T) >= 4 ? 8 : 0, ITEMS = AHEAD ? 8 / VEC : 2;
     a.slabs = emb_slabs(a.H / VEC, ITEMS);
-    const int64_t blocks = (a.chunks * a.slabs + 7) / 8;
+    // a chunk's runs over four warps where there are few chunks (620 tokens of 128 bf16: 19.7 us, not 26.0; 90000: 52.1 and 63.2)
+    if (AHEAD && a.chunks * a.slabs < 152 * 32) a.split = 4;
+    const int64_t blocks = (a.chunks * a.slabs * a.split + 7) / 8;
     if (blocks == 0) return LCE_OK;  // no tokens: all rows have been cleared
     if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
     constexpr size_t smem = static_cast<size_t>(AHEAD) * ITEMS * 256 * VEC * sizeof(T);
@@ -641,7 +672,7 @@ lce_status_t lce_embedding_backward(int64_t N, int64_t V, int64_t H, int dtype, 
         using T = decltype(t);
         const EmbBwd<T> a{static_cast<const T*>(grad_y), ldg, N, V, scale, e.keys[where], e.rows[where],
                           late ? e.named : nullptr, e.n_spans, e.spans,
-                          e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, static_cast<int32_t>(H), 0, 0};
+                          e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, static_cast<int32_t>(H), 0, 1, 0};
         return gtype == LCE_F32 ? emb_gradient<T, float>(a, s) : emb_gradient<T, T>(a, s);
     });
 }

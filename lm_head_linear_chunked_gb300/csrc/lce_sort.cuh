@@ -32,7 +32,8 @@ namespace lce {
 constexpr int SORT_WARPS = 32;
 constexpr int SORT_THREADS = 32 * SORT_WARPS;
 constexpr int SORT_BINS_MAX = 1025;
-constexpr int64_t SORT_ITEMS = 2048;  // a block's fewest
+constexpr int64_t SORT_ALONE = 4096;  // items that one block sorts by itself
+constexpr int64_t SORT_ITEMS = 2048;  // a block's fewest where there are more
 constexpr int64_t SORT_BLOCKS = 152;
 
 struct SortShape {
@@ -43,8 +44,8 @@ struct SortShape {
 };
 
 inline int64_t sort_blocks(int64_t n) {
-    const int64_t b = (n + SORT_ITEMS - 1) / SORT_ITEMS;
-    return b < 1 ? 1 : (b < SORT_BLOCKS ? b : SORT_BLOCKS);
+    const int64_t b = n <= SORT_ALONE ? 1 : (n + SORT_ITEMS - 1) / SORT_ITEMS;
+    return b < SORT_BLOCKS ? b : SORT_BLOCKS;
 }
 inline size_t sort_smem(int bins) { return static_cast<size_t>(SORT_WARPS) * bins * 4; }
 
@@ -96,14 +97,11 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count(SortJob<F> job) {
     if (threadIdx.x == 0 && s.bad) s.bad[blockIdx.x] = any;
 }
 
+// Puts a block's items in their places.
 template <typename F>
-__global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
-    const F& f = job.f;
-    const SortShape& s = job.shape;
+__device__ __forceinline__ void place_items(const F& f, const SortShape& s) {
     extern __shared__ __align__(16) int32_t counts[];  // [SORT_WARPS, bins]: of each warp's items, then their places
     __shared__ int32_t sums[SORT_WARPS];
-    if (static_cast<int>(blockIdx.x) >= s.blocks) return f.beside(s.blocks > 1, blockIdx.x - s.blocks, s.extra);
-    launch_dependents();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     for (int d = t; d < SORT_WARPS * s.bins / 4; d += SORT_THREADS) reinterpret_cast<int4*>(counts)[d] = make_int4(0, 0, 0, 0);
     wait_for_primary();
@@ -205,6 +203,36 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     }
 }
 
+template <typename F>
+__global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
+    if (static_cast<int>(blockIdx.x) >= job.shape.blocks)
+        return job.f.beside(job.shape.blocks > 1, blockIdx.x - job.shape.blocks, job.shape.extra);
+    launch_dependents();
+    place_items(job.f, job.shape);
+}
+
+// All digits of so few items that one block sorts them: `first`, then `passes` of `next`.
+constexpr int SORT_PASSES_MAX = 3;
+template <typename F, typename G>
+struct SortAlone {
+    F first;
+    G next[SORT_PASSES_MAX];
+    SortShape shape;
+    int passes;
+};
+template <typename F, typename G>
+__global__ void __launch_bounds__(SORT_THREADS) sort_alone(SortAlone<F, G> job) {
+    if (blockIdx.x > 0) return job.first.beside(0, blockIdx.x - 1, job.shape.extra);
+    launch_dependents();
+    place_items(job.first, job.shape);
+    SortShape later = job.shape;
+    later.bad = nullptr;
+    for (int p = 0; p < job.passes; ++p) {
+        __syncthreads();  // what the last pass has put, and its counters
+        place_items(job.next[p], later);
+    }
+}
+
 // Lets a kernel take `bytes` of dynamic shared memory, out of the largest share
 // of an SM's: kernels that overlap with the one before them need the same
 // division into L1 and shared memory.  Asked once per device.
@@ -241,6 +269,14 @@ lce_status_t sort_by(const F& f, const SortShape& shape, bool first, cudaStream_
         LCE_PROFILED(sort_place<F><<<blocks, SORT_THREADS, sort_smem(shape.bins), s>>>(job));
     else
         LCE_PROFILED(launch_after(sort_place<F>, dim3(blocks), SORT_THREADS, sort_smem(shape.bins), s, job));
+    return LCE_OK;
+}
+
+template <typename F, typename G>
+lce_status_t sort_alone_by(const SortAlone<F, G>& job, cudaStream_t s) {
+    static std::atomic<uint64_t> known{0};
+    if (!allow_smem(&known, sort_alone<F, G>, static_cast<int>(sort_smem(SORT_BINS_MAX)))) return LCE_ERR_CUDA;
+    LCE_PROFILED(sort_alone<F, G><<<static_cast<unsigned>(1 + job.shape.extra), SORT_THREADS, sort_smem(job.shape.bins), s>>>(job));
     return LCE_OK;
 }
 

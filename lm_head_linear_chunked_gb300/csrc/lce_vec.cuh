@@ -159,6 +159,10 @@ __device__ __forceinline__ void load_now(Vec<T, VEC>& v, const Vec<T, VEC>* p) {
         uint32_t u[4];
         asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "l"(p) : "memory");
         __builtin_memcpy(&v, u, 16);
+    } else if constexpr (sizeof(v) == 8) {
+        uint32_t u[2];
+        asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "l"(p) : "memory");
+        __builtin_memcpy(&v, u, 8);
     } else if constexpr (sizeof(v) == 4) {
         uint32_t u;
         asm volatile("ld.global.u32 %0, [%1];" : "=r"(u) : "l"(p) : "memory");
