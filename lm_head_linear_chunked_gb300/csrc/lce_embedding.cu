@@ -128,11 +128,19 @@ __device__ __forceinline__ void clear_bytes(uint8_t* p, int64_t n) {  // by a bl
     for (int64_t i = lead + mid * 16 + 2 * threadIdx.x; i < n; i += 2 * SORT_THREADS) *reinterpret_cast<uint16_t*>(p + i) = 0;
 }
 
+// Piece by piece, side by side with the other blocks: all of them together
+// write one window that moves on (311 MB by 152 blocks: 53 us; a stretch of
+// its own to each block 60).
 __device__ __forceinline__ void clear_share(const Clear& c, int kernel, int64_t block, int64_t of) {
     const int64_t first = c.rows * (c.part + kernel) / c.of, rows = c.rows * (c.part + kernel + 1) / c.of - first;
-    const int64_t r0 = first + rows * block / of, r1 = first + rows * (block + 1) / of;
-    if (c.stride == c.bytes) return clear_bytes(c.at + r0 * c.bytes, (r1 - r0) * c.bytes);
-    for (int64_t r = r0; r < r1; ++r) clear_bytes(c.at + r * c.stride, c.bytes);
+    if (c.stride == c.bytes) {
+        constexpr int64_t PIECE = 64 * SORT_THREADS;
+        uint8_t* p = c.at + first * c.bytes;
+        const int64_t n = rows * c.bytes;
+        for (int64_t i = block * PIECE; i < n; i += of * PIECE) clear_bytes(p + i, n - i < PIECE ? n - i : PIECE);
+    } else {
+        for (int64_t r = block; r < rows; r += of) clear_bytes(c.at + (first + r) * c.stride, c.bytes);
+    }
 }
 
 struct SortItem {
@@ -197,7 +205,6 @@ struct NextDigit {
 };
 
 constexpr int EMB_CHUNK = 32;       // sorted tokens of a warp
-constexpr int EMB_ZERO_ROWS = 8;    // vocabulary rows of a warp that looks for rows to clear
 
 template <typename T>
 struct EmbBwd {
@@ -215,6 +222,7 @@ struct EmbBwd {
     int32_t H, slabs;
     int32_t split;    // warps to a chunk and slab
     int32_t joining;  // blocks of the last kernel that add pieces up
+    int32_t clear_rows;  // vocabulary rows of a warp of the others
 };
 
 // A lane's share of a row's slab: ITEMS vectors, 32 vectors apart, as pairs of FP32 sums.
@@ -379,9 +387,9 @@ __global__ void __launch_bounds__(256) emb_finish(EmbBwd<float> a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_primary();
     if (static_cast<int>(blockIdx.x) >= a.joining) {
-        const int64_t v0 = ((static_cast<int64_t>(blockIdx.x) - a.joining) * 8 + warp) * EMB_ZERO_ROWS;
-        const unsigned named = __ballot_sync(0xFFFFFFFFu, lane >= EMB_ZERO_ROWS || v0 + lane >= a.V || a.named[v0 + lane]);
-        for (int j = 0; j < EMB_ZERO_ROWS; ++j) {
+        const int64_t v0 = ((static_cast<int64_t>(blockIdx.x) - a.joining) * 8 + warp) * a.clear_rows;
+        const unsigned named = __ballot_sync(0xFFFFFFFFu, lane >= a.clear_rows || v0 + lane >= a.V || a.named[v0 + lane]);
+        for (int j = 0; j < a.clear_rows; ++j) {
             if (named >> j & 1) continue;
             using Z = Vec<W, CLEAR_VEC>;
             Z* out = reinterpret_cast<Z*>(static_cast<W*>(a.dw) + (v0 + j) * a.lddw);
@@ -484,11 +492,16 @@ size_t emb_space(int64_t N, int64_t V, int64_t H, EmbSpace* e, void* ws) {
 
 // Whether all of the gradient's rows are cleared while the tokens are sorted, on
 // the SMs that the sort leaves idle: where the tokens are so few that they name
-// few rows (16384 tokens, 151936 rows of 1024: 86 us against 92).  Else the
-// rows that no token names are cleared at the end.  (131072 tokens, rows of
-// 4096: clearing a part of them early, 64 MB, gained 1%, 256 MB lost 2%.)
+// few rows, and where what the sort hides is more than the few blocks beside
+// it lose against many short ones.  Else the rows that no token names are
+// cleared at the end.  Early and late: 16384 tokens, 151936 rows of 1024 bf16
+// 72.2 and 78.5 us; 64 and 32768 of 1024 18.6 and 26.8; 4096 and 151936 of 2048
+// 111 and 115, of 4096 212 and 198.
 constexpr int64_t EMB_CLEAR_RATIO = 4;  // vocabulary rows to a token
-bool emb_early(int64_t N, int64_t V) { return sort_blocks(N) <= SORT_BLOCKS / 2 && N <= V / EMB_CLEAR_RATIO; }
+constexpr int64_t EMB_CLEAR_BYTES = 512ll << 20;
+bool emb_early(int64_t N, int64_t V, int64_t bytes) {
+    return sort_blocks(N) <= SORT_BLOCKS / 2 && N <= V / EMB_CLEAR_RATIO && bytes <= EMB_CLEAR_BYTES;
+}
 
 // The sorted tokens: their place in e.keys and e.rows.
 lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int64_t padding, bool name, Clear clear,
@@ -594,7 +607,12 @@ lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
     j.add = a.add;
     j.H = a.H;
     j.slabs = emb_slabs(a.H / JVEC, JITEMS);
-    const int64_t most = (a.chunks - 1) * j.slabs, clearing = a.named ? (a.V + 8 * EMB_ZERO_ROWS - 1) / (8 * EMB_ZERO_ROWS) : 0;
+    // about 8 KB to a warp: many short blocks write faster than few long ones (131072 tokens, rows of 4096 bf16: 389 us
+    // with one row to a warp, 401 with eight)
+    const int64_t some = 8192 / (a.H * static_cast<int64_t>(sizeof(W)));
+    j.clear_rows = static_cast<int32_t>(some < 1 ? 1 : some < 8 ? some : 8);
+    const int64_t most = (a.chunks - 1) * j.slabs, clearing = a.named ? (a.V + 8 * j.clear_rows - 1) / (8 * j.clear_rows) : 0;
+    if (most + clearing > INT32_MAX) return LCE_ERR_UNSUPPORTED;
     j.joining = static_cast<int32_t>(most < 1216 ? most : 1216);
     if (j.joining + clearing == 0) return LCE_OK;
     LCE_PROFILED(launch_after(finish, dim3(static_cast<unsigned>(j.joining + clearing)), 256, 0, s, j));
@@ -664,7 +682,7 @@ lce_status_t lce_embedding_backward(int64_t N, int64_t V, int64_t H, int dtype, 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int where = 0;
     const int64_t size = static_cast<int64_t>(dtype_bytes(gtype));
-    const bool early = !add && emb_early(N, V), late = !add && !early;
+    const bool early = !add && emb_early(N, V, V * H * size), late = !add && !early;
     const Clear clear{static_cast<uint8_t*>(grad_weight), early ? V : 0, H * size, ldgw * size, 0, 1};
     const lce_status_t sorted = emb_sort(N, V, tokens, index_bytes == 8, padding_token, late, clear, e, &where, s);
     if (sorted != LCE_OK) return sorted;
@@ -672,7 +690,7 @@ lce_status_t lce_embedding_backward(int64_t N, int64_t V, int64_t H, int dtype, 
         using T = decltype(t);
         const EmbBwd<T> a{static_cast<const T*>(grad_y), ldg, N, V, scale, e.keys[where], e.rows[where],
                           late ? e.named : nullptr, e.n_spans, e.spans,
-                          e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, static_cast<int32_t>(H), 0, 1, 0};
+                          e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, static_cast<int32_t>(H), 0, 1, 0, 0};
         return gtype == LCE_F32 ? emb_gradient<T, float>(a, s) : emb_gradient<T, T>(a, s);
     });
 }
