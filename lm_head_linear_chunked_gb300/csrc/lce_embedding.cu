@@ -38,6 +38,7 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, bool idx64, int6
 template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) emb_fwd_wide(EmbFwd<T> a) {
     using V = Vec<T, VEC>;
+    wait_for_primary();
     const int n = a.H / VEC, parts = (n + 32 * U - 1) / (32 * U), lane = threadIdx.x & 31;
     const int64_t item = blockIdx.x * 8ll + (threadIdx.x >> 5), i = item / parts;
     if (i >= a.N) return;
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(256) emb_fwd_wide(EmbFwd<T> a) {
 template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) emb_fwd_narrow(EmbFwd<T> a) {
     using V = Vec<T, VEC>;
+    wait_for_primary();
     const Dealt<U> mine(a.deal, blockIdx.x);
     V x[U];
     uint32_t at[U];
@@ -529,11 +531,11 @@ lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int6
     }
     clear.of = 2 * d.passes;  // a share for each kernel
     first.clear = clear;
-    lce_status_t st = sort_by(first, shape, true, s);
+    lce_status_t st = sort_by(first, shape, s);
     shape.bad = nullptr;
     for (int p = 1; p < d.passes && st == LCE_OK; ++p) {
         clear.part = 2 * p;
-        st = sort_by(next(p), shape, false, s);
+        st = sort_by(next(p), shape, s);
     }
     return st;
 }
@@ -559,9 +561,9 @@ lce_status_t emb_lookup(EmbFwd<T> a, cudaStream_t s) {
         const int64_t blocks = ((enough ? wide : a.N * ((n + 31) / 32)) + 7) / 8;
         if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
         if (enough)
-            LCE_PROFILED(emb_fwd_wide<T, VEC, U><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+            LCE_PROFILED(launch_after(emb_fwd_wide<T, VEC, U>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a));
         else
-            LCE_PROFILED(emb_fwd_wide<T, VEC, 1><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+            LCE_PROFILED(launch_after(emb_fwd_wide<T, VEC, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a));
         return LCE_OK;
     }
     const int64_t vectors = a.N * n;
@@ -570,9 +572,9 @@ lce_status_t emb_lookup(EmbFwd<T> a, cudaStream_t s) {
     if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
     a.deal = deal_of(n);
     if (enough)
-        LCE_PROFILED(emb_fwd_narrow<T, VEC, 4><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+        LCE_PROFILED(launch_after(emb_fwd_narrow<T, VEC, 4>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a));
     else
-        LCE_PROFILED(emb_fwd_narrow<T, VEC, 1><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a));
+        LCE_PROFILED(launch_after(emb_fwd_narrow<T, VEC, 1>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a));
     return LCE_OK;
 }
 

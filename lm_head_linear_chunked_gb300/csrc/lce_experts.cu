@@ -105,6 +105,7 @@ __device__ __forceinline__ void clear_rows(const MoveArgs& a, int64_t r0) {
 template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) expert_spread(MoveArgs a) {
     using V = Vec<T, VEC>;
+    wait_for_primary();
     const int lane = threadIdx.x & 31, n = a.H / VEC, parts = (n + 32 * U - 1) / (32 * U);
     if (static_cast<int>(blockIdx.x) < a.clearing) return clear_rows<T, VEC>(a, (blockIdx.x * 8ll + (threadIdx.x >> 5)) * EXPERT_CLEAR);
     const uint32_t item = (blockIdx.x - a.clearing) * 8u + (threadIdx.x >> 5);
@@ -133,6 +134,7 @@ template <typename T, int VEC, int U, int BATCH>
 __global__ void __launch_bounds__(256) expert_join(MoveArgs a) {
     using Row = RowVectors<T, VEC, U>;
     using V = Vec<T, VEC>;
+    wait_for_primary();
     const int lane = threadIdx.x & 31, n = a.H / VEC, parts = (n + 32 * U - 1) / (32 * U);
     const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5);
     if (item >= static_cast<uint32_t>(a.T) * parts) return;
@@ -187,6 +189,7 @@ __device__ __forceinline__ int64_t slot_row(const MoveArgs& a, int64_t slot) {
 template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) expert_spread_narrow(MoveArgs a) {
     using V = Vec<T, VEC>;
+    wait_for_primary();
     if (static_cast<int>(blockIdx.x) < a.clearing) return clear_rows<T, VEC>(a, (blockIdx.x * 8ll + (threadIdx.x >> 5)) * EXPERT_CLEAR);
     const Dealt<U> mine(a.deal, blockIdx.x - a.clearing);
     V v[U];
@@ -210,6 +213,7 @@ template <typename T, int VEC, int U, int BATCH>
 __global__ void __launch_bounds__(256) expert_join_narrow(MoveArgs a) {
     using Row = RowVectors<T, VEC, U>;
     using V = Vec<T, VEC>;
+    wait_for_primary();
     const Dealt<U> mine(a.deal, blockIdx.x);
     uint32_t at[U];
     int64_t t[U];
@@ -262,6 +266,7 @@ __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
     static_assert(BATCH <= LANES);
     constexpr unsigned ALL = 0xFFFFFFFFu;
     __shared__ float part[8][BATCH];
+    wait_for_primary();
     const int lane = threadIdx.x & (LANES - 1), warp = threadIdx.x >> 5, n = a.H / VEC;
     if (static_cast<int>(blockIdx.x) < a.clearing) return clear_rows<T, VEC>(a, (blockIdx.x * 8ll + warp) * EXPERT_CLEAR);
     const int64_t block = static_cast<int64_t>(blockIdx.x) - a.clearing;
@@ -441,36 +446,36 @@ lce_status_t move_as(MoveArgs a, Move what, cudaStream_t s) {
         if constexpr (V16) {
             if (lanes < 32) {
                 if (lanes == 16)
-                    LCE_PROFILED(expert_join_bwd<T, VEC, BWD, 4, 16><<<grid, 256, 0, s>>>(a));
+                    LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, 4, 16>, dim3(grid), 256, 0, s, a));
                 else
-                    LCE_PROFILED(expert_join_bwd<T, VEC, BWD, 4, 8><<<grid, 256, 0, s>>>(a));
+                    LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, 4, 8>, dim3(grid), 256, 0, s, a));
                 return LCE_OK;
             }
             if (a.k > 4) {
-                LCE_PROFILED(expert_join_bwd<T, VEC, BWD, BATCH, 32><<<grid, 256, 0, s>>>(a));
+                LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, BATCH, 32>, dim3(grid), 256, 0, s, a));
                 return LCE_OK;
             }
         }
-        LCE_PROFILED(expert_join_bwd<T, VEC, BWD, 4, 32><<<grid, 256, 0, s>>>(a));
+        LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, 4, 32>, dim3(grid), 256, 0, s, a));
     } else if (what == Move::JOIN) {
         if constexpr (V16) {
             if (narrow) {
-                LCE_PROFILED(expert_join_narrow<T, VEC, JOIN, BATCH><<<grid, 256, 0, s>>>(a));
+                LCE_PROFILED(launch_after(expert_join_narrow<T, VEC, JOIN, BATCH>, dim3(grid), 256, 0, s, a));
                 return LCE_OK;
             }
         }
-        LCE_PROFILED(expert_join<T, VEC, JOIN, BATCH><<<grid, 256, 0, s>>>(a));
+        LCE_PROFILED(launch_after(expert_join<T, VEC, JOIN, BATCH>, dim3(grid), 256, 0, s, a));
     } else {
         if constexpr (V16) {
             if (narrow) {
-                LCE_PROFILED(expert_spread_narrow<T, VEC, JOIN><<<grid, 256, 0, s>>>(a));
+                LCE_PROFILED(launch_after(expert_spread_narrow<T, VEC, JOIN>, dim3(grid), 256, 0, s, a));
                 return LCE_OK;
             }
         }
         if (wide)
-            LCE_PROFILED(expert_spread<T, VEC, WIDE><<<grid, 256, 0, s>>>(a));
+            LCE_PROFILED(launch_after(expert_spread<T, VEC, WIDE>, dim3(grid), 256, 0, s, a));
         else
-            LCE_PROFILED(expert_spread<T, VEC, NARROW><<<grid, 256, 0, s>>>(a));
+            LCE_PROFILED(launch_after(expert_spread<T, VEC, NARROW>, dim3(grid), 256, 0, s, a));
     }
     return LCE_OK;
 }
@@ -519,7 +524,7 @@ lce_status_t lce_expert_plan(int64_t T, int64_t k, int64_t E, int64_t align, con
     if (ws_bytes < plan_space(T, k, E, &shape, ws)) return LCE_ERR_WORKSPACE;
     const PlanArgs a{experts, index_bytes == 8, mask, static_cast<int32_t>(E), static_cast<int32_t>(k), static_cast<int32_t>(align),
                      positions, slots, counts, offsets, static_cast<int32_t>(rows), &static_cast<WsHeader*>(ws)->status};
-    return sort_by(a, shape, true, reinterpret_cast<cudaStream_t>(stream));
+    return sort_by(a, shape, reinterpret_cast<cudaStream_t>(stream));
 }
 
 lce_status_t lce_expert_dispatch(int64_t T, int64_t k, int64_t H, int64_t R, int dtype, const void* x, int64_t ldx,

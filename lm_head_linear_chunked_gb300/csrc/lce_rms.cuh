@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) rms_fwd_rows(RmsFwd<T>
     constexpr int PAIRS = Row::PAIRS;
     __shared__ float part[2][R][MAX_WARPS], most[2][R][MAX_WARPS];
     extern __shared__ __align__(16) uint8_t dyn[];
+    wait_for_primary();
     const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, warps = threads >> 5, lane = t & 31;
     const int n = a.H / VEC;
     const float inv = 1.f / static_cast<float>(a.H);
@@ -308,6 +309,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) rms_fwd_rows(RmsFwd<T>
 template <typename T, bool QUANT>
 __global__ void __launch_bounds__(512) rms_fwd_any(RmsFwd<T> a) {
     __shared__ float part[2][32];
+    wait_for_primary();
     const int64_t r = blockIdx.x;
     const T* x = a.x + r * a.ldx;
     float s = 0.f;
@@ -383,6 +385,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) rms_bwd_rows(RmsBwd<T> a) {
     constexpr bool RING = sizeof(V) >= 4;  // single 16-bit elements wait in registers
     static_assert(KEEP || RING, "the rows are read again from the ring");
     launch_dependents();
+    wait_for_primary();
     const int tpr = WARP ? 32 : blockDim.x;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
@@ -526,6 +529,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) rms_bwd_rows(RmsBwd<T> a) {
 template <typename T>
 __global__ void __launch_bounds__(512) rms_dx_any(RmsBwd<T> a) {
     __shared__ float part[32];
+    wait_for_primary();
     const int64_t r = blockIdx.x;
     const T* x = a.x + r * a.ldx;
     const T* dy = a.dy + r * a.ldd;
@@ -547,6 +551,7 @@ __global__ void __launch_bounds__(512) rms_dx_any(RmsBwd<T> a) {
 template <typename T>
 __global__ void __launch_bounds__(256) rms_dw_any(RmsBwd<T> a) {
     __shared__ float sw[8][33];
+    wait_for_primary();
     const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + c;
     const int64_t r0 = blockIdx.y * a.rows_per_part;
@@ -572,7 +577,7 @@ lce_status_t rms_rows(const RmsFwd<T>& a, cudaStream_t s) {
     const size_t vec = sizeof(Vec<T, VEC>), smem = vec >= 4 ? (a.r ? 2 : 1) * static_cast<size_t>(STAGES) * R * ITEMS * threads * vec : 0;
     const int64_t most = resident_blocks(&memo, kernel, threads, smem), groups = (a.rows + R - 1) / R;
     if (most <= 0) return LCE_ERR_CUDA;
-    LCE_PROFILED(kernel<<<static_cast<unsigned>(groups < most ? groups : most), threads, smem, s>>>(a));
+    LCE_PROFILED(launch_after(kernel, dim3(static_cast<unsigned>(groups < most ? groups : most)), threads, smem, s, a));
     return LCE_OK;
 }
 
@@ -599,7 +604,7 @@ lce_status_t rms_forward_as(const RmsCall& c, const RmsFwd<T>& a) {
     if (V4 > 1 && fits(V4) && c.H / V4 <= 4096) return rms_rows<T, W, V4, 8, 1, 3, 16, 1, QUANT>(a, s);
     if (c.H <= 4096) return rms_rows<T, W, 1, 8, 1, 3, 16, 1, QUANT>(a, s);
     if (c.H <= 8192) return rms_rows<T, W, 1, 16, 1, 3, 16, 1, QUANT>(a, s);
-    LCE_PROFILED(rms_fwd_any<T, QUANT><<<static_cast<unsigned>(c.rows), 512, 0, s>>>(a));
+    LCE_PROFILED(launch_after(rms_fwd_any<T, QUANT>, dim3(static_cast<unsigned>(c.rows)), 512, 0, s, a));
     return LCE_OK;
 }
 
@@ -624,7 +629,7 @@ lce_status_t rms_bwd(const RmsBwd<T>& a, int* parts, cudaStream_t s) {
     if (blocks > work) blocks = work;
     if (blocks > NORM_PARTS) blocks = NORM_PARTS;
     *parts = static_cast<int>(blocks);
-    LCE_PROFILED(kernel<<<static_cast<unsigned>(blocks), threads, smem, s>>>(a));
+    LCE_PROFILED(launch_after(kernel, dim3(static_cast<unsigned>(blocks)), threads, smem, s, a));
     return LCE_OK;
 }
 
@@ -655,12 +660,12 @@ lce_status_t rms_backward(const RmsCall& c) {
     } else if (c.H <= 8192) {
         st = rms_bwd<T, W, 1, 16, false, true>(a, &parts, s);
     } else {
-        if (c.y) LCE_PROFILED(rms_dx_any<T><<<static_cast<unsigned>(c.rows), 512, 0, s>>>(a));
+        if (c.y) LCE_PROFILED(launch_after(rms_dx_any<T>, dim3(static_cast<unsigned>(c.rows)), 512, 0, s, a));
         if (c.dw) {
             a.rows_per_part = (c.rows + NORM_PARTS - 1) / NORM_PARTS;
             if (a.rows_per_part < 32) a.rows_per_part = 32;
             parts = static_cast<int>((c.rows + a.rows_per_part - 1) / a.rows_per_part);
-            LCE_PROFILED(rms_dw_any<T><<<dim3((c.H + 31) / 32, parts), 256, 0, s>>>(a));
+            LCE_PROFILED(launch_after(rms_dw_any<T>, dim3((c.H + 31) / 32, parts), 256, 0, s, a));
         }
     }
     if (st != LCE_OK || !c.dw) return st;

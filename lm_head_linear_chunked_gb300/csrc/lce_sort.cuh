@@ -81,7 +81,10 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count(SortJob<F> job) {
     const F& f = job.f;
     const SortShape& s = job.shape;
     extern __shared__ __align__(16) int32_t counts[];
-    if (static_cast<int>(blockIdx.x) >= s.blocks) return f.beside(0, blockIdx.x - s.blocks, s.extra);
+    if (static_cast<int>(blockIdx.x) >= s.blocks) {
+        wait_for_primary();
+        return f.beside(0, blockIdx.x - s.blocks, s.extra);
+    }
     launch_dependents();
     for (int d = threadIdx.x; d < s.bins; d += SORT_THREADS) counts[d] = 0;
     wait_for_primary();
@@ -205,8 +208,10 @@ __device__ __forceinline__ void place_items(const F& f, const SortShape& s) {
 
 template <typename F>
 __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
-    if (static_cast<int>(blockIdx.x) >= job.shape.blocks)
+    if (static_cast<int>(blockIdx.x) >= job.shape.blocks) {
+        wait_for_primary();
         return job.f.beside(job.shape.blocks > 1, blockIdx.x - job.shape.blocks, job.shape.extra);
+    }
     launch_dependents();
     place_items(job.f, job.shape);
 }
@@ -222,7 +227,10 @@ struct SortAlone {
 };
 template <typename F, typename G>
 __global__ void __launch_bounds__(SORT_THREADS) sort_alone(SortAlone<F, G> job) {
-    if (blockIdx.x > 0) return job.first.beside(0, blockIdx.x - 1, job.shape.extra);
+    if (blockIdx.x > 0) {
+        wait_for_primary();
+        return job.first.beside(0, blockIdx.x - 1, job.shape.extra);
+    }
     launch_dependents();
     place_items(job.first, job.shape);
     SortShape later = job.shape;
@@ -249,26 +257,18 @@ bool allow_smem(std::atomic<uint64_t>* known, K kernel, int bytes) {
     return true;
 }
 
-// Sorts by one digit; `first`: after all that came before it in the stream,
-// else under the kernel before it, whose results it waits for.
+// Sorts by one digit.
 template <typename F>
-lce_status_t sort_by(const F& f, const SortShape& shape, bool first, cudaStream_t s) {
+lce_status_t sort_by(const F& f, const SortShape& shape, cudaStream_t s) {
     static std::atomic<uint64_t> counts{0}, places{0};
     if (!allow_smem(&counts, sort_count<F>, SORT_BINS_MAX * 4) ||
         !allow_smem(&places, sort_place<F>, static_cast<int>(sort_smem(SORT_BINS_MAX))))
         return LCE_ERR_CUDA;
     const SortJob<F> job{f, shape};
-    const unsigned blocks = static_cast<unsigned>(shape.blocks + shape.extra);
-    if (shape.blocks > 1) {
-        if (first)
-            LCE_PROFILED(sort_count<F><<<blocks, SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s>>>(job));
-        else
-            LCE_PROFILED(launch_after(sort_count<F>, dim3(blocks), SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s, job));
-    }
-    if (shape.blocks == 1 && first)
-        LCE_PROFILED(sort_place<F><<<blocks, SORT_THREADS, sort_smem(shape.bins), s>>>(job));
-    else
-        LCE_PROFILED(launch_after(sort_place<F>, dim3(blocks), SORT_THREADS, sort_smem(shape.bins), s, job));
+    const dim3 blocks(static_cast<unsigned>(shape.blocks + shape.extra));
+    if (shape.blocks > 1)
+        LCE_PROFILED(launch_after(sort_count<F>, blocks, SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s, job));
+    LCE_PROFILED(launch_after(sort_place<F>, blocks, SORT_THREADS, sort_smem(shape.bins), s, job));
     return LCE_OK;
 }
 
@@ -276,7 +276,7 @@ template <typename F, typename G>
 lce_status_t sort_alone_by(const SortAlone<F, G>& job, cudaStream_t s) {
     static std::atomic<uint64_t> known{0};
     if (!allow_smem(&known, sort_alone<F, G>, static_cast<int>(sort_smem(SORT_BINS_MAX)))) return LCE_ERR_CUDA;
-    LCE_PROFILED(sort_alone<F, G><<<static_cast<unsigned>(1 + job.shape.extra), SORT_THREADS, sort_smem(job.shape.bins), s>>>(job));
+    LCE_PROFILED(launch_after(sort_alone<F, G>, dim3(static_cast<unsigned>(1 + job.shape.extra)), SORT_THREADS, sort_smem(job.shape.bins), s, job));
     return LCE_OK;
 }
 

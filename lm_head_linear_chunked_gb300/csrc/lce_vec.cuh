@@ -237,8 +237,9 @@ __device__ __forceinline__ void copy_async_wait() {
 // A kernel that reads what the one before it in the stream wrote, launched
 // while that one still runs: its blocks may start once every block of the first
 // has called launch_dependents() or ended, and wait_for_primary() returns when
-// the first has ended and its writes are visible.  The first is launched the
-// usual way, after all that came before it.
+// the first has ended and its writes are visible.  Every kernel of a chain waits
+// before it touches memory, or comes first and is launched the usual way, so
+// what came before the first is over as well.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
