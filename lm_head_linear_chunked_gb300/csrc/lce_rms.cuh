@@ -581,6 +581,13 @@ lce_status_t rms_rows(const RmsFwd<T>& a, cudaStream_t s) {
     return LCE_OK;
 }
 
+// The forward's form by the row's width in vectors: 16 bytes where rows start on
+// such boundaries (up to 128 a warp per row with the next rows copied ahead, up
+// to 512 a block with four a thread, or two rows of two where a quarter of such
+// a block would be idle, up to 2048 wider blocks), else 4 bytes, else one
+// element.  Measured with a residual: 32768 x 4096 bf16 to 8 bits 154 us, 0.90
+// of the copy rate (two or four stages of the ring 168 and 156, eight warps
+// 157), 16384 x 1024 bf16 18.6 us, within the copy rate as its writes stay in L2.
 template <typename T, typename W, bool QUANT>
 lce_status_t rms_forward_as(const RmsCall& c, const RmsFwd<T>& a) {
     cudaStream_t s = c.s;
@@ -616,6 +623,13 @@ lce_status_t rms_forward(const RmsCall& c) {
     return c.q ? rms_forward_as<T, W, true>(c, a) : rms_forward_as<T, W, false>(c, a);
 }
 
+// The backward's form by the row's width, as layer norm's (lce_norm.cuh): up to
+// 128 16-byte vectors a warp per row, up to 1024 a block with two vectors a
+// thread, up to 2048 with four, read twice from the ring; narrower vectors eight
+// a thread, a warp per row where that covers it (30000 x 250 bf16: 26 us, a
+// block per row 54), or sixteen single elements; wider rows are read again.
+// Measured with the sum's gradient: 16384 x 1024 bf16 27 us (the copy rate
+// would be 20), 65536 x 2560 without it 155 us (148).
 template <typename T, typename W, int VEC, int ITEMS, bool WARP, bool KEEP>
 lce_status_t rms_bwd(const RmsBwd<T>& a, int* parts, cudaStream_t s) {
     static Resident memo;
@@ -654,9 +668,9 @@ lce_status_t rms_backward(const RmsCall& c) {
              : n <= 1024 ? rms_bwd<T, W, V, 2, false, true>(a, &parts, s)
                          : rms_bwd<T, W, V, 4, false, false>(a, &parts, s);
     } else if (V4 > 1 && fits(V4) && c.H / V4 <= 4096) {
-        st = rms_bwd<T, W, V4, 8, false, true>(a, &parts, s);
+        st = c.H / V4 <= 256 ? rms_bwd<T, W, V4, 8, true, true>(a, &parts, s) : rms_bwd<T, W, V4, 8, false, true>(a, &parts, s);
     } else if (c.H <= 4096) {
-        st = rms_bwd<T, W, 1, 8, false, true>(a, &parts, s);
+        st = c.H <= 256 ? rms_bwd<T, W, 1, 8, true, true>(a, &parts, s) : rms_bwd<T, W, 1, 8, false, true>(a, &parts, s);
     } else if (c.H <= 8192) {
         st = rms_bwd<T, W, 1, 16, false, true>(a, &parts, s);
     } else {
