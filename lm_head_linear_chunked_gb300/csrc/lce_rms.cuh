@@ -102,12 +102,28 @@ __device__ __forceinline__ int rms_at(int i, int warp, int warps, int lane) {
     return ((i / S * warps + warp) * S + i % S) * 32 + lane;
 }
 
-// The forward: a block (for narrow rows a warp) takes R rows at a time and
+// The sum (largest) over each LANES neighbouring lanes of a warp.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_max_nan(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+// The forward: a block (for narrow rows a warp, or LANES of its lanes) takes R rows at a time and
 // copies the next ones ahead, each thread its own vectors, so that only the
 // sums over a row wait for the other warps.  The row stays in registers
 // between its sum and the output.
-template <typename T, typename W, int VEC, int ITEMS, int R, int STAGES, int MAX_WARPS, int BLOCKS, bool QUANT>
+template <typename T, typename W, int VEC, int ITEMS, int R, int STAGES, int MAX_WARPS, int BLOCKS, bool QUANT, int LANES>
 __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) rms_fwd_rows(RmsFwd<T> a) {
+    constexpr int PER = R * 32 / LANES;  // rows of a block at a time
+    static_assert(LANES == 32 || (R == 1 && MAX_WARPS == 1 && ITEMS == 1 && VEC >= 4 && LANES * VEC <= LCE_FP8_GROUP));
     constexpr bool RING = sizeof(Vec<T, VEC>) >= 4;  // single 16-bit elements wait in registers
     static_assert(RING || R == 1, "the next row waits in registers");
     using Row = RowRegs<T, VEC, ITEMS>;
@@ -116,21 +132,22 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) rms_fwd_rows(RmsFwd<T>
     __shared__ float part[2][R][MAX_WARPS], most[2][R][MAX_WARPS];
     extern __shared__ __align__(16) uint8_t dyn[];
     wait_for_primary();
-    const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, warps = threads >> 5, lane = t & 31;
+    const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, warps = threads >> 5, lane = t & (LANES - 1);
+    const int sub = LANES < 32 ? t / LANES : 0;  // the row of a warp that takes several
     const int n = a.H / VEC;
     const float inv = 1.f / static_cast<float>(a.H);
     V* ring = reinterpret_cast<V*>(dyn);  // [STAGES][R][x, r][ITEMS][threads]
     const int mats = a.r ? 2 : 1;
-    const int64_t groups = (a.rows + R - 1) / R;
+    const int64_t groups = (a.rows + PER - 1) / PER;
     auto slot = [&](int stage, int k, int m, int i) { return ring + (((stage * R + k) * mats + m) * ITEMS + i) * threads + t; };
     auto copy_group = [&](int64_t g, int stage) {
         if constexpr (RING) {
             if (g < groups)
 #pragma unroll
                 for (int k = 0; k < R; ++k)
-                    if (g * R + k < a.rows) {
-                        const V* x = reinterpret_cast<const V*>(a.x + (g * R + k) * a.ldx);
-                        const V* r = reinterpret_cast<const V*>(a.r + (g * R + k) * a.ldr);
+                    if (g * PER + k + sub < a.rows) {
+                        const V* x = reinterpret_cast<const V*>(a.x + (g * PER + k + sub) * a.ldx);
+                        const V* r = reinterpret_cast<const V*>(a.r + (g * PER + k + sub) * a.ldr);
 #pragma unroll
                         for (int i = 0; i < ITEMS; ++i) {
                             const int at = rms_at<VEC>(i, warp, warps, lane);
@@ -177,7 +194,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) rms_fwd_rows(RmsFwd<T>
         float q[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int64_t row = g * R + k;
+            const int64_t row = g * PER + k + sub;
             Row x, r;
             if constexpr (RING) {
 #pragma unroll
@@ -211,7 +228,7 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) rms_fwd_rows(RmsFwd<T>
         }
         if (++stage == STAGES) stage = 0;
 #pragma unroll
-        for (int k = 0; k < R; ++k) q[k] = warp_sum(q[k]);
+        for (int k = 0; k < R; ++k) q[k] = lanes_sum<LANES>(q[k]);
         if constexpr (MAX_WARPS > 1) {
 #pragma unroll
             for (int k = 0; k < R; ++k)
@@ -237,8 +254,8 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) rms_fwd_rows(RmsFwd<T>
                 if (a.w) d[k][p] = mul2(d[k][p], w.pair(p));
                 if constexpr (QUANT) amax[k] = max_nan(amax[k], max_nan(fabsf(lo(d[k][p])), fabsf(hi(d[k][p]))));
             }
-            const int64_t row = g * R + k;
-            if (t == 0 && a.rstd && row < a.rows) a.rstd[row] = rstd;
+            const int64_t row = g * PER + k + sub;
+            if (warp == 0 && lane == 0 && a.rstd && row < a.rows) a.rstd[row] = rstd;
             if constexpr (!QUANT) {
                 if (row >= a.rows) break;
                 Row o;
@@ -248,11 +265,11 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) rms_fwd_rows(RmsFwd<T>
             }
         }
         if constexpr (QUANT) {
-            const bool one = a.groups == 1;
+            const bool one = LANES < 32 || a.groups == 1;
             if (one) {
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
-                    amax[k] = warp_max_nan(amax[k]);
+                    amax[k] = lanes_max_nan<LANES>(amax[k]);
                     if (MAX_WARPS > 1 && lane == 0) most[flip][k][warp] = amax[k];
                 }
                 if constexpr (MAX_WARPS > 1) {
@@ -263,25 +280,25 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, BLOCKS) rms_fwd_rows(RmsFwd<T>
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                const int64_t row = g * R + k;
+                const int64_t row = g * PER + k + sub;
                 if (row >= a.rows) break;
                 float scale = group_scale(amax[k]), by = 1.f / scale;
-                if (one && t == 0) a.scales[row] = scale;
-                constexpr int S = VEC >= 4 ? 1 : LCE_FP8_GROUP / 32 / VEC, LANES = VEC >= 4 ? LCE_FP8_GROUP / VEC : 32;
+                if (one && warp == 0 && lane == 0) a.scales[row] = scale;
+                constexpr int S = VEC >= 4 ? 1 : LCE_FP8_GROUP / 32 / VEC, GROUP = VEC >= 4 ? LCE_FP8_GROUP / VEC : 32;
                 constexpr int PER = VEC == 1 ? 1 : VEC / 2;  // pairs of a vector (with single elements half of one)
 #pragma unroll
                 for (int i = 0; i < ITEMS; ++i) {
-                    if (!one && i % S == 0) {
+                    if (LANES == 32 && !one && i % S == 0) {
                         float m = 0.f;
 #pragma unroll
                         for (int e = i * VEC; e < (i + S) * VEC; ++e)
                             m = max_nan(m, fabsf(e & 1 ? hi(d[k][e / 2]) : lo(d[k][e / 2])));
 #pragma unroll
-                        for (int o = LANES / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                        for (int o = GROUP / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
                         scale = group_scale(m);
                         by = 1.f / scale;
                         const int at = rms_at<VEC>(i, warp, warps, lane);
-                        if ((lane & (LANES - 1)) == 0 && at < n) a.scales[row * a.groups + at * VEC / LCE_FP8_GROUP] = scale;
+                        if ((lane & (GROUP - 1)) == 0 && at < n) a.scales[row * a.groups + at * VEC / LCE_FP8_GROUP] = scale;
                     }
                     const int at = rms_at<VEC>(i, warp, warps, lane);
                     if (at >= n) continue;
@@ -375,8 +392,10 @@ struct RmsBwd {
 // only for the sum over a row.  KEEP: xh and g stay in registers between the
 // sum and dx; without it they are computed again from the ring, for the widest
 // rows, whose ds has no room in the ring and is read when it is added.
-template <typename T, typename W, int VEC, int ITEMS, bool WARP, bool KEEP>
+template <typename T, typename W, int VEC, int ITEMS, bool WARP, bool KEEP, int LANES>
 __global__ void __launch_bounds__(WARP ? 128 : 512) rms_bwd_rows(RmsBwd<T> a) {
+    static_assert(LANES == 32 || (WARP && ITEMS == 1 && VEC > 1));
+    constexpr int PER = 32 / LANES;  // rows of a warp at a time
     constexpr int STAGES = RMS_BWD_STAGES;
     __shared__ float part[2][16];
     extern __shared__ __align__(16) uint8_t dyn[];  // the ring, then (WARP) the sums of the columns
@@ -386,14 +405,14 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) rms_bwd_rows(RmsBwd<T> a) {
     static_assert(KEEP || RING, "the rows are read again from the ring");
     launch_dependents();
     wait_for_primary();
-    const int tpr = WARP ? 32 : blockDim.x;
-    const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int tpr = WARP ? LANES : blockDim.x;
+    const int t = WARP ? threadIdx.x & (LANES - 1) : threadIdx.x;
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     const int n = a.H / VEC, mats = KEEP && a.ds ? 3 : 2;
-    const int64_t step = WARP ? gridDim.x * 4ll : gridDim.x;
+    const int64_t step = WARP ? gridDim.x * 4ll * PER : gridDim.x;
     const float inv = 1.f / static_cast<float>(a.H);
     V* ring = reinterpret_cast<V*>(dyn);  // [STAGES][x, dy, ds][ITEMS][threads]
-    const int64_t r0 = WARP ? blockIdx.x * 4ll + warp : blockIdx.x;
+    const int64_t r0 = WARP ? (blockIdx.x * 4ll + warp) * PER + lane / LANES : blockIdx.x;
     auto slot = [&](int stage, int m, int i) { return ring + ((stage * mats + m) * ITEMS + i) * blockDim.x + threadIdx.x; };
     auto copy_row = [&](int64_t r, int stage) {
         if constexpr (RING) {
@@ -429,15 +448,17 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) rms_bwd_rows(RmsBwd<T> a) {
     };
     if constexpr (!RING)
         if (r0 < a.rows) load_next(r0);
-    for (int64_t r = r0; r < a.rows; r += step) {
+    // (the lanes of a warp stay together: those without a row have zeros and write nothing)
+    for (int64_t r = r0; LANES < 32 ? r - lane / LANES < a.rows : r < a.rows; r += step) {
+        const bool in = LANES == 32 || r < a.rows;
         const F2 rstd = f2(rstd_next);
-        if (r + step < a.rows) rstd_next = a.rstd[r + step];
+        rstd_next = r + step < a.rows ? a.rstd[r + step] : 0.f;  // 0 without a row: what a NaN would do to the sums
         Row x, d, ds;
         auto from_ring = [&](Row& row, int m) {
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
                 row.v[i] = V{};
-                if (i * tpr + t < n) row.v[i] = *slot(stage, m, i);
+                if (in && i * tpr + t < n) row.v[i] = *slot(stage, m, i);
             }
         };
         if constexpr (RING) {
@@ -466,7 +487,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) rms_bwd_rows(RmsBwd<T> a) {
             }
         }
         if (a.dx) {
-            float q = warp_sum(lo(q2) + hi(q2));
+            float q = lanes_sum<LANES>(lo(q2) + hi(q2));
             if (!WARP) {
                 if (lane == 0) part[flip][warp] = q;
                 __syncthreads();
@@ -497,17 +518,22 @@ __global__ void __launch_bounds__(WARP ? 128 : 512) rms_bwd_rows(RmsBwd<T> a) {
                 g = fma2(xh, mq, g);
                 x.set(p, a.ds ? fma2(rstd, g, ds.pair(p)) : mul2(rstd, g));
             }
-            x.store(a.dx + r * a.lddx, t, tpr, n);
+            if (in) x.store(a.dx + r * a.lddx, t, tpr, n);
         }
         if (++stage == STAGES) stage = 0;
     }
     if (!a.part_w) return;
     float* pw = a.part_w + static_cast<int64_t>(blockIdx.x) * a.H;
     auto column = [&](int e) { return VEC == 1 ? e * tpr + t : ((e / VEC) * tpr + t) * VEC + e % VEC; };
+    if constexpr (LANES < 32)  // of the rows of a warp, pair by pair
+#pragma unroll
+        for (int o = LANES; o < 32; o <<= 1)
+#pragma unroll
+            for (int p = 0; p < Row::PAIRS; ++p) sw[p] = add2(sw[p], F2{__shfl_xor_sync(0xFFFFFFFFu, sw[p].u, o)});
     if (WARP) {  // the warps' sums, one warp after the other
         float* cols = reinterpret_cast<float*>(dyn + (RING ? STAGES * mats * ITEMS * 128 * sizeof(V) : 0));
         for (int k = 0; k < 4; ++k) {
-            if (warp == k)
+            if (warp == k && lane < LANES)
 #pragma unroll
                 for (int e = 0; e < 2 * Row::PAIRS; ++e) {
                     const int c = column(e);
@@ -569,13 +595,13 @@ __global__ void __launch_bounds__(256) rms_dw_any(RmsBwd<T> a) {
     }
 }
 
-template <typename T, typename W, int VEC, int ITEMS, int R, int STAGES, int MAX_WARPS, int BLOCKS, bool QUANT>
+template <typename T, typename W, int VEC, int ITEMS, int R, int STAGES, int MAX_WARPS, int BLOCKS, bool QUANT, int LANES = 32>
 lce_status_t rms_rows(const RmsFwd<T>& a, cudaStream_t s) {
     static Resident memo;
-    auto kernel = rms_fwd_rows<T, W, VEC, ITEMS, R, STAGES, MAX_WARPS, BLOCKS, QUANT>;
-    const int threads = threads_for(a.H / VEC, ITEMS);
+    auto kernel = rms_fwd_rows<T, W, VEC, ITEMS, R, STAGES, MAX_WARPS, BLOCKS, QUANT, LANES>;
+    const int threads = LANES < 32 ? 32 : threads_for(a.H / VEC, ITEMS);
     const size_t vec = sizeof(Vec<T, VEC>), smem = vec >= 4 ? (a.r ? 2 : 1) * static_cast<size_t>(STAGES) * R * ITEMS * threads * vec : 0;
-    const int64_t most = resident_blocks(&memo, kernel, threads, smem), groups = (a.rows + R - 1) / R;
+    const int64_t per = R * 32 / LANES, most = resident_blocks(&memo, kernel, threads, smem), groups = (a.rows + per - 1) / per;
     if (most <= 0) return LCE_ERR_CUDA;
     LCE_PROFILED(launch_after(kernel, dim3(static_cast<unsigned>(groups < most ? groups : most)), threads, smem, s, a));
     return LCE_OK;
@@ -600,6 +626,8 @@ lce_status_t rms_forward_as(const RmsCall& c, const RmsFwd<T>& a) {
     };
     if (fits(V) && c.H / V <= 2048) {
         const int n = c.H / V;
+        if (n <= 8) return rms_rows<T, W, V, 1, 1, 3, 1, 12, QUANT, 8>(a, s);
+        if (n <= 16) return rms_rows<T, W, V, 1, 1, 3, 1, 12, QUANT, 16>(a, s);
         if (n <= 32) return rms_rows<T, W, V, 1, 1, 3, 1, 12, QUANT>(a, s);
         if (n <= 64) return rms_rows<T, W, V, 2, 1, 3, 1, 12, QUANT>(a, s);
         if (n <= 128) return rms_rows<T, W, V, 4, 1, 3, 1, 12, QUANT>(a, s);
@@ -630,16 +658,17 @@ lce_status_t rms_forward(const RmsCall& c) {
 // block per row 54), or sixteen single elements; wider rows are read again.
 // Measured with the sum's gradient: 16384 x 1024 bf16 27 us (the copy rate
 // would be 20), 65536 x 2560 without it 155 us (148).
-template <typename T, typename W, int VEC, int ITEMS, bool WARP, bool KEEP>
+template <typename T, typename W, int VEC, int ITEMS, bool WARP, bool KEEP, int LANES = 32>
 lce_status_t rms_bwd(const RmsBwd<T>& a, int* parts, cudaStream_t s) {
     static Resident memo;
-    auto kernel = rms_bwd_rows<T, W, VEC, ITEMS, WARP, KEEP>;
+    auto kernel = rms_bwd_rows<T, W, VEC, ITEMS, WARP, KEEP, LANES>;
     const int threads = WARP ? 128 : threads_for(a.H / VEC, ITEMS);
     const size_t vec = sizeof(Vec<T, VEC>), ring = vec >= 4 ? RMS_BWD_STAGES * (KEEP && a.ds ? 3 : 2) * ITEMS * threads * vec : 0;
     const size_t smem = ring + (WARP ? static_cast<size_t>(a.H) * 4 : 0);
     int64_t blocks = resident_blocks(&memo, kernel, threads, smem);
     if (blocks <= 0) return LCE_ERR_CUDA;
-    const int64_t work = WARP ? (a.rows + 3) / 4 : a.rows;
+    constexpr int PER = WARP ? 4 * 32 / LANES : 1;  // rows of a block at a time
+    const int64_t work = (a.rows + PER - 1) / PER;
     if (blocks > work) blocks = work;
     if (blocks > NORM_PARTS) blocks = NORM_PARTS;
     *parts = static_cast<int>(blocks);
@@ -662,7 +691,9 @@ lce_status_t rms_backward(const RmsCall& c) {
     lce_status_t st = LCE_OK;
     if (fits(V) && c.H / V <= 2048) {
         const int n = c.H / V;
-        st = n <= 32     ? rms_bwd<T, W, V, 1, true, true>(a, &parts, s)
+        st = n <= 8      ? rms_bwd<T, W, V, 1, true, true, 8>(a, &parts, s)
+             : n <= 16   ? rms_bwd<T, W, V, 1, true, true, 16>(a, &parts, s)
+             : n <= 32   ? rms_bwd<T, W, V, 1, true, true>(a, &parts, s)
              : n <= 64   ? rms_bwd<T, W, V, 2, true, true>(a, &parts, s)
              : n <= 128  ? rms_bwd<T, W, V, 4, true, true>(a, &parts, s)
              : n <= 1024 ? rms_bwd<T, W, V, 2, false, true>(a, &parts, s)

@@ -175,3 +175,33 @@ def test_no_rows():
     assert f["y"].shape == (0, 64) and f["rstd"].shape == (0,)
     assert rms_norm_fp8(x, w)["scales"].shape == (0, 1)
     assert not rms_norm_backward(x, x, w, f["rstd"])["grad_weight"].any()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 31, 33, 1000, 40001])
+@pytest.mark.parametrize("H,dtype", [(8, "bf16"), (24, "bf16"), (64, "fp16"), (72, "bf16"), (128, "fp16"), (136, "bf16"), (32, "fp32"),
+                                     (48, "fp32"), (64, "fp32"), (68, "fp32")])
+def test_narrow_rows(rows, H, dtype):
+    """Several rows to a warp: rows that end inside one, and rows beside one that is not finite."""
+    from lm_head_linear_chunked_gb300.rms_norm import rms_norm_backward, rms_norm_forward, rms_norm_fp8
+    x, res, w, dy, ds = inputs(rows, H, dtype, dtype, 70)
+    f = rms_norm_forward(x, w, res, EPS)
+    y, rstd = rms_ref(f["sum"], w, EPS)
+    assert_within(f["y"], y, rms_tolerance(y, H, x.dtype), "y")
+    assert_within(f["rstd"], rstd, rstd * (sum_depth(H) / 2 + 6) * U32, "rstd")
+    check_backward(dy, f["sum"], w, f["rstd"], ds, rms_norm_backward(dy, f["sum"], w, f["rstd"], ds), w.dtype)
+    for group in (0, 128):
+        q = rms_norm_fp8(x, w, res, EPS, group)
+        scale = q["scales"].repeat_interleave(group or H, 1)[:, :H].double()
+        assert_within(q["q"].double(), y / scale, (y / scale).abs() * (2.0 ** -4 + 64 * U32) + 2.0 ** -10, "q")
+    bad = x.clone()
+    bad[rows // 2, H // 2] = float("nan")
+    g = rms_norm_forward(bad, w, res, EPS)
+    fine = torch.arange(rows, device="cuda") != rows // 2
+    assert torch.equal(g["y"][fine], f["y"][fine]) and bool(g["y"][~fine].isnan().all())
+    d = rms_norm_backward(dy, g["sum"], w, g["rstd"], ds)
+    assert bool(d["grad_x"][fine].isfinite().all()) and bool(d["grad_weight"].isnan().all())
+    # its gradient zero: the row adds nothing that is not NaN itself, and the other columns' sums are those of the others
+    zero = rms_norm_backward(torch.where(fine[:, None], dy, 0), torch.where(fine[:, None], f["sum"], 0), w, f["rstd"])["grad_weight"]
+    part = rms_norm_backward(dy[fine], f["sum"][fine], w, f["rstd"][fine])["grad_weight"]
+    each = (dy.double() * f["sum"].double() * f["rstd"].double()[:, None]).abs().sum(0)
+    assert_within(zero, part.double(), each * 2 * (rows + 4) * U32 + 3 * half_step(w.dtype) * part.double().abs() + 3 * tiny(w.dtype), "sums")
