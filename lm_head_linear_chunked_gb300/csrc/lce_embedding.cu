@@ -220,7 +220,7 @@ struct EmbBwd {
     float* parts;
     void* dw;
     int64_t lddw, chunks;
-    bool add;
+    bool add, few;
     int32_t H, slabs;
     int32_t split;    // warps to a chunk and slab
     int32_t joining;  // blocks of the last kernel that add pieces up
@@ -377,6 +377,91 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
         }
     }
 }
+
+// ---------------------------------------------------------------- few tokens
+
+// Up to EMB_FEW tokens: a few threads count the tokens that come before one, which is its place; and a block adds up a
+// whole run: two short kernels, whatever the vocabulary.  64 x 256 bf16 into 1000 rows: 6.5 us, 10.6 the long way; 256 x
+// 513 fp16 into 32768: 9.8 and 25.7, with one token alone 16.1 and 23.5; 256 x 4096 bf16 into 3000: 11.3 and 15.4.  The
+// count is of N * N and a run waits on one block: to 512 tokens, 512 x 4096 took 21.7 against 14.4.
+constexpr int EMB_FEW = 256, EMB_FEW_SHARE = 1024 / EMB_FEW, EMB_FEW_WARPS = 8;
+
+struct FewJob {
+    FirstDigit f;
+    int32_t n, extra;
+};
+__global__ void __launch_bounds__(EMB_FEW * EMB_FEW_SHARE) emb_sort_few(FewJob job) {
+    __shared__ __align__(16) int32_t keys[EMB_FEW];
+    wait_for_primary();
+    if (blockIdx.x > 0) return job.f.beside(0, blockIdx.x - 1, job.extra);
+    launch_dependents();
+    const int i = threadIdx.x / EMB_FEW_SHARE, share = threadIdx.x % EMB_FEW_SHARE;
+    bool bad = false;
+    SortItem x{0, INT32_MAX, 0};
+    if (i < job.n) x = job.f.load(i, &bad);
+    if (share == 0) keys[i] = x.key;
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) job.f.status(any);
+    int32_t at = 0;
+#pragma unroll 4
+    for (int j = 4 * share; j < job.n; j += 4 * EMB_FEW_SHARE) {  // (token, place) before (token, place)
+        const int4 k = *reinterpret_cast<const int4*>(keys + j);
+        at += (k.x < x.key + (j < i)) + (k.y < x.key + (j + 1 < i)) + (k.z < x.key + (j + 2 < i)) + (k.w < x.key + (j + 3 < i));
+    }
+#pragma unroll
+    for (int o = 1; o < EMB_FEW_SHARE; o *= 2) at += __shfl_xor_sync(0xFFFFFFFFu, at, o);
+    if (share == 0 && i < job.n) job.f.put(x, at);
+}
+
+// A block per sorted token and slab: the first of a run adds it up, its rows
+// shared out over its warps and joined in a fixed order.
+template <typename T, typename W, int VEC, int ITEMS>
+__global__ void __launch_bounds__(32 * EMB_FEW_WARPS) emb_sum_few(EmbBwd<T> a) {
+    using V = Vec<T, VEC>;
+    constexpr int PAIRS = VEC * ITEMS / 2, WARPS = EMB_FEW_WARPS, BATCH = VEC * sizeof(T) == 16 ? 8 / ITEMS : 4;
+    __shared__ F2 part[WARPS][PAIRS][32];
+    wait_for_primary();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.H / VEC, N = static_cast<int>(a.N);
+    const int i = static_cast<int>(blockIdx.x / a.slabs), k0 = static_cast<int>(blockIdx.x % a.slabs) * 32 * ITEMS + lane;
+    const int32_t v = a.keys[i];
+    if (v >= a.V || (i > 0 && a.keys[i - 1] == v)) return;
+    int end = i + 1;
+    for (unsigned same = 0xFFFFFFFFu; same == 0xFFFFFFFFu; end += same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1)
+        same = __ballot_sync(0xFFFFFFFFu, end + lane < N && a.keys[end + lane] == v);
+    if (warp && end - i == 1) return;
+    F2 s[PAIRS];
+#pragma unroll
+    for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
+    for (int r = i + warp; r < end; r += WARPS * BATCH) {
+        RowVectors<T, VEC, ITEMS> x[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const bool in = r + WARPS * b < end;
+            const V* from = reinterpret_cast<const V*>(a.dy + static_cast<int64_t>(in ? a.rows[r + WARPS * b] : 0) * a.ldd) + k0;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                x[b].v[k] = V{};
+                if (in && k0 + 32 * k < n) load_now(x[b].v[k], from + 32 * k);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], x[b].pair(p));
+    }
+    if (end - i > 1) {
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) part[warp][p][lane] = s[p];
+        __syncthreads();
+        if (warp) return;
+        for (int w = 1; w < WARPS; ++w)
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], part[w][p][lane]);
+    }
+    emb_store<W, VEC, ITEMS>(s, static_cast<W*>(a.dw) + v * a.lddw, k0, n, a.scale, a.add);
+}
+
+// ---------------------------------------------------------------- the end
 
 // What is left after the sums.  The first `joining` blocks: the runs that reach
 // past a chunk, a slab of columns of one per block, its pieces shared out over
@@ -540,6 +625,14 @@ lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int6
     return st;
 }
 
+lce_status_t emb_order_few(int64_t N, int64_t V, const void* tokens, bool idx64, int64_t padding, const Clear& clear,
+                           const EmbSpace& e, cudaStream_t s) {
+    const FewJob job{{tokens, idx64, static_cast<int32_t>(V), 0, padding, e.keys[0], e.rows[0], &e.hdr->status, nullptr, nullptr, 1, clear},
+                     static_cast<int32_t>(N), clear.rows ? static_cast<int32_t>(SORT_BLOCKS) - 1 : 0};
+    LCE_PROFILED(launch_after(emb_sort_few, dim3(static_cast<unsigned>(1 + job.extra)), EMB_FEW * EMB_FEW_SHARE, 0, s, job));
+    return LCE_OK;
+}
+
 // The widest vectors in which rows `ld` elements apart from p can be read.
 template <typename T>
 int vector_of(const void* p, int64_t ld, int64_t H) {
@@ -582,6 +675,14 @@ int32_t emb_slabs(int64_t vectors, int items) { return static_cast<int32_t>((vec
 
 template <typename T, typename W, int VEC>
 lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
+    if (a.few) {
+        constexpr int ITEMS = 8 / VEC;
+        a.slabs = emb_slabs(a.H / VEC, ITEMS);
+        const int64_t blocks = a.N * a.slabs;
+        if (blocks == 0) return LCE_OK;
+        LCE_PROFILED(launch_after(emb_sum_few<T, W, VEC, ITEMS>, dim3(static_cast<unsigned>(blocks)), 32 * EMB_FEW_WARPS, 0, s, a));
+        return LCE_OK;
+    }
     constexpr int AHEAD = VEC * sizeof(T) >= 4 ? 8 : 0, ITEMS = AHEAD ? 8 / VEC : 2;
     a.slabs = emb_slabs(a.H / VEC, ITEMS);
     // a chunk's runs over four warps where there are few chunks (620 tokens of 128 bf16: 19.7 us, not 26.0; 90000: 52.1 and 63.2)
@@ -684,15 +785,18 @@ lce_status_t lce_embedding_backward(int64_t N, int64_t V, int64_t H, int dtype, 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int where = 0;
     const int64_t size = static_cast<int64_t>(dtype_bytes(gtype));
-    const bool early = !add && emb_early(N, V, V * H * size), late = !add && !early;
+    const bool few = N <= EMB_FEW && (add || V * H * size <= EMB_CLEAR_BYTES);
+    const bool early = !add && (few || emb_early(N, V, V * H * size)), late = !add && !early;
     const Clear clear{static_cast<uint8_t*>(grad_weight), early ? V : 0, H * size, ldgw * size, 0, 1};
-    const lce_status_t sorted = emb_sort(N, V, tokens, index_bytes == 8, padding_token, late, clear, e, &where, s);
+    const lce_status_t sorted =
+        few ? emb_order_few(N, V, tokens, index_bytes == 8, padding_token, clear, e, s)
+            : emb_sort(N, V, tokens, index_bytes == 8, padding_token, late, clear, e, &where, s);
     if (sorted != LCE_OK) return sorted;
     return with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);
         const EmbBwd<T> a{static_cast<const T*>(grad_y), ldg, N, V, scale, e.keys[where], e.rows[where],
                           late ? e.named : nullptr, e.n_spans, e.spans,
-                          e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, static_cast<int32_t>(H), 0, 1, 0, 0};
+                          e.parts, grad_weight, ldgw, (N + EMB_CHUNK - 1) / EMB_CHUNK, add, few, static_cast<int32_t>(H), 0, 1, 0, 0};
         return gtype == LCE_F32 ? emb_gradient<T, float>(a, s) : emb_gradient<T, T>(a, s);
     });
 }

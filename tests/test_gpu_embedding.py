@@ -125,6 +125,29 @@ def test_outputs_given_and_added_to(H):
         check_grad(embedding_backward(dy[:1].expand(N, H), t, V), dy[:1].expand(N, H), t, V, 1.0)
 
 
+@pytest.mark.parametrize("N", [1, 3, 31, 33, 63, 255, 256, 257])
+@pytest.mark.parametrize("H", [1, 64, 513, 4096])
+def test_few_tokens(N, H):
+    """A short path to 256 tokens: into a new gradient, one given and one that has values, which other rows keep."""
+    from lm_head_linear_chunked_gb300.embedding import embedding_backward
+    V = 700
+    for kind in ("one", "distinct", "few"):
+        t = tokens_of(kind, N, V, 21)
+        if N > 4:
+            t[2], t[3], t[4] = -100, V, -5
+        for dtype in (torch.bfloat16, torch.float16, torch.float32):
+            dy = normal((N, H), 22, dtype)
+            check_grad(embedding_backward(dy, t, V, 0.5, -100), dy, t, V, 0.5, -100)
+            acc = normal((V, H + 3), 23)
+            before = acc.clone()
+            out = embedding_backward(dy, t, V, 0.5, -100, out=acc[:, :H], accumulate=True)
+            check_grad(out, dy, t, V, 0.5, -100, before[:, :H])
+            unnamed = torch.ones(V, dtype=torch.bool, device="cuda")
+            unnamed[t[(t >= 0) & (t < V)]] = False
+            assert torch.equal(out[unnamed], before[:, :H][unnamed]) and torch.equal(acc[:, H:], before[:, H:])
+            check_grad(embedding_backward(dy, t, V, 0.5, -100, out=acc[:, :H]), dy, t, V, 0.5, -100)
+
+
 def test_autograd_and_tied_weights():
     """The module's gradient, and the sum of both uses of a matrix that the head shares."""
     import lm_head_linear_chunked_gb300 as lce
