@@ -413,12 +413,12 @@ LCE_API lce_status_t lce_rms_norm_backward(int64_t rows, int64_t H, int dtype, i
  * types, strides, alignment and the tokens, so equal calls give equal bits.
  *  - weight [V, H], y and grad_y [N, H], grad_weight [V, H], each with its own
  *    stride in elements; tokens [N] int32 or int64 (index_bytes 4 or 8).
- *  - A token equal to padding_token (LCE_NO_PADDING: none) gives no gradient;
- *    its y is its row of the weight, or zero where it lies outside [0, V).
- *    Another token outside [0, V) gives a row of NaN and no gradient, and
- *    LCE_ERR_INDEX_RANGE from lce_check_status: of `status` (a device word
- *    that the caller has zeroed; may be NULL) after the forward, of ws after
- *    the backward.
+ *  - A token equal to padding_token (LCE_NO_PADDING: none, that value apart)
+ *    gives no gradient; its y is its row of the weight, or zero where it lies
+ *    outside [0, V).  Another token outside [0, V) gives a row of NaN and no
+ *    gradient, and LCE_ERR_INDEX_RANGE from lce_check_status: of `status` (a
+ *    device word that the caller has zeroed; may be NULL) after the forward, of
+ *    ws after the backward.
  *  - gtype, grad_weight's type, is dtype or LCE_F32.  All of grad_weight is
  *    written, zeros where no token names a row.  With LCE_ACCUMULATE (flags;
  *    gtype LCE_F32) the sums are added to what it holds, and rows that no token

@@ -31,7 +31,7 @@ struct RmsIn {
     int code, wcode;
     int64_t rows, H, ldx = 0, ldr = 0;
     Tensor x;
-    OptTensor residual;
+    OptTensor residual, weight;
 };
 
 RmsIn rms_in(const Tensor& x, const OptTensor& weight, const OptTensor& residual) {
@@ -57,11 +57,14 @@ RmsIn rms_in(const Tensor& x, const OptTensor& weight, const OptTensor& residual
     return in;
 }
 
+Tensor plain(const Tensor& t) { return t.is_neg() ? t.resolve_neg().contiguous() : t.contiguous(); }
+
 // The rows, on their device (under the caller's guard).
-void rms_rows(RmsIn* in, const Tensor& x, const OptTensor& residual) {
+void rms_rows(RmsIn* in, const Tensor& x, const OptTensor& weight, const OptTensor& residual) {
     in->x = rows_of(x, &in->ldx);
     in->ldr = in->ldx;
     if (residual) in->residual = rows_of(*residual, &in->ldr);
+    if (weight) in->weight = plain(*weight);
 }
 
 // y, and where wanted the sum and rstd
@@ -71,12 +74,12 @@ std::tuple<Tensor, OptTensor, OptTensor> rms_forward(const Tensor& x, const OptT
     RmsIn in = rms_in(x, weight, residual);
     const at::Device dev = x.device();
     const c10::cuda::CUDAGuard guard(dev);
-    rms_rows(&in, x, residual);
+    rms_rows(&in, x, weight, residual);
     const Tensor y = like(in.x);
     OptTensor sum, rstd;
     if (residual) sum = like(in.x);
     if (stats) rstd = empty({in.rows}, at::kFloat, dev);
-    check(lib.rms_forward(in.rows, in.H, in.code, in.wcode, in.x.data_ptr(), in.ldx, ptr(in.residual), in.ldr, ptr(weight),
+    check(lib.rms_forward(in.rows, in.H, in.code, in.wcode, in.x.data_ptr(), in.ldx, ptr(in.residual), in.ldr, ptr(in.weight),
                           static_cast<float>(eps), ptr(sum), in.H, y.data_ptr(), in.H, static_cast<float*>(ptr(rstd)),
                           stream_of(dev)),
           "lce_rms_norm_forward");
@@ -92,12 +95,12 @@ std::tuple<Tensor, Tensor, OptTensor> rms_fp8(const Tensor& x, const OptTensor& 
     RmsIn in = rms_in(x, weight, residual);
     const at::Device dev = x.device();
     const c10::cuda::CUDAGuard guard(dev);
-    rms_rows(&in, x, residual);
+    rms_rows(&in, x, weight, residual);
     const Tensor q = empty(x.sizes(), at::kFloat8_e4m3fn, dev);
     const Tensor scales = empty(with_last(x.sizes(), group ? (in.H + group - 1) / group : 1), at::kFloat, dev);
     OptTensor sum;
     if (residual) sum = like(in.x);
-    check(lib.rms_fp8(in.rows, in.H, in.code, in.wcode, in.x.data_ptr(), in.ldx, ptr(in.residual), in.ldr, ptr(weight),
+    check(lib.rms_fp8(in.rows, in.H, in.code, in.wcode, in.x.data_ptr(), in.ldx, ptr(in.residual), in.ldr, ptr(in.weight),
                       static_cast<float>(eps), ptr(sum), in.H, static_cast<uint8_t*>(q.data_ptr()), in.H, ptr<float>(scales),
                       group, stream_of(dev)),
           "lce_rms_norm_fp8");
@@ -120,7 +123,7 @@ std::tuple<OptTensor, OptTensor> rms_backward(const Tensor& dy_in, const Tensor&
     want_w = want_w && weight.has_value();
     check_shape(rstd, {rows}, "rstd");
     check_type(rstd, at::kFloat, "rstd");
-    if (!rstd.is_contiguous()) throw py::type_error("rstd must be contiguous");
+    if (!rstd.is_contiguous() || rstd.is_neg()) throw py::type_error("rstd must be contiguous");
     if (ds_in) {
         check_shape(*ds_in, x_in.sizes(), "grad_sum");
         check_type(*ds_in, x_in.scalar_type(), "grad_sum");
@@ -134,7 +137,8 @@ std::tuple<OptTensor, OptTensor> rms_backward(const Tensor& dy_in, const Tensor&
     on_device(ds_in, dev, "grad_sum");
     int64_t ldx = 0, ldd = 0, ldds = 0;
     const Tensor x = rows_of(x_in, &ldx), dy = rows_of(dy_in, &ldd);
-    OptTensor ds, dx, dw, ws;
+    OptTensor ds, dx, dw, ws, w;
+    if (weight) w = plain(*weight);
     if (ds_in) ds = rows_of(*ds_in, &ldds);
     if (want_x) dx = like(x);
     size_t bytes = 0;
@@ -145,7 +149,7 @@ std::tuple<OptTensor, OptTensor> rms_backward(const Tensor& dy_in, const Tensor&
     }
     if (want_x || want_w)
         check(lib.rms_backward(rows, H, code, weight ? type_code(*weight, "weight") : code, dy.data_ptr(), ldd, x.data_ptr(), ldx,
-                               ptr(weight), ptr<float>(rstd), ptr(ds), ldds, ptr(dx), H, ptr(dw), ptr(ws), bytes,
+                               ptr(w), ptr<float>(rstd), ptr(ds), ldds, ptr(dx), H, ptr(dw), ptr(ws), bytes,
                                stream_of(dev)),
               "lce_rms_norm_backward");
     return {dx, dw};
@@ -178,6 +182,16 @@ Tensor embedding_forward(const Tensor& tokens_in, const Tensor& weight, double s
     return y;
 }
 
+// out [n, H], rows apart by its stride, must not reach into the memory that `in` may lie in.
+void apart(const Tensor& out, int64_t n, int64_t H, const Tensor& in, const char* what) {
+    if (!out.has_storage() || !in.has_storage() || !out.numel() || !in.numel()) return;
+    const auto first = reinterpret_cast<uintptr_t>(out.const_data_ptr()), from = reinterpret_cast<uintptr_t>(in.const_data_ptr());
+    int64_t last = 0;
+    for (int64_t d = 0; d < in.dim(); ++d) last += (in.size(d) - 1) * in.stride(d);
+    const uintptr_t end = first + ((n > 1 ? (n - 1) * out.stride(0) : 0) + H) * out.element_size();
+    if (first < from + (last + 1) * in.element_size() && from < end) throw py::value_error(std::string("out and ") + what + " overlap");
+}
+
 // grad_weight and the workspace
 std::tuple<Tensor, Tensor> embedding_backward(const Tensor& dy_in, const Tensor& tokens_in, int64_t V, double scale,
                                               std::optional<int64_t> padding, std::optional<at::ScalarType> type,
@@ -199,6 +213,7 @@ std::tuple<Tensor, Tensor> embedding_backward(const Tensor& dy_in, const Tensor&
         check_type(*out, gtype, "out");
         if ((H > 1 && out->stride(1) != 1) || (V > 1 && out->stride(0) < H) || out->is_neg())
             throw py::value_error("out must have contiguous rows that do not overlap, got strides " + text(out->strides()));
+        apart(*out, V, H, dy_in, "grad_y");
     }
     const at::Device dev = dy_in.device();
     on_cuda(dev);
@@ -216,6 +231,7 @@ std::tuple<Tensor, Tensor> embedding_backward(const Tensor& dy_in, const Tensor&
                                  static_cast<float>(scale), padding.value_or(LCE_NO_PADDING), dw.data_ptr(),
                                  V > 1 ? dw.stride(0) : H, ws.data_ptr(), space, stream_of(dev), accumulate ? LCE_ACCUMULATE : 0),
           "lce_embedding_backward");
+    if (out && !out->is_inference()) out->unsafeGetTensorImpl()->bump_version();  // written, for what has saved it
     return {dw, ws};
 }
 
@@ -303,8 +319,6 @@ int check_weights(const Tensor& weights, const Tensor& rows, const Tensor& posit
     if (weights.scalar_type() != rows.scalar_type()) check_type(weights, at::kFloat, "weights");
     return type_code(weights, "weights");
 }
-
-Tensor plain(const Tensor& t) { return t.is_neg() ? t.resolve_neg().contiguous() : t.contiguous(); }
 
 Tensor expert_combine(const Tensor& rows_in, const OptTensor& weights_in, const Tensor& positions, const Tensor& slots,
                       bool recorded) {

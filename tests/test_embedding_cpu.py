@@ -70,6 +70,7 @@ def test_workspace_size():
 W = torch.zeros(10, 16, dtype=torch.bfloat16)
 T = torch.zeros(4, dtype=torch.int64)
 D = torch.zeros(4, 16, dtype=torch.bfloat16)
+ONE = torch.zeros(20, 16)
 
 
 @pytest.mark.parametrize("call,error", [
@@ -91,12 +92,19 @@ D = torch.zeros(4, 16, dtype=torch.bfloat16)
     (lambda: embedding_backward(D, T, 10, dtype=torch.float32, out=W), TypeError),
     (lambda: embedding_backward(D, T, 10, out=W[:1].expand(10, 16)), ValueError),
     (lambda: embedding_backward(D, T, 10, out=torch.zeros(16, 10, dtype=torch.bfloat16).t()), ValueError),
+    (lambda: embedding_backward(ONE[1:9], T.repeat(2), 10, out=ONE[8:18]), ValueError),   # overlap
     (lambda: Embedding(0, 4), ValueError),
     (lambda: Embedding(4, 0), ValueError),
 ])
 def test_front_end_refusals(call, error):
     with pytest.raises(error):
         call()
+
+
+def test_an_output_that_overlaps_the_gradient():
+    for a, b, overlap in ((0, 4, False), (1, 4, True), (4, 4, True), (13, 4, True), (14, 4, False), (5, 0, False)):
+        with pytest.raises(ValueError, match="overlap" if overlap else "CUDA"):
+            embedding_backward(ONE[a:a + b], T[:b], 10, out=ONE[4:14])
 
 
 def test_module_parameters():

@@ -148,6 +148,20 @@ def test_few_tokens(N, H):
             check_grad(embedding_backward(dy, t, V, 0.5, -100, out=acc[:, :H]), dy, t, V, 0.5, -100)
 
 
+def test_an_output_that_autograd_has_saved():
+    """Written into, it is not what was saved: the backward that would read it says so."""
+    from lm_head_linear_chunked_gb300.embedding import embedding_backward
+    t, dy = tokens_of("zipf", 40, 30, 24), normal((40, 16), 25)
+    acc, x = torch.zeros(30, 16, device="cuda"), normal((30, 16), 26).requires_grad_(True)
+    y = (x * acc).sum()
+    embedding_backward(dy, t, 30, out=acc, accumulate=True)
+    with pytest.raises(RuntimeError, match="modified"):
+        y.backward()
+    with torch.inference_mode():
+        acc = torch.zeros(30, 16, device="cuda")
+        check_grad(embedding_backward(dy, t, 30, out=acc, accumulate=True), dy, t, 30, 1.0)
+
+
 def test_autograd_and_tied_weights():
     """The module's gradient, and the sum of both uses of a matrix that the head shares."""
     import lm_head_linear_chunked_gb300 as lce

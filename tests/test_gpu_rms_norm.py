@@ -133,6 +133,23 @@ def test_strides_and_alignment(H):
     assert torch.equal(rms_norm(torch._neg_view(x4), None, None, EPS), rms_norm(-x4, None, None, EPS))
 
 
+def test_negated_views():
+    """Memory that stands for other values, in every place that takes a tensor."""
+    from lm_head_linear_chunked_gb300.rms_norm import rms_norm_backward, rms_norm_forward, rms_norm_fp8
+    x, r, d, s = (normal((5, 320), k) for k in (34, 35, 36, 37))
+    w = normal((320,), 38)
+    neg = torch._neg_view
+    want, got = rms_norm_forward(-x, -w, -r, EPS), rms_norm_forward(neg(x), neg(w), neg(r), EPS)
+    assert all(torch.equal(want[k], got[k]) for k in want)
+    want, got = rms_norm_fp8(-x, -w, -r, EPS), rms_norm_fp8(neg(x), neg(w), neg(r), EPS)
+    assert all(torch.equal(want[k].float(), got[k].float()) for k in want)
+    rstd = rms_norm_forward(-x, None, None, EPS)["rstd"]
+    want, got = rms_norm_backward(-d, -x, -w, rstd, -s), rms_norm_backward(neg(d), neg(x), neg(w), rstd, neg(s))
+    assert all(torch.equal(want[k], got[k]) for k in want)
+    with pytest.raises(TypeError):
+        rms_norm_backward(d, x, w, neg(rstd), s)
+
+
 def test_autograd():
     """Through the module: y and the sum used, one of them, and neither's gradient asked for."""
     from lm_head_linear_chunked_gb300.rms_norm import RMSNorm, rms_norm, rms_norm_backward, rms_norm_forward

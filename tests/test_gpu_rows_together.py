@@ -136,15 +136,16 @@ def operators():
         b = torch.bfloat16
         return {"norm": (normal((900, 640), seed, b), normal((900, 640), seed + 1, b), normal(640, seed + 2), normal((900, 640), seed + 3, b)),
                 "short": (tokens_of("zipf", 700, 900, seed), normal((900, 72), seed, b), normal((700, 72), seed + 1, b)),
+                "handful": (tokens_of("zipf", 200, 900, seed), normal((900, 72), seed, b), normal((200, 72), seed + 1, b)),
                 "long": (tokens_of("few", 9000, 5000, seed), normal((5000, 136), seed), normal((9000, 136), seed + 1)),
                 "sparse": (tokens_of("zipf", 6000, 60000, seed), normal((60000, 24), seed), normal((6000, 24), seed + 1)),
                 "experts": (normal((3000, 200), seed, b), experts_of(3000, 4, 40, seed, "unused"), normal((3000, 4), seed + 1),
                             normal((3000, 200), seed + 2, b))}
 
-    return {"norm": norm, "short": lookup, "long": lookup, "sparse": lookup, "experts": experts}, inputs
+    return {"norm": norm, "handful": lookup, "short": lookup, "long": lookup, "sparse": lookup, "experts": experts}, inputs
 
 
-@pytest.mark.parametrize("name", ["norm", "short", "long", "sparse", "experts"])
+@pytest.mark.parametrize("name", ["norm", "handful", "short", "long", "sparse", "experts"])
 def test_side_streams_and_replayed_graphs(name):
     """Two graphs of one operator on their own inputs, replayed in turn and with new inputs, give the eager bits."""
     calls, inputs = operators()
