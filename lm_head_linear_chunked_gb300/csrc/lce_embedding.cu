@@ -380,38 +380,57 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
 
 // ---------------------------------------------------------------- few tokens
 
-// Up to EMB_FEW tokens: a few threads count the tokens that come before one, which is its place; and a block adds up a
-// whole run: two short kernels, whatever the vocabulary.  64 x 256 bf16 into 1000 rows: 6.5 us, 10.6 the long way; 256 x
-// 513 fp16 into 32768: 9.8 and 25.7, with one token alone 16.1 and 23.5; 256 x 4096 bf16 into 3000: 11.3 and 15.4.  The
-// count is of N * N and a run waits on one block: to 512 tokens, 512 x 4096 took 21.7 against 14.4.
-constexpr int EMB_FEW = 256, EMB_FEW_SHARE = 1024 / EMB_FEW, EMB_FEW_WARPS = 8;
+// Up to EMB_RANK tokens are sorted in one kernel: a token's place is the number of tokens that come before it, and every
+// block counts them for 32, a lane each, its warps a share of the tokens.  That is N * N comparisons, and the gradient's
+// rows are cleared behind them: 620 tokens of 128 bf16 11.8 us, 17.0 by digits in one block; 5084 of 128 fp16 19.8 and
+// 23.8 by digits; 8192 of 512 bf16 27.7 and 27.9, of 1024 into 151936 rows 68.9 and 62.9.
+constexpr int EMB_RANK = 6144;
 
-struct FewJob {
+struct RankJob {
     FirstDigit f;
-    int32_t n, extra;
+    int32_t n, blocks;  // blocks that count; all of them clear a share
 };
-__global__ void __launch_bounds__(EMB_FEW * EMB_FEW_SHARE) emb_sort_few(FewJob job) {
-    __shared__ __align__(16) int32_t keys[EMB_FEW];
+__global__ void __launch_bounds__(SORT_THREADS) emb_rank(RankJob job) {
+    __shared__ __align__(16) int32_t keys[EMB_RANK];
+    __shared__ int32_t before[32];
+    const FirstDigit& f = job.f;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = job.n;
+    if (!f.clear.rows) launch_dependents();
     wait_for_primary();
-    if (blockIdx.x > 0) return job.f.beside(0, blockIdx.x - 1, job.extra);
-    launch_dependents();
-    const int i = threadIdx.x / EMB_FEW_SHARE, share = threadIdx.x % EMB_FEW_SHARE;
-    bool bad = false;
-    SortItem x{0, INT32_MAX, 0};
-    if (i < job.n) x = job.f.load(i, &bad);
-    if (share == 0) keys[i] = x.key;
-    const int any = __syncthreads_or(bad);
-    if (threadIdx.x == 0) job.f.status(any);
-    int32_t at = 0;
+    f.begin();
+    if (static_cast<int>(blockIdx.x) < job.blocks) {
+        bool bad = false;
 #pragma unroll 4
-    for (int j = 4 * share; j < job.n; j += 4 * EMB_FEW_SHARE) {  // (token, place) before (token, place)
-        const int4 k = *reinterpret_cast<const int4*>(keys + j);
-        at += (k.x < x.key + (j < i)) + (k.y < x.key + (j + 1 < i)) + (k.z < x.key + (j + 2 < i)) + (k.w < x.key + (j + 3 < i));
+        for (int i = t; i < (n + 3) / 4 * 4; i += SORT_THREADS) keys[i] = i < n ? f.load(i, &bad).key : INT32_MAX;
+        if (t < 32) before[t] = 0;
+        const int any = __syncthreads_or(bad);
+        if (t == 0 && blockIdx.x == 0) f.status(any);
+        const int own = blockIdx.x * 32, i = own + lane;
+        const int32_t key = i < n ? keys[i] : 0;
+        const int each = (n + 127) / 128 * 4, j0 = warp * each, end = (n + 3) / 4 * 4, j1 = j0 + each < end ? j0 + each : end;
+        const int lo = own < j1 ? own : j1, hi = own + 32 < j1 ? own + 32 : j1;
+        int32_t count = 0;
+        int j = j0;
+        auto add = [&](int32_t a, int32_t b, int32_t c, int32_t d) {
+            const int4 k = *reinterpret_cast<const int4*>(keys + j);
+            count += (k.x < a) + (k.y < b) + (k.z < c) + (k.w < d);
+        };
+#pragma unroll 4
+        for (; j < lo; j += 4) add(key + 1, key + 1, key + 1, key + 1);  // equal ones that stand before come before
+        for (; j < hi; j += 4) add(key + (j < i), key + (j + 1 < i), key + (j + 2 < i), key + (j + 3 < i));
+#pragma unroll 4
+        for (; j < j1; j += 4) add(key, key, key, key);
+        atomicAdd(before + lane, count);
+        __syncthreads();
+        if (t < 32 && i < n) f.put({0, key, i}, before[lane]);
     }
-#pragma unroll
-    for (int o = 1; o < EMB_FEW_SHARE; o *= 2) at += __shfl_xor_sync(0xFFFFFFFFu, at, o);
-    if (share == 0 && i < job.n) job.f.put(x, at);
+    if (f.clear.rows) clear_share(f.clear, 0, blockIdx.x, gridDim.x);
 }
+
+// A block adds up a whole run, where there are up to EMB_FEW tokens: no pieces, so no third kernel.  64 tokens of 256 bf16
+// 8.1 us, 10.4 the long way, 256 of 513 fp16 10.1 and 24.1, with one token alone 16.6 and 21.6; but a run waits on one
+// block: 512 of 64 bf16 7.9 and 10.9, with one token alone 18.1 and 10.9.
+constexpr int EMB_FEW = 256, EMB_FEW_WARPS = 8;
 
 // A block per sorted token and slab: the first of a run adds it up, its rows
 // shared out over its warps and joined in a fixed order.
@@ -540,7 +559,6 @@ lce_status_t emb_sizes(int64_t N, int64_t V, int64_t H) {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Bits of the keys 0 .. V, in digits of at most EMB_DIGIT_BITS.
-static_assert(EMB_DIGIT_BITS * (SORT_PASSES_MAX + 1) >= 31);
 struct Digits {
     int passes, bits;
 };
@@ -593,6 +611,16 @@ bool emb_early(int64_t N, int64_t V, int64_t bytes) {
 // The sorted tokens: their place in e.keys and e.rows.
 lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int64_t padding, bool name, Clear clear,
                       const EmbSpace& e, int* where, cudaStream_t s) {
+    if (N <= EMB_RANK) {
+        const int32_t blocks = N > 32 ? static_cast<int32_t>((N + 31) / 32) : 1;
+        const int32_t all = blocks < SORT_BLOCKS && clear.rows ? static_cast<int32_t>(SORT_BLOCKS) : blocks;
+        const RankJob job{{tokens, idx64, static_cast<int32_t>(V), 0, padding, e.keys[0], e.rows[0], &e.hdr->status, e.n_spans,
+                           name ? e.named : nullptr, all, clear},
+                          static_cast<int32_t>(N), blocks};
+        *where = 0;
+        LCE_PROFILED(launch_after(emb_rank, dim3(static_cast<unsigned>(all)), SORT_THREADS, 0, s, job));
+        return LCE_OK;
+    }
     const Digits d = digits_of(V);
     SortShape shape{};
     shape.n = N;
@@ -609,11 +637,6 @@ lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int6
         const int from = (p - 1) & 1, to = p & 1;
         return NextDigit{e.keys[from], e.rows[from], p * d.bits, shape.bins - 1, e.keys[to], e.rows[to], clear};
     };
-    if (shape.blocks == 1) {
-        SortAlone<FirstDigit, NextDigit> job{first, {}, shape, d.passes - 1};
-        for (int p = 1; p < d.passes; ++p) job.next[p - 1] = next(p);
-        return sort_alone_by(job, s);
-    }
     clear.of = 2 * d.passes;  // a share for each kernel
     first.clear = clear;
     lce_status_t st = sort_by(first, shape, s);
@@ -623,14 +646,6 @@ lce_status_t emb_sort(int64_t N, int64_t V, const void* tokens, bool idx64, int6
         st = sort_by(next(p), shape, s);
     }
     return st;
-}
-
-lce_status_t emb_order_few(int64_t N, int64_t V, const void* tokens, bool idx64, int64_t padding, const Clear& clear,
-                           const EmbSpace& e, cudaStream_t s) {
-    const FewJob job{{tokens, idx64, static_cast<int32_t>(V), 0, padding, e.keys[0], e.rows[0], &e.hdr->status, nullptr, nullptr, 1, clear},
-                     static_cast<int32_t>(N), clear.rows ? static_cast<int32_t>(SORT_BLOCKS) - 1 : 0};
-    LCE_PROFILED(launch_after(emb_sort_few, dim3(static_cast<unsigned>(1 + job.extra)), EMB_FEW * EMB_FEW_SHARE, 0, s, job));
-    return LCE_OK;
 }
 
 // The widest vectors in which rows `ld` elements apart from p can be read.
@@ -788,9 +803,7 @@ lce_status_t lce_embedding_backward(int64_t N, int64_t V, int64_t H, int dtype, 
     const bool few = N <= EMB_FEW && (add || V * H * size <= EMB_CLEAR_BYTES);
     const bool early = !add && (few || emb_early(N, V, V * H * size)), late = !add && !early;
     const Clear clear{static_cast<uint8_t*>(grad_weight), early ? V : 0, H * size, ldgw * size, 0, 1};
-    const lce_status_t sorted =
-        few ? emb_order_few(N, V, tokens, index_bytes == 8, padding_token, clear, e, s)
-            : emb_sort(N, V, tokens, index_bytes == 8, padding_token, late, clear, e, &where, s);
+    const lce_status_t sorted = emb_sort(N, V, tokens, index_bytes == 8, padding_token, late, clear, e, &where, s);
     if (sorted != LCE_OK) return sorted;
     return with_dtype(dtype, [&](auto t) -> lce_status_t {
         using T = decltype(t);

@@ -216,31 +216,6 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     place_items(job.f, job.shape);
 }
 
-// All digits of so few items that one block sorts them: `first`, then `passes` of `next`.
-constexpr int SORT_PASSES_MAX = 3;
-template <typename F, typename G>
-struct SortAlone {
-    F first;
-    G next[SORT_PASSES_MAX];
-    SortShape shape;
-    int passes;
-};
-template <typename F, typename G>
-__global__ void __launch_bounds__(SORT_THREADS) sort_alone(SortAlone<F, G> job) {
-    if (blockIdx.x > 0) {
-        wait_for_primary();
-        return job.first.beside(0, blockIdx.x - 1, job.shape.extra);
-    }
-    launch_dependents();
-    place_items(job.first, job.shape);
-    SortShape later = job.shape;
-    later.bad = nullptr;
-    for (int p = 0; p < job.passes; ++p) {
-        __syncthreads();  // what the last pass has put, and its counters
-        place_items(job.next[p], later);
-    }
-}
-
 // Lets a kernel take `bytes` of dynamic shared memory, out of the largest share
 // of an SM's: kernels that overlap with the one before them need the same
 // division into L1 and shared memory.  Asked once per device.
@@ -269,14 +244,6 @@ lce_status_t sort_by(const F& f, const SortShape& shape, cudaStream_t s) {
     if (shape.blocks > 1)
         LCE_PROFILED(launch_after(sort_count<F>, blocks, SORT_THREADS, static_cast<size_t>(shape.bins) * 4, s, job));
     LCE_PROFILED(launch_after(sort_place<F>, blocks, SORT_THREADS, sort_smem(shape.bins), s, job));
-    return LCE_OK;
-}
-
-template <typename F, typename G>
-lce_status_t sort_alone_by(const SortAlone<F, G>& job, cudaStream_t s) {
-    static std::atomic<uint64_t> known{0};
-    if (!allow_smem(&known, sort_alone<F, G>, static_cast<int>(sort_smem(SORT_BINS_MAX)))) return LCE_ERR_CUDA;
-    LCE_PROFILED(launch_after(sort_alone<F, G>, dim3(static_cast<unsigned>(1 + job.shape.extra)), SORT_THREADS, sort_smem(job.shape.bins), s, job));
     return LCE_OK;
 }
 

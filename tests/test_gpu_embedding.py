@@ -87,7 +87,7 @@ def test_padding_and_tokens_outside():
 
 @pytest.mark.parametrize("N,V,H", [(0, 5, 8), (1, 1, 1), (2, 1, 64), (31, 97, 33), (33, 1023, 64), (1000, 1024, 200), (1025, 1025, 256),
                                    (5000, 50257, 64), (3000, 151936, 128), (20000, 300, 1601), (70000, 151936, 40),
-                                   (2000, (1 << 20) + 3, 8), (4097, 7, 4096), (513, 2000, 5000), (300000, 5000, 16)])
+                                   (2000, (1 << 20) + 3, 8), (4097, 7, 4096), (6144, 3000, 24), (6145, 60000, 24), (513, 2000, 5000), (300000, 5000, 16)])
 @pytest.mark.parametrize("kind", ["one", "distinct", "few", "zipf"])
 def test_gradient(N, V, H, kind):
     from lm_head_linear_chunked_gb300.embedding import embedding_backward
