@@ -1,9 +1,11 @@
 // The torch side of the operators beside the head: checks of tensors, their
 // outputs and workspaces, and one call of the C ABI, in compiled code.  A
-// small call is bound by the host (a norm of 16 rows takes 7.8 us, replayed in
-// a CUDA graph 2.3; a selection over four beams 11.5 and 7.7), and the same
-// steps from Python took up to twice as long (13 and 23 us).  The library itself stays behind include/lce.h:
-// its addresses come from the ctypes binding, so that both use one library.
+// small call is bound by the host (a norm of 16 rows takes 4.9 us, replayed in
+// a CUDA graph 2.3; a selection over four beams 10.0 and 7.7), and the same
+// steps from Python took two to three times as long (13 and 23 us).  The library
+// itself stays behind include/lce.h: its addresses come from the ctypes binding,
+// so that both use one library.  What several operators share is in lce_torch.h,
+// the operators between token ids and the head are in lce_torch_rows.cpp.
 //
 // Everything that a kernel would otherwise read through a wrong pointer,
 // stride or type is refused here (TypeError, ValueError); a status other than
