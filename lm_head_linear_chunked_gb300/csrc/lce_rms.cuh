@@ -611,9 +611,12 @@ lce_status_t rms_rows(const RmsFwd<T>& a, cudaStream_t s) {
 // such boundaries (up to 128 a warp per row with the next rows copied ahead, up
 // to 512 a block with four a thread, or two rows of two where a quarter of such
 // a block would be idle, up to 2048 wider blocks), else 4 bytes, else one
-// element.  Measured with a residual: 32768 x 4096 bf16 to 8 bits 154 us, 0.90
+// element, up to 256 of them a warp per row as well.  A thread has as many as the
+// row needs.  Measured with a residual: 32768 x 4096 bf16 to 8 bits 154 us, 0.90
 // of the copy rate (two or four stages of the ring 168 and 156, eight warps
-// 157), 16384 x 1024 bf16 18.6 us, within the copy rate as its writes stay in L2.
+// 157), 16384 x 1024 bf16 18.6 us, within the copy rate as its writes stay in L2;
+// 71723 x 704 fp16 to 8 bits 62 us with three vectors a thread, 72 with four;
+// 88770 x 82 bf16 17.9 us, 38.7 by a block with room for eight 4-byte vectors a thread.
 template <typename T, typename W, bool QUANT>
 lce_status_t rms_forward_as(const RmsCall& c, const RmsFwd<T>& a) {
     cudaStream_t s = c.s;
@@ -630,13 +633,21 @@ lce_status_t rms_forward_as(const RmsCall& c, const RmsFwd<T>& a) {
         if (n <= 16) return rms_rows<T, W, V, 1, 1, 3, 1, 12, QUANT, 16>(a, s);
         if (n <= 32) return rms_rows<T, W, V, 1, 1, 3, 1, 12, QUANT>(a, s);
         if (n <= 64) return rms_rows<T, W, V, 2, 1, 3, 1, 12, QUANT>(a, s);
+        if (n <= 96) return rms_rows<T, W, V, 3, 1, 3, 1, 12, QUANT>(a, s);
         if (n <= 128) return rms_rows<T, W, V, 4, 1, 3, 1, 12, QUANT>(a, s);
         if (n <= 512 && 4 * threads_for(n, 4) > n + n / 8) return rms_rows<T, W, V, 2, 2, 2, 8, 2, QUANT>(a, s);
         if (n <= 512) return rms_rows<T, W, V, 4, 1, 3, 4, 4, QUANT>(a, s);
         if (n <= 1024) return rms_rows<T, W, V, 4, 1, 3, 8, 2, QUANT>(a, s);
         return rms_rows<T, W, V, 4, 1, 3, 16, 1, QUANT>(a, s);
     }
-    if (V4 > 1 && fits(V4) && c.H / V4 <= 4096) return rms_rows<T, W, V4, 8, 1, 3, 16, 1, QUANT>(a, s);
+    if (V4 > 1 && fits(V4) && c.H / V4 <= 4096) {
+        if (c.H / V4 <= 64) return rms_rows<T, W, V4, 2, 1, 3, 1, 12, QUANT>(a, s);
+        if (c.H / V4 <= 128) return rms_rows<T, W, V4, 4, 1, 3, 1, 12, QUANT>(a, s);
+        if (c.H / V4 <= 256) return rms_rows<T, W, V4, 8, 1, 3, 1, 12, QUANT>(a, s);
+        return rms_rows<T, W, V4, 8, 1, 3, 16, 1, QUANT>(a, s);
+    }
+    if (c.H <= 128) return rms_rows<T, W, 1, 4, 1, 3, 1, 12, QUANT>(a, s);
+    if (c.H <= 256) return rms_rows<T, W, 1, 8, 1, 3, 1, 12, QUANT>(a, s);
     if (c.H <= 4096) return rms_rows<T, W, 1, 8, 1, 3, 16, 1, QUANT>(a, s);
     if (c.H <= 8192) return rms_rows<T, W, 1, 16, 1, 3, 16, 1, QUANT>(a, s);
     LCE_PROFILED(launch_after(rms_fwd_any<T, QUANT>, dim3(static_cast<unsigned>(c.rows)), 512, 0, s, a));
@@ -653,9 +664,10 @@ lce_status_t rms_forward(const RmsCall& c) {
 
 // The backward's form by the row's width, as layer norm's (lce_norm.cuh): up to
 // 128 16-byte vectors a warp per row, up to 1024 a block with two vectors a
-// thread, up to 2048 with four, read twice from the ring; narrower vectors eight
-// a thread, a warp per row where that covers it (30000 x 250 bf16: 26 us, a
-// block per row 54), or sixteen single elements; wider rows are read again.
+// thread, up to 2048 with four, read twice from the ring; narrower vectors up to
+// eight a thread, a warp per row where that covers it (30000 x 250 bf16: 17.7 us
+// with four, 25.1 with eight, a block per row 54; 88770 x 82 25.5 with two, 55.5
+// with eight), or sixteen single elements; wider rows are read again.
 // Measured with the sum's gradient: 16384 x 1024 bf16 27 us (the copy rate
 // would be 20), 65536 x 2560 without it 155 us (148).
 template <typename T, typename W, int VEC, int ITEMS, bool WARP, bool KEEP, int LANES = 32>
@@ -695,13 +707,20 @@ lce_status_t rms_backward(const RmsCall& c) {
              : n <= 16   ? rms_bwd<T, W, V, 1, true, true, 16>(a, &parts, s)
              : n <= 32   ? rms_bwd<T, W, V, 1, true, true>(a, &parts, s)
              : n <= 64   ? rms_bwd<T, W, V, 2, true, true>(a, &parts, s)
+             : n <= 96   ? rms_bwd<T, W, V, 3, true, true>(a, &parts, s)
              : n <= 128  ? rms_bwd<T, W, V, 4, true, true>(a, &parts, s)
              : n <= 1024 ? rms_bwd<T, W, V, 2, false, true>(a, &parts, s)
                          : rms_bwd<T, W, V, 4, false, false>(a, &parts, s);
     } else if (V4 > 1 && fits(V4) && c.H / V4 <= 4096) {
-        st = c.H / V4 <= 256 ? rms_bwd<T, W, V4, 8, true, true>(a, &parts, s) : rms_bwd<T, W, V4, 8, false, true>(a, &parts, s);
+        const int n = c.H / V4;
+        st = n <= 64    ? rms_bwd<T, W, V4, 2, true, true>(a, &parts, s)
+             : n <= 128 ? rms_bwd<T, W, V4, 4, true, true>(a, &parts, s)
+             : n <= 256 ? rms_bwd<T, W, V4, 8, true, true>(a, &parts, s)
+                        : rms_bwd<T, W, V4, 8, false, true>(a, &parts, s);
     } else if (c.H <= 4096) {
-        st = c.H <= 256 ? rms_bwd<T, W, 1, 8, true, true>(a, &parts, s) : rms_bwd<T, W, 1, 8, false, true>(a, &parts, s);
+        st = c.H <= 128   ? rms_bwd<T, W, 1, 4, true, true>(a, &parts, s)
+             : c.H <= 256 ? rms_bwd<T, W, 1, 8, true, true>(a, &parts, s)
+                          : rms_bwd<T, W, 1, 8, false, true>(a, &parts, s);
     } else if (c.H <= 8192) {
         st = rms_bwd<T, W, 1, 16, false, true>(a, &parts, s);
     } else {

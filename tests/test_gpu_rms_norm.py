@@ -196,7 +196,9 @@ def test_no_rows():
 
 @pytest.mark.parametrize("rows", [1, 2, 3, 5, 31, 33, 1000, 40001])
 @pytest.mark.parametrize("H,dtype", [(8, "bf16"), (24, "bf16"), (64, "fp16"), (72, "bf16"), (128, "fp16"), (136, "bf16"), (32, "fp32"),
-                                     (48, "fp32"), (64, "fp32"), (68, "fp32")])
+                                     (48, "fp32"), (64, "fp32"), (68, "fp32"), (82, "bf16"), (87, "bf16"), (87, "fp32"), (130, "fp16"),
+                                     (201, "fp32"), (250, "bf16"), (255, "fp16"), (258, "bf16"), (500, "fp16"), (576, "bf16"),
+                                     (704, "fp16"), (776, "bf16")])
 def test_narrow_rows(rows, H, dtype):
     """Several rows to a warp: rows that end inside one, and rows beside one that is not finite."""
     from lm_head_linear_chunked_gb300.rms_norm import rms_norm_backward, rms_norm_forward, rms_norm_fp8
