@@ -11,6 +11,8 @@
 // All four passes go by tokens, so a token's row is read or written once and
 // its slots' rows are each touched once: they are bound by those bytes.  Sums
 // over slots and columns are FP32, in an order fixed by the sizes.
+#include <type_traits>
+
 #include "lce_sort.cuh"
 
 namespace lce {
@@ -422,9 +424,13 @@ lce_status_t move_as(MoveArgs a, Move what, cudaStream_t s) {
     const int64_t n = a.H / VEC, vectors = a.T * n;
     auto parts = [&](int u) { return (n + 32 * u - 1) / (32 * u); };
     // rows of less than half a warp of 16-byte vectors are dealt out by the vector (65536 tokens of 4 slots, 64 bf16:
-    // dispatch 10.3 us, combine 14.5; a warp to a token 16.5 and 40.6), the gradients by parts of a warp
-    const bool narrow = V16 && n <= 16, wide = !narrow && what == Move::SPREAD && a.T * parts(WIDE) >= 152 * 32;
-    const int lanes = !V16 || n > 16 ? 32 : n > 8 ? 16 : 8;
+    // dispatch 10.3 us, combine 14.5; a warp to a token 16.5 and 40.6), in combine of less than a warp (20000 tokens of 4
+    // slots, 192: 6.9 and 9.1), with one or two slots than two (60000 of one, 192: 9.0 and 15.2; 40000 of 2, 512: 27.3 and
+    // 25.8).  The gradients take parts of a warp, up to a warp's width with one or two slots (60000 of one, 192: 18.3 us,
+    // a warp 27.3; 20000 of 4, 192: 18.0 and 17.2)
+    const bool narrow = V16 && (n <= 16 || (what == Move::JOIN && (n < 32 || (n < 64 && a.k <= 2))));
+    const bool wide = !narrow && what == Move::SPREAD && a.T * parts(WIDE) >= 152 * 32, halves = n > 16 && n <= 32 && a.k <= 2;
+    const int lanes = !V16 || (n > 16 && !halves) ? 32 : n > 8 ? 16 : 8;
     int64_t work = 0;  // blocks
     if (what == Move::JOIN_BWD) {
         a.share = 1;
@@ -444,29 +450,47 @@ lce_status_t move_as(MoveArgs a, Move what, cudaStream_t s) {
     if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
     a.clearing = static_cast<int32_t>(clearing);
     const unsigned grid = static_cast<unsigned>(blocks);
+    // no more slots at a time than a token has (16384 tokens of one, 2048 bf16: combine 28.6 us, with eight 38.8, its
+    // gradients 35.6 and, with four, 41.9)
+    auto by_slots = [&](auto launch) -> lce_status_t {
+        if (a.k <= 2) return launch(std::integral_constant<int, 2>{});
+        if constexpr (BATCH > 4)
+            if (a.k > 4) return launch(std::integral_constant<int, BATCH>{});
+        return launch(std::integral_constant<int, 4>{});
+    };
     if (what == Move::JOIN_BWD) {
-        if constexpr (V16) {
-            if (lanes < 32) {
-                if (lanes == 16)
-                    LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, 4, 16>, dim3(grid), 256, 0, s, a));
-                else
-                    LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, 4, 8>, dim3(grid), 256, 0, s, a));
-                return LCE_OK;
+        return by_slots([&](auto batch) -> lce_status_t {
+            constexpr int B = decltype(batch)::value;
+            if constexpr (V16) {
+                constexpr int FEW = B < 4 ? B : 4;
+                if constexpr (B == 2)
+                    if (halves) {
+                        LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, 2, B, 16>, dim3(grid), 256, 0, s, a));
+                        return LCE_OK;
+                    }
+                if (lanes < 32) {
+                    if (lanes == 16)
+                        LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, FEW, 16>, dim3(grid), 256, 0, s, a));
+                    else
+                        LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, FEW, 8>, dim3(grid), 256, 0, s, a));
+                    return LCE_OK;
+                }
             }
-            if (a.k > 4) {
-                LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, BATCH, 32>, dim3(grid), 256, 0, s, a));
-                return LCE_OK;
-            }
-        }
-        LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, 4, 32>, dim3(grid), 256, 0, s, a));
+            LCE_PROFILED(launch_after(expert_join_bwd<T, VEC, BWD, B, 32>, dim3(grid), 256, 0, s, a));
+            return LCE_OK;
+        });
     } else if (what == Move::JOIN) {
-        if constexpr (V16) {
-            if (narrow) {
-                LCE_PROFILED(launch_after(expert_join_narrow<T, VEC, JOIN, BATCH>, dim3(grid), 256, 0, s, a));
-                return LCE_OK;
+        return by_slots([&](auto batch) -> lce_status_t {
+            constexpr int B = decltype(batch)::value;
+            if constexpr (V16) {
+                if (narrow) {
+                    LCE_PROFILED(launch_after(expert_join_narrow<T, VEC, JOIN, B>, dim3(grid), 256, 0, s, a));
+                    return LCE_OK;
+                }
             }
-        }
-        LCE_PROFILED(launch_after(expert_join<T, VEC, JOIN, BATCH>, dim3(grid), 256, 0, s, a));
+            LCE_PROFILED(launch_after(expert_join<T, VEC, JOIN, B>, dim3(grid), 256, 0, s, a));
+            return LCE_OK;
+        });
     } else {
         if constexpr (V16) {
             if (narrow) {
