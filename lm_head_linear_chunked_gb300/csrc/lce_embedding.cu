@@ -207,6 +207,8 @@ struct NextDigit {
 };
 
 constexpr int EMB_CHUNK = 32;       // sorted tokens of a warp
+constexpr int EMB_AHEAD = 8;        // rows on their way
+constexpr int EMB_ANY_WORDS = 132;  // of a row's slab on any boundary: 128 and the next
 
 template <typename T>
 struct EmbBwd {
@@ -245,6 +247,20 @@ __device__ __forceinline__ void emb_store(const F2 (&s)[VEC * ITEMS / 2], W* row
     }
 }
 
+// The same of a row on any boundary, element by element.
+template <typename W, int ITEMS>
+__device__ __forceinline__ void emb_store_any(const F2 (&s)[ITEMS], W* row, int k0, int H, float scale, bool add) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int c = 2 * (k0 + 32 * i) + e;
+            if (c >= H) break;
+            const float v = e ? hi(s[i]) : lo(s[i]);
+            row[c] = from_f32<W>(add ? fmaf(v, scale, to_f32(row[c])) : v * scale);
+        }
+}
+
 // The sums.  A warp takes 32 sorted tokens and a slab of columns, copies their
 // rows ahead to shared memory and adds them up until the token changes.  A run
 // of equal tokens that reaches into the next chunk belongs to the warp it starts in, as
@@ -252,13 +268,19 @@ __device__ __forceinline__ void emb_store(const F2 (&s)[VEC * ITEMS / 2], W* row
 // and their pieces go to `parts`: [chunk][0] of a run that comes from the chunk
 // before, [chunk][1] of one that starts here; so a token that fills half of the
 // batch is spread over as many warps as its rows need.
-template <typename T, typename W, int VEC, int ITEMS, int AHEAD>
+// ANY: rows of 16-bit elements on any boundary.  They are copied by the words
+// that they lie in, and a lane puts its two columns together from one word or
+// two neighbours.  A word that reaches past the first or the last row is read by
+// its half inside, as nothing says that what lies there may be read (40000 x 1601 bf16 into 32768 rows: 118 us, element by element 351).
+template <typename T, typename W, int VEC, int ITEMS, bool ANY>
 __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
     extern __shared__ __align__(16) uint8_t dyn[];
     using V = Vec<T, VEC>;
+    static_assert(!ANY || (VEC == 2 && sizeof(T) == 2));
     constexpr unsigned ALL = 0xFFFFFFFFu;
+    constexpr int AHEAD = EMB_AHEAD;
     const int lane = threadIdx.x & 31;
-    const int n = a.H / VEC;
+    const int n = a.H / VEC;  // (not with ANY)
     int64_t item = blockIdx.x * 8ll + (threadIdx.x >> 5);
     launch_dependents();
     wait_for_primary();
@@ -305,76 +327,116 @@ __global__ void __launch_bounds__(256) emb_sum(EmbBwd<T> a) {
     F2 s[PAIRS];
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
-    const V* from = reinterpret_cast<const V*>(a.dy + row * a.ldd) + k0;  // shifted back by the lane that holds the row
-    const V* from2 = reinterpret_cast<const V*>(a.dy + row2 * a.ldd) + k0;
+    const int shift = ANY ? 0 : k0;  // a row's address at this lane's columns: shifted back by the lane that holds the row
+    const uintptr_t from = reinterpret_cast<uintptr_t>(reinterpret_cast<const V*>(a.dy + row * a.ldd) + shift);
+    const uintptr_t from2 = reinterpret_cast<uintptr_t>(reinterpret_cast<const V*>(a.dy + row2 * a.ldd) + shift);
     auto row_at = [&](int i) {
-        const auto p = reinterpret_cast<unsigned long long>(i < 32 ? from : from2);
-        return reinterpret_cast<const V*>(__shfl_sync(ALL, p, i & 31)) + (lane - (i & 31));
+        const unsigned long long p = __shfl_sync(ALL, static_cast<unsigned long long>(i < 32 ? from : from2), i & 31);
+        return reinterpret_cast<const V*>(p) + (ANY ? 0 : lane - (i & 31));
     };
     auto finish = [&](int i) {  // of a run, or of its part in this chunk: i is its last row
         const int32_t v = i < 32 ? __shfl_sync(ALL, key, i) : tail;
         const bool is_head = v == head && head_long, is_tail = v == tail && tail_long;
         if (a.named && k0 == 0) a.named[v] = 1;
-        if (!is_head && !is_tail)
-            emb_store<W, VEC, ITEMS>(s, static_cast<W*>(a.dw) + v * a.lddw, k0, n, a.scale, a.add);
-        else
-            emb_store<float, VEC, ITEMS>(s, a.parts + (c * 2 + (is_head ? 0 : 1)) * a.H, k0, n, 1.f, false);
+        const bool whole_run = !is_head && !is_tail;
+        W* out = static_cast<W*>(a.dw) + v * a.lddw;
+        float* piece = a.parts + (c * 2 + (is_head ? 0 : 1)) * a.H;
+        if constexpr (ANY) {
+            if (whole_run)
+                emb_store_any<W, ITEMS>(s, out, k0, a.H, a.scale, a.add);
+            else
+                emb_store_any<float, ITEMS>(s, piece, k0, a.H, 1.f, false);
+        } else {
+            if (whole_run)
+                emb_store<W, VEC, ITEMS>(s, out, k0, n, a.scale, a.add);
+            else
+                emb_store<float, VEC, ITEMS>(s, piece, k0, n, 1.f, false);
+        }
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) s[p] = f2(0.f);
     };
-    if constexpr (AHEAD > 0) {
-        // rows on their way: [AHEAD][ITEMS][threads], each thread its own vectors
-        constexpr int SLOT = ITEMS * 256;
-        V* ring = reinterpret_cast<V*>(dyn) + threadIdx.x;
-        auto copy = [&](int i, int slot) {
-            if (i < end) {
-                const V* p = row_at(i);
-#pragma unroll
-                for (int k = 0; k < ITEMS; ++k)
-                    if (k0 + 32 * k < n) copy_async<sizeof(V)>(ring + slot + k * 256, p + 32 * k);
-            }
-            copy_async_commit();
-        };
-#pragma unroll
-        for (int k = 0; k < AHEAD - 1; ++k) copy(begin + k, k * SLOT);
-        int slot = 0;
+    auto sum_rows = [&](auto next_row) {
         for (int i = begin; i < end;) {
             const unsigned ends = i < 32 ? last >> i : 0u;
             const int stop = ends ? i + __ffs(ends) : end;
             for (; i < stop; ++i) {
-                copy(i + AHEAD - 1, (slot + (AHEAD - 1) * SLOT) & (AHEAD * SLOT - 1));
-                copy_async_wait<AHEAD - 1>();
-                RowVectors<T, VEC, ITEMS> x;
-#pragma unroll
-                for (int k = 0; k < ITEMS; ++k) x.v[k] = ring[slot + k * 256];
-                slot = (slot + SLOT) & (AHEAD * SLOT - 1);
+                const RowVectors<T, VEC, ITEMS> x = next_row(i);
 #pragma unroll
                 for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], x.pair(p));
             }
             finish(i - 1);
         }
-    } else {  // a few rows in registers
-        constexpr int BATCH = 16;
-        for (int i0 = begin; i0 < end; i0 += BATCH) {
-            RowVectors<T, VEC, ITEMS> x[BATCH];
+    };
+    int slot = 0;
+    if constexpr (!ANY) {
+        // rows on their way: [AHEAD][ITEMS][threads], each thread its own vectors
+        constexpr int SLOT = ITEMS * 256;
+        V* ring = reinterpret_cast<V*>(dyn) + threadIdx.x;
+        auto copy = [&](int i, int to) {
+            if (i < end) {
+                const V* p = row_at(i);
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b) {
-                const V* p = row_at(i0 + b);
-#pragma unroll
-                for (int k = 0; k < ITEMS; ++k) {
-                    x[b].v[k] = V{};
-                    if (i0 + b < end && k0 + 32 * k < n) load_now(x[b].v[k], p + 32 * k);
-                }
+                for (int k = 0; k < ITEMS; ++k)
+                    if (k0 + 32 * k < n) copy_async<sizeof(V)>(ring + to + k * 256, p + 32 * k);
             }
+            copy_async_commit();
+        };
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b) {
-                const int i = i0 + b;
-                if (i >= end) break;
+        for (int k = 0; k < AHEAD - 1; ++k) copy(begin + k, k * SLOT);
+        sum_rows([&](int i) {
+            copy(i + AHEAD - 1, (slot + (AHEAD - 1) * SLOT) & (AHEAD * SLOT - 1));
+            copy_async_wait<AHEAD - 1>();
+            RowVectors<T, VEC, ITEMS> x;
 #pragma unroll
-                for (int p = 0; p < PAIRS; ++p) s[p] = add2(s[p], x[b].pair(p));
-                if (i < 32 ? last >> i & 1 : i + 1 == end) finish(i);
+            for (int k = 0; k < ITEMS; ++k) x.v[k] = ring[slot + k * 256];
+            slot = (slot + SLOT) & (AHEAD * SLOT - 1);
+            return x;
+        });
+    } else {
+        // rows on their way: [warps][AHEAD][EMB_ANY_WORDS], a warp's words side by side
+        static_assert(32 * ITEMS + 1 <= EMB_ANY_WORDS);
+        uint32_t* ring = reinterpret_cast<uint32_t*>(dyn) + (threadIdx.x >> 5) * AHEAD * EMB_ANY_WORDS;
+        const unsigned odd = __ballot_sync(ALL, from & 2), odd2 = __ballot_sync(ALL, from2 & 2);  // rows that start in a word's middle
+        const uintptr_t first_row = reinterpret_cast<uintptr_t>(a.dy), last_row = reinterpret_cast<uintptr_t>(a.dy + (a.N - 1) * a.ldd);
+        const int bytes = 2 * a.H;
+        auto copy = [&](int i, int to) {
+            if (i < end) {
+                const uintptr_t p = reinterpret_cast<uintptr_t>(row_at(i));
+                const int words = static_cast<int>((p & 2) + bytes + 3) >> 2;
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(p & ~uintptr_t{3});
+                uint32_t* out = ring + to * EMB_ANY_WORDS - (k0 - lane);
+                const bool before = p == first_row && (p & 2), behind = p == last_row && ((p + bytes) & 2);  // words that reach outside
+                auto word = [&](int q) {
+                    if (before && q == 0)
+                        out[q] = static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(w + q)[1]) << 16;
+                    else if (behind && q == words - 1)
+                        out[q] = *reinterpret_cast<const uint16_t*>(w + q);
+                    else if (q < words)
+                        copy_async<4>(out + q, w + q);
+                };
+#pragma unroll
+                for (int k = 0; k < ITEMS; ++k) word(k0 + 32 * k);
+                if (lane == 0 && (p & 2)) word(k0 + 32 * ITEMS);
             }
-        }
+            copy_async_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < AHEAD - 1; ++k) copy(begin + k, k);
+        sum_rows([&](int i) {
+            copy_async_wait<AHEAD - 2>();
+            __syncwarp();  // all lanes' words of this row have come, and the row before has been read
+            copy(i + AHEAD - 1, (slot + AHEAD - 1) & (AHEAD - 1));
+            const uint32_t* w = ring + slot * EMB_ANY_WORDS + lane;
+            const unsigned by = (i < 32 ? odd >> i : odd2 >> (i - 32)) & 1 ? 0x5432 : 0x3210;
+            RowVectors<T, VEC, ITEMS> x;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                const uint32_t both = __byte_perm(w[32 * k], w[32 * k + 1], by);
+                __builtin_memcpy(&x.v[k], &both, 4);
+            }
+            slot = (slot + 1) & (AHEAD - 1);
+            return x;
+        });
     }
 }
 
@@ -698,20 +760,21 @@ lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
         LCE_PROFILED(launch_after(emb_sum_few<T, W, VEC, ITEMS>, dim3(static_cast<unsigned>(blocks)), 32 * EMB_FEW_WARPS, 0, s, a));
         return LCE_OK;
     }
-    constexpr int AHEAD = VEC * sizeof(T) >= 4 ? 8 : 0, ITEMS = AHEAD ? 8 / VEC : 2;
-    a.slabs = emb_slabs(a.H / VEC, ITEMS);
+    constexpr bool ANY = VEC * sizeof(T) < 4;
+    constexpr int SVEC = ANY ? 2 : VEC, ITEMS = 8 / SVEC;
+    a.slabs = emb_slabs(ANY ? (a.H + 1) / 2 : a.H / VEC, ITEMS);
     // a chunk's runs over four warps where there are few chunks (620 tokens of 128 bf16: 19.7 us, not 26.0; 90000: 52.1 and 63.2)
-    if (AHEAD && a.chunks * a.slabs < 152 * 32) a.split = 4;
+    if (a.chunks * a.slabs < 152 * 32) a.split = 4;
     const int64_t blocks = (a.chunks * a.slabs * a.split + 7) / 8;
     if (blocks == 0) return LCE_OK;  // no tokens: all rows have been cleared
     if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
-    constexpr size_t smem = static_cast<size_t>(AHEAD) * ITEMS * 256 * VEC * sizeof(T);
+    constexpr size_t smem = static_cast<size_t>(EMB_AHEAD) * (ANY ? 8 * EMB_ANY_WORDS * 4 : ITEMS * 256 * VEC * sizeof(T));
     static std::atomic<uint64_t> sums{0}, finishes{0};
     // 16-byte vectors of FP32 pieces where dw's rows have vectors at all, and few columns to a block: there are few long runs
     constexpr int JVEC = VEC % 4 == 0 ? 4 : VEC, JITEMS = JVEC == 4 ? 1 : 4 / JVEC;
     auto finish = emb_finish<W, JVEC, JITEMS, VEC>;
-    if (!allow_smem(&sums, emb_sum<T, W, VEC, ITEMS, AHEAD>, static_cast<int>(smem)) || !allow_smem(&finishes, finish, 0)) return LCE_ERR_CUDA;
-    LCE_PROFILED(launch_after(emb_sum<T, W, VEC, ITEMS, AHEAD>, dim3(static_cast<unsigned>(blocks)), 256, smem, s, a));
+    if (!allow_smem(&sums, emb_sum<T, W, SVEC, ITEMS, ANY>, static_cast<int>(smem)) || !allow_smem(&finishes, finish, 0)) return LCE_ERR_CUDA;
+    LCE_PROFILED(launch_after(emb_sum<T, W, SVEC, ITEMS, ANY>, dim3(static_cast<unsigned>(blocks)), 256, smem, s, a));
     EmbBwd<float> j{};
     j.V = a.V;
     j.scale = a.scale;

@@ -148,6 +148,26 @@ def test_few_tokens(N, H):
             check_grad(embedding_backward(dy, t, V, 0.5, -100, out=acc[:, :H]), dy, t, V, 0.5, -100)
 
 
+@pytest.mark.parametrize("H", [1, 2, 3, 63, 128, 129, 255, 256, 257, 258, 511, 1601])
+@pytest.mark.parametrize("start", [0, 1, 2, 3])
+def test_16_bit_rows_on_any_boundary(H, start):
+    """Gradients that start anywhere, side by side or apart, with NaN before, between and behind them."""
+    from lm_head_linear_chunked_gb300.embedding import embedding_backward
+    V = 90
+    for N, kind in ((300, "one"), (1000, "few"), (7001, "zipf")):
+        t = tokens_of(kind, N, V, 27)
+        for gap in (0, 1, 5):
+            for dtype in (torch.bfloat16, torch.float16):
+                flat = torch.full((start + N * (H + gap) + 8,), float("nan"), device="cuda", dtype=dtype)
+                dy = flat[start:start + N * (H + gap)].view(N, H + gap)[:, :H]
+                dy.copy_(normal((N, H), 28, dtype))
+                check_grad(embedding_backward(dy, t, V, 0.5, 3), dy, t, V, 0.5, 3)
+                acc = normal((V, H + 1), 29)
+                before = acc.clone()
+                check_grad(embedding_backward(dy, t, V, 0.5, 3, out=acc[:, 1:], accumulate=True), dy, t, V, 0.5, 3, before[:, 1:])
+                assert torch.equal(acc[:, 0], before[:, 0])
+
+
 def test_an_output_that_autograd_has_saved():
     """Written into, it is not what was saved: the backward that would read it says so."""
     from lm_head_linear_chunked_gb300.embedding import embedding_backward
