@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(SORT_THREADS) emb_rank(RankJob job) {
         if (t == 0 && blockIdx.x == 0) f.status(any);
         const int own = blockIdx.x * 32, i = own + lane;
         const int32_t key = i < n ? keys[i] : 0;
-        const int each = (n + 127) / 128 * 4, j0 = warp * each, end = (n + 3) / 4 * 4, j1 = j0 + each < end ? j0 + each : end;
+        const int each = (n + 4 * SORT_WARPS - 1) / (4 * SORT_WARPS) * 4, j0 = warp * each, end = (n + 3) / 4 * 4, j1 = j0 + each < end ? j0 + each : end;
         const int lo = own < j1 ? own : j1, hi = own + 32 < j1 ? own + 32 : j1;
         int32_t count = 0;
         int j = j0;

@@ -199,7 +199,7 @@ __device__ __forceinline__ void place_items(const F& f, const SortShape& s) {
         }
         __syncwarp();
     });
-    if constexpr (F::SEGMENTS) f.ends(warp_sum(sums[lane]));
+    if constexpr (F::SEGMENTS) f.ends(warp_sum(lane < SORT_WARPS ? sums[lane] : 0));
     if (s.bad && blockIdx.x == 0) {
         const int any = alone ? bad : __syncthreads_or(t < s.blocks && s.bad[t]);
         if (t == 0) f.status(any);
