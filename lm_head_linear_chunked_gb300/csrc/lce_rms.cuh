@@ -722,7 +722,7 @@ lce_status_t rms_backward(const RmsCall& c) {
              : c.H <= 256 ? rms_bwd<T, W, 1, 8, true, true>(a, &parts, s)
                           : rms_bwd<T, W, 1, 8, false, true>(a, &parts, s);
     } else if (c.H <= 8192) {
-        st = rms_bwd<T, W, 1, 16, false, true>(a, &parts, s);
+        st = rms_bwd<T, W, 1, 16, false, sizeof(T) == 2>(a, &parts, s);  // (a ring with ds would be 295 KB in fp32)
     } else {
         if (c.y) LCE_PROFILED(launch_after(rms_dx_any<T>, dim3(static_cast<unsigned>(c.rows)), 512, 0, s, a));
         if (c.dw) {

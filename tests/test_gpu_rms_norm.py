@@ -133,6 +133,22 @@ def test_strides_and_alignment(H):
     assert torch.equal(rms_norm(torch._neg_view(x4), None, None, EPS), rms_norm(-x4, None, None, EPS))
 
 
+@pytest.mark.parametrize("dtype,H", [("fp32", H) for H in (255, 4095, 4097, 6399, 6401, 8188, 8191, 8192)] +
+                         [(d, H) for d in ("bf16", "fp16") for H in (255, 510, 4095, 4097, 8190, 8191, 8192, 16376, 16384)])
+def test_every_form_at_its_widest(dtype, H):
+    """With a residual and the sum's gradient, which take the most shared memory."""
+    from lm_head_linear_chunked_gb300.rms_norm import rms_norm_backward, rms_norm_forward, rms_norm_fp8
+    for rows, wtype in ((3, dtype), (700, "fp32")):
+        x, res, w, dy, ds = inputs(rows, H, dtype, wtype, 50)
+        f = rms_norm_forward(x, w, res, EPS)
+        ref, _ = rms_ref(f["sum"], w, EPS)
+        assert torch.equal(f["sum"], x + res)
+        assert_within(f["y"], ref, rms_tolerance(ref, H, x.dtype), "y")
+        check_backward(dy, f["sum"], w, f["rstd"], ds, rms_norm_backward(dy, f["sum"], w, f["rstd"], ds), w.dtype)
+        check_backward(dy, f["sum"], w, f["rstd"], None, rms_norm_backward(dy, f["sum"], w, f["rstd"]), w.dtype)
+        assert torch.equal(rms_norm_fp8(x, w, res, EPS)["sum"], f["sum"])
+
+
 def test_negated_views():
     """Memory that stands for other values, in every place that takes a tensor."""
     from lm_head_linear_chunked_gb300.rms_norm import rms_norm_backward, rms_norm_forward, rms_norm_fp8
