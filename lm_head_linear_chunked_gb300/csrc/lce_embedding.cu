@@ -658,16 +658,19 @@ size_t emb_space(int64_t N, int64_t V, int64_t H, EmbSpace* e, void* ws) {
 }
 
 // Whether all of the gradient's rows are cleared while the tokens are sorted, on
-// the SMs that the sort leaves idle: where the tokens are so few that they name
-// few rows, and where what the sort hides is more than the few blocks beside
-// it lose against many short ones.  Else the rows that no token names are
-// cleared at the end.  Early and late: 16384 tokens, 151936 rows of 1024 bf16
-// 72.2 and 78.5 us; 64 and 32768 of 1024 18.6 and 26.8; 4096 and 151936 of 2048
-// 111 and 115, of 4096 212 and 198.
-constexpr int64_t EMB_CLEAR_RATIO = 4;  // vocabulary rows to a token
-constexpr int64_t EMB_CLEAR_BYTES = 512ll << 20;
+// the SMs that the sort leaves idle, although some are written again: where the
+// sort by digits has few blocks and more rows than tokens lie behind it, or where
+// the clearing behind the one kernel that ranks few tokens is short.  Else the rows
+// that no token names are cleared at the end, by many short blocks.  Early and
+// late: 16384 tokens, 151936 rows of 1024 bf16 70.5 and 75.4 us; 31070 and 50257
+// of 1472 63.7 and 74.4; 40183 and 5534 of 2176 80.2 and 76.9; 131072 and 151936
+// of 1024 175 and 155; and ranked 4000 and 8000 of 1024 16.7 and 22.2, 3000 and
+// 8000 of 4096 27.1 and 26.4, 4096 and 151936 of 1024 61.7 and 56.4.
+constexpr int64_t EMB_CLEAR_TOKENS = 65536;
+constexpr int64_t EMB_CLEAR_BYTES = 512ll << 20, EMB_CLEAR_BYTES_RANKED = 32ll << 20;
 bool emb_early(int64_t N, int64_t V, int64_t bytes) {
-    return sort_blocks(N) <= SORT_BLOCKS / 2 && N <= V / EMB_CLEAR_RATIO && bytes <= EMB_CLEAR_BYTES;
+    if (N <= EMB_RANK) return bytes <= EMB_CLEAR_BYTES_RANKED;
+    return N <= EMB_CLEAR_TOKENS && N <= V && bytes <= EMB_CLEAR_BYTES;
 }
 
 // The sorted tokens: their place in e.keys and e.rows.
@@ -763,7 +766,8 @@ lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
     constexpr bool ANY = VEC * sizeof(T) < 4;
     constexpr int SVEC = ANY ? 2 : VEC, ITEMS = 8 / SVEC;
     a.slabs = emb_slabs(ANY ? (a.H + 1) / 2 : a.H / VEC, ITEMS);
-    // a chunk's runs over four warps where there are few chunks (620 tokens of 128 bf16: 19.7 us, not 26.0; 90000: 52.1 and 63.2)
+    // a chunk's runs over four warps where there are few chunks (620 tokens of 128 bf16: 12.0 us, not 18.4; 90000 of 64: 51.2
+    // and 65.4)
     if (a.chunks * a.slabs < 152 * 32) a.split = 4;
     const int64_t blocks = (a.chunks * a.slabs * a.split + 7) / 8;
     if (blocks == 0) return LCE_OK;  // no tokens: all rows have been cleared
