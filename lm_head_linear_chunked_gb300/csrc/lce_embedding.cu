@@ -669,6 +669,7 @@ size_t emb_space(int64_t N, int64_t V, int64_t H, EmbSpace* e, void* ws) {
 constexpr int64_t EMB_CLEAR_TOKENS = 65536;
 constexpr int64_t EMB_CLEAR_BYTES = 512ll << 20, EMB_CLEAR_BYTES_RANKED = 32ll << 20;
 bool emb_early(int64_t N, int64_t V, int64_t bytes) {
+    if (N == 0) return true;  // no kernel comes after the one that ranks
     if (N <= EMB_RANK) return bytes <= EMB_CLEAR_BYTES_RANKED;
     return N <= EMB_CLEAR_TOKENS && N <= V && bytes <= EMB_CLEAR_BYTES;
 }
@@ -770,7 +771,7 @@ lce_status_t emb_sums(EmbBwd<T> a, cudaStream_t s) {
     // and 65.4)
     if (a.chunks * a.slabs < 152 * 32) a.split = 4;
     const int64_t blocks = (a.chunks * a.slabs * a.split + 7) / 8;
-    if (blocks == 0) return LCE_OK;  // no tokens: all rows have been cleared
+    if (blocks == 0) return LCE_OK;  // no tokens: all rows have been cleared (emb_early), or the sums stay as they are
     if (blocks > INT32_MAX) return LCE_ERR_UNSUPPORTED;
     constexpr size_t smem = static_cast<size_t>(EMB_AHEAD) * (ANY ? 8 * EMB_ANY_WORDS * 4 : ITEMS * 256 * VEC * sizeof(T));
     static std::atomic<uint64_t> sums{0}, finishes{0};

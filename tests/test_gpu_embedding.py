@@ -209,3 +209,27 @@ def test_autograd_and_tied_weights():
     both = out["grad_W_acc"].double()
     parts = head.abs().double() + embedding_grad_ref(c, t, V, 2.0, 9)[0].abs()
     assert_within(m.weight.grad, both, 3 * half_step(torch.bfloat16) * parts + 1e-6, "tied gradient")  # three roundings to bf16
+
+
+def check_named(got, dy, tokens, V, scale):
+    """As check_grad, over the rows that tokens name alone; the others have to be zero (got is cleared)."""
+    tokens = tokens.reshape(-1)
+    inside = (tokens >= 0) & (tokens < V)
+    named, at = tokens[inside].unique(return_inverse=True)
+    check_grad(got[named], dy[inside], at, named.numel(), scale)
+    got[named] = 0
+    assert not got.any()
+
+
+@pytest.mark.parametrize("N", [0, 1, 33])
+@pytest.mark.parametrize("H,dtype", [(4096, "bf16"), (1024, "fp32")])
+@pytest.mark.parametrize("gap", [0, 3])
+def test_few_tokens_into_a_large_gradient(N, H, dtype, gap):
+    """Every row is written, above the half gigabyte that is cleared beside the sort as below it."""
+    from lm_head_linear_chunked_gb300.embedding import embedding_backward
+    V = 151936
+    room = torch.full((V, H + gap), float("nan"), device="cuda", dtype=DTYPES[dtype])
+    t, dy = tokens_of("few", N, V, 31), normal((N, H), 32, DTYPES[dtype])
+    got = embedding_backward(dy, t, V, 0.5, out=room[:, :H])
+    check_named(got, dy, t, V, 0.5)
+    assert bool(room[:, H:].isnan().all())
