@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
         }
         if (mine_in && lead) {
             const int64_t slot = t * a.k + j0 + lane;
+            if (row < 0) mine = 0.f;  // not 0 dy: dy may be infinite or NaN
             if (a.w32)
                 static_cast<float*>(a.weights_out)[slot] = mine;
             else

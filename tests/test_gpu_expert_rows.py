@@ -174,3 +174,33 @@ def test_autograd():
     for g, r, terms in zip(got, want, (H * k, 2 * T, H)):
         assert (g.double() - r).abs().max() <= 4 * terms * U32 * r.abs().max() * 8  # products and sums of `terms` in FP32
     assert not dispatch(x.detach(), plan).requires_grad
+
+
+@pytest.mark.parametrize("H", [8, 65, 66, 128, 256, 264, 1601, 8200])
+@pytest.mark.parametrize("k", [1, 2, 3, 8, 11])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_unused_slots_beside_a_gradient_that_is_not_finite(H, k, dtype):
+    """A slot without a row has the weight's gradient 0, whatever dy and the token's other slots hold."""
+    from lm_head_linear_chunked_gb300.expert_rows import combine_backward, expert_plan
+    T, E = 30, 16
+    t, j = torch.arange(T, device="cuda")[:, None], torch.arange(k, device="cuda")
+    experts = torch.where((t + j * j) % 3 == 0, -1, (t + j) % E)
+    mask = t[:, 0] % 7 != 5
+    plan = expert_plan(experts, E, mask, 4)
+    dy, rows = normal((T, H), 70, DTYPES[dtype]), normal((plan["slots"].shape[0], H), 71, DTYPES[dtype])
+    for i, v in enumerate((float("inf"), float("-inf"), float("nan"))):
+        dy[i::5, (7 * i) % H] = v
+    rows[plan["slots"] < 0] = float("nan")
+    p = plan["positions"].long()
+    has = p >= 0
+    assert torch.equal(has, (experts >= 0) & mask[:, None])
+    each = rows[p.clamp(min=0)].double() * dy.double()[:, None]
+    ref = torch.where(has, each.sum(2), 0.0)
+    for wtype in (torch.float32, DTYPES[dtype]):
+        got = combine_backward(dy, rows, normal((T, k), 72, wtype), plan)
+        assert not got["grad_weights"][~has].any()
+        assert torch.equal(got["grad_weights"].isnan(), ref.isnan()) and torch.equal(got["grad_weights"].isinf(), ref.isinf())
+        finite = has & ref.isfinite()
+        tol = each.abs().sum(2)[finite] * (sum_depth(H) + H / 32 + 4) * U32 + ref[finite].abs() * half_step(wtype) + tiny(wtype)
+        assert_within(got["grad_weights"][finite], ref[finite], tol, "grad_weights")
+        assert not got["grad_rows"][plan["slots"] < 0].any()
