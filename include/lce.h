@@ -371,9 +371,10 @@ LCE_API lce_status_t lce_layer_norm_backward(int64_t rows, int64_t H, int dtype,
  * lce_rms_norm_fp8 gives the output in 8 bits: for each row's groups of
  * `group` columns (0: the whole row, or LCE_FP8_GROUP; the last may be
  * shorter), with y not rounded in between,
- *   scale = max(max |y|, 2^-100) / 448,  q = e4m3(y / scale),
- * scales [rows, ceil(H / group)] float, contiguous.  A group that holds a NaN
- * has a NaN scale.
+ *   scale = max(max |y|, 2^-100) / 448,  q = e4m3(y (1 / scale)),
+ * scales [rows, ceil(H / group)] float, contiguous; scale, its reciprocal and
+ * the product are each rounded to FP32.  A group that holds a NaN has a NaN
+ * scale.
  * Sums are FP32 and in an order fixed by the sizes, types, strides, the
  * alignment of the pointers and the device, so calls equal in these give equal
  * bits.  A row whose sum of squares passes FP32's range has rstd 0.
@@ -382,7 +383,9 @@ LCE_API lce_status_t lce_layer_norm_backward(int64_t rows, int64_t H, int dtype,
  *    LCE_ERR_UNSUPPORTED).  weight may be NULL (1).
  *  - Rows are contiguous, each matrix with its own stride in elements (>= H).
  *    Pointers need only the alignment of their element type; rows that start
- *    on 16-byte boundaries (q: H a multiple of 16) are read in vectors.
+ *    on 16-byte boundaries are read in vectors of 16 bytes (where rows of q start
+ *    on multiples of 8 bytes, 4 with FP32 inputs), 16-bit ones on 4-byte
+ *    boundaries in vectors of 4 (q: of 2).
  *  - sum (s) is written where a residual is given: both or neither.  rstd
  *    [rows] (may be NULL) is written by the forward and read by the backward,
  *    whose x is s.

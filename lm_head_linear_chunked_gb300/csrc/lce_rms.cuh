@@ -4,12 +4,16 @@
 //   s = x + r, rounded to the rows' type;  rstd = 1 / sqrt(sum_h s^2 / H + eps)
 //   y = s rstd w
 //   8 bits: a = max |y| of a group of columns, scale = max(a, 2^-100) / 448,
-//     q = e4m3(y / scale)
+//     q = e4m3(y (1 / scale))
 //   xh = s rstd,  g = dy w,  dx = rstd (g - xh mean_h(g xh)) + ds
 //   dw = sum_r dy xh
 //
 // The sum is rounded before it is normed: the rounded one is what the next
 // block adds to and what the backward reads, so all three see the same s.
+// y is multiplied by the scale's rounded reciprocal, not divided: two roundings
+// of 2^-24 before the one to 8 bits (2^-4), so another value only where y / scale
+// lies that close to the middle of two (32768 x 4096 bf16 to 8 bits 153 us, with
+// a division for each element 193).
 // All sums are FP32.
 #pragma once
 

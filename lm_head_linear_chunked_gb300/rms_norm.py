@@ -45,7 +45,7 @@ def rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residua
                  eps: float = 1e-6, group: int = FP8_GROUP) -> dict:
     """{"q", "scales", "sum"}: the output as float8_e4m3fn q (x's shape) and float32 scales [..., groups], y being about
     q * scale: one scale for every `group` = 128 columns (the last group may be shorter), or with group=0 one for the
-    row.  Not differentiable."""
+    row.  A scale is the largest magnitude / 448, q the rounded y * (1 / scale).  Not differentiable."""
     q, scales, total = native().rms_fp8(x, weight, residual, eps, group)
     return {"q": q, "scales": scales, "sum": x if total is None else total}
 

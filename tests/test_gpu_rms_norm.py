@@ -240,3 +240,33 @@ def test_narrow_rows(rows, H, dtype):
     part = rms_norm_backward(dy[fine], f["sum"][fine], w, f["rstd"][fine])["grad_weight"]
     each = (dy.double() * f["sum"].double() * f["rstd"].double()[:, None]).abs().sum(0)
     assert_within(zero, part.double(), each * 2 * (rows + 4) * U32 + 3 * half_step(w.dtype) * part.double().abs() + 3 * tiny(w.dtype), "sums")
+
+
+@pytest.mark.parametrize("H", [64, 96, 250, 1024, 1601, 4096, 8192, 16384, 16400, 40001])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("group", [0, 128])
+def test_8_bit_values_bit_by_bit(H, dtype, group):
+    """q is rounded from y times the rounded reciprocal of the scale.  Even widths have a weight whose
+    quotients by the scale lie between two values of e4m3; where rstd = 1 dividing would round some the other way."""
+    from lm_head_linear_chunked_gb300.rms_norm import rms_norm_forward, rms_norm_fp8
+    t, rows = DTYPES[dtype], 5
+    m = torch.arange(H, device="cuda") % 128 % 120
+    between = ((8 + m % 8).float() * 2 + 1) / 16 * 2.0 ** (m // 8 - 7).float()
+    between[torch.arange(H, device="cuda") % 128 == min(H, 128) - 1] = 448
+    c = torch.randint(1 << 15, 1 << 16, (-(-H // 128),), generator=torch.Generator().manual_seed(6)).cuda() * 2.0 ** -15
+    w = between * c.repeat_interleave(128)[:H]
+    x = torch.where(normal((rows, H), 30) > 0, 1.0, -1.0).to(t)
+    if H % 2:
+        x, w = normal((rows, H), 31, t), normal((H,), 32)
+    rstd = rms_norm_forward(x, w, None, 0.0)["rstd"].cpu()
+    assert H & (H - 1) or bool((rstd == 1).all())
+    got = rms_norm_fp8(x, w, None, 0.0, group)
+    y = x.float().cpu() * rstd[:, None] * w.cpu()
+    width = group or H
+    wide = torch.nn.functional.pad(y, (0, -H % width)).view(rows, -1, width)
+    scales = wide.abs().amax(2) / 448
+    assert torch.equal(got["scales"].cpu(), scales)
+    q = (wide * (1 / scales)[:, :, None]).view(rows, -1)[:, :H].to(torch.float8_e4m3fn)
+    assert torch.equal(got["q"].cpu().view(torch.uint8), q.view(torch.uint8))
+    if group and H & (H - 1) == 0 and H >= 1024:
+        assert not torch.equal((wide / scales[:, :, None]).view(rows, -1)[:, :H].to(torch.float8_e4m3fn).view(torch.uint8), q.view(torch.uint8))
