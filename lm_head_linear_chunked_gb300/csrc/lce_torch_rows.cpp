@@ -182,14 +182,24 @@ Tensor embedding_forward(const Tensor& tokens_in, const Tensor& weight, double s
     return y;
 }
 
-// out [n, H], rows apart by its stride, must not reach into the memory that `in` may lie in.
+// out [n, H], rows apart by its stride, must not reach into the memory that `in` may lie in, unless the rows of both are
+// other columns of one buffer.
 void apart(const Tensor& out, int64_t n, int64_t H, const Tensor& in, const char* what) {
     if (!out.has_storage() || !in.has_storage() || !out.numel() || !in.numel()) return;
     const auto first = reinterpret_cast<uintptr_t>(out.const_data_ptr()), from = reinterpret_cast<uintptr_t>(in.const_data_ptr());
+    const int64_t es = static_cast<int64_t>(in.element_size());
+    if (n > 1) {
+        const int64_t step = out.stride(0) * static_cast<int64_t>(out.element_size());
+        int64_t column = static_cast<int64_t>(from - first) % step;
+        if (column < 0) column += step;
+        bool rows = in.size(-1) == 1 || in.stride(-1) == 1;
+        for (int64_t d = 0; d + 1 < in.dim(); ++d) rows &= in.size(d) == 1 || in.stride(d) * es % step == 0;
+        if (rows && column >= H * static_cast<int64_t>(out.element_size()) && column + in.size(-1) * es <= step) return;
+    }
     int64_t last = 0;
     for (int64_t d = 0; d < in.dim(); ++d) last += (in.size(d) - 1) * in.stride(d);
     const uintptr_t end = first + ((n > 1 ? (n - 1) * out.stride(0) : 0) + H) * out.element_size();
-    if (first < from + (last + 1) * in.element_size() && from < end) throw py::value_error(std::string("out and ") + what + " overlap");
+    if (first < from + (last + 1) * es && from < end) throw py::value_error(std::string("out and ") + what + " overlap");
 }
 
 // grad_weight and the workspace

@@ -107,6 +107,28 @@ def test_an_output_that_overlaps_the_gradient():
             embedding_backward(ONE[a:a + b], T[:b], 10, out=ONE[4:14])
 
 
+SIDE = torch.zeros(20, 40)
+BITS = SIDE.view(torch.bfloat16)
+
+
+@pytest.mark.parametrize("dy,out,overlap", [
+    (SIDE[2:6, 16:32], SIDE[:10, :16], False),             # other columns of one buffer
+    (SIDE[2:6, 24:40], SIDE[5:15, 8:24], False),
+    (SIDE[6:10, :16], SIDE[:10, 16:32], False),
+    (SIDE[6:10, :16], SIDE[:10, 15:31], True),
+    (SIDE[2:6, 15:31], SIDE[:10, :16], True),
+    (SIDE[::2][:4, 24:40], SIDE[:10, 8:24], False),        # every other row
+    (SIDE[2:3, 16:32].expand(4, 16), SIDE[:10, :16], False),
+    (SIDE.reshape(-1)[30:190].view(4, 40)[:, :16], SIDE[:10, :16], True),    # reaches into the next row's first columns
+    (SIDE.reshape(-1)[:288].view(8, 36)[:4, 16:32], SIDE[:10, :16], True),   # rows of another length
+    (BITS[2:6, 32:48], SIDE[:10, :16], False),             # 16-bit rows beside float32 ones
+    (BITS[2:6, 31:47], SIDE[:10, :16], True),
+])
+def test_an_output_beside_the_gradient(dy, out, overlap):
+    with pytest.raises(ValueError, match="overlap" if overlap else "CUDA"):
+        embedding_backward(dy, T, 10, out=out)
+
+
 def test_module_parameters():
     m = Embedding(6, 4, padding_idx=2, dtype=torch.bfloat16)
     assert m.weight.shape == (6, 4) and m.weight.dtype == torch.bfloat16 and not m.weight[2].any()

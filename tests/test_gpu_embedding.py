@@ -233,3 +233,15 @@ def test_few_tokens_into_a_large_gradient(N, H, dtype, gap):
     got = embedding_backward(dy, t, V, 0.5, out=room[:, :H])
     check_named(got, dy, t, V, 0.5)
     assert bool(room[:, H:].isnan().all())
+
+
+@pytest.mark.parametrize("N,V,H", [(50, 300, 64), (3000, 5000, 65), (9000, 9001, 33)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_an_output_beside_the_gradient(N, V, H, dtype):
+    """Both are columns of one buffer; neither reaches into the other."""
+    from lm_head_linear_chunked_gb300.embedding import embedding_backward
+    both = normal((V, 2 * H + 1), 33, DTYPES[dtype])
+    before, t = both.clone(), tokens_of("few", N, V, 34)
+    got = embedding_backward(both[:N, H:2 * H], t, V, 0.5, out=both[:, :H])
+    check_grad(got, before[:N, H:2 * H], t, V, 0.5)
+    assert torch.equal(both[:, H:], before[:, H:])
