@@ -14,10 +14,10 @@
 //     ends(end), one past the last segment, called by all threads of all blocks
 //   void status(int any)   with shape.bad: whether an item was bad, once
 //   void beside(int kernel, int64_t block, int64_t of)   called by all threads
-//     of the shape's `extra` blocks of each kernel (the first is 0): work that
-//     needs nothing sorted, for the SMs that so few items leave idle.  The next
-//     kernel is launched when they have ended: earlier, its blocks would crowd
-//     onto the first SMs that are free
+//     of the shape's `extra` blocks of each kernel (counting 0, placing 1): work
+//     that needs nothing sorted, for the SMs that so few items leave idle; only
+//     where both kernels run.  The next kernel is launched when they have ended:
+//     earlier, its blocks would crowd onto the first SMs that are free
 #pragma once
 
 #include <atomic>
@@ -210,7 +210,7 @@ template <typename F>
 __global__ void __launch_bounds__(SORT_THREADS) sort_place(SortJob<F> job) {
     if (static_cast<int>(blockIdx.x) >= job.shape.blocks) {
         wait_for_primary();
-        return job.f.beside(job.shape.blocks > 1, blockIdx.x - job.shape.blocks, job.shape.extra);
+        return job.f.beside(1, blockIdx.x - job.shape.blocks, job.shape.extra);
     }
     launch_dependents();
     place_items(job.f, job.shape);

@@ -175,10 +175,10 @@ __device__ __forceinline__ void load_now(Vec<T, VEC>& v, const Vec<T, VEC>* p) {
     }
 }
 
-// Rows of n vectors, one after the other, dealt out to blocks of 256 threads
+// Rows of n < 256 vectors, one after the other, dealt out to blocks of 256 threads
 // with U vectors a thread, 256 apart: narrow rows leave no thread idle.
 struct Deal {
-    uint32_t n, magic;  // magic: 2^32 / n + 1, for rows shorter than a block's share
+    uint32_t n, magic;  // magic: 2^32 / n + 1
 };
 inline Deal deal_of(int64_t n) { return {static_cast<uint32_t>(n), static_cast<uint32_t>((1ull << 32) / n + 1)}; }
 template <int U>
@@ -190,10 +190,10 @@ struct Dealt {
         row0 = static_cast<int64_t>(first / d.n);
         at0 = static_cast<uint32_t>(first - static_cast<uint64_t>(row0) * d.n) + threadIdx.x;
     }
-    // The row of this thread's vector u, and the vector's place in it.  g is below n + 256 U, so with n < 256 U the
-    // product g n stays below 2^32 and the rounded-up reciprocal gives the exact quotient.
+    // The row of this thread's vector u, and the vector's place in it.  g is below n + 256 U, so the product g n stays
+    // below 2^32 and the rounded-up reciprocal gives the exact quotient.
     __device__ __forceinline__ int64_t get(const Deal& d, int u, uint32_t* at) const {
-        const uint32_t g = at0 + 256 * u, q = d.n >= 256 * U ? (g >= d.n ? 1u : 0u) : d.n == 1 ? g : __umulhi(g, d.magic);
+        const uint32_t g = at0 + 256 * u, q = d.n == 1 ? g : __umulhi(g, d.magic);
         *at = g - q * d.n;
         return row0 + q;
     }
