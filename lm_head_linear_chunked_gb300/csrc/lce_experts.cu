@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
         float mine = 0.f;  // lane b: the batch's slot b
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
-            float v = lo(dot[b]) + hi(dot[b]);
+            float v = from[b] ? lo(dot[b]) + hi(dot[b]) : 0.f;  // without a row not 0 dy: dy may be infinite or NaN
 #pragma unroll
             for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
             if (lane == b) mine = v;
@@ -339,7 +339,6 @@ __global__ void __launch_bounds__(256) expert_join_bwd(MoveArgs a) {
         }
         if (mine_in && lead) {
             const int64_t slot = t * a.k + j0 + lane;
-            if (row < 0) mine = 0.f;  // not 0 dy: dy may be infinite or NaN
             if (a.w32)
                 static_cast<float*>(a.weights_out)[slot] = mine;
             else
