@@ -416,8 +416,8 @@ template <typename T, int VEC>
 lce_status_t move_as(MoveArgs a, Move what, cudaStream_t s) {
     // (16384 tokens of 8 slots, 2048 bf16: combine with two vectors and eight slots at a time 4% faster than with one and
     // eight or four and four; single elements with four slots, not eight: 4099 x 1601 fp16 in training 95 us, not 138;
-    // their gradients with four elements a lane 23 us, with two 28, with eight 26.  Rows on any boundary put together from
-    // two aligned vectors: dispatch 15 us, not 12, combine 32, not 14)
+    // their gradients with four elements a lane 23 us, with two 28, with eight 26.  Rows on any boundary put together in
+    // registers from two aligned vectors: dispatch 15 us, not 12, combine 32, not 14)
     constexpr bool V16 = VEC * sizeof(T) == 16;
     constexpr int NARROW = VEC == 1 ? 8 : V16 ? 1 : 4, WIDE = V16 ? 4 : NARROW, BWD = VEC == 1 ? 4 : V16 ? 1 : 2, JOIN = V16 ? 2 : NARROW;
     constexpr int BATCH = V16 ? 8 : 4;
